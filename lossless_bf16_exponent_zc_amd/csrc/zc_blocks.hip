@@ -1,0 +1,272 @@
+// zc_blocks.hip -- casts to 8-bit blocks of 128 with power-of-two scales.
+//
+//   s = least power of two with max|x| <= 448 s,   q = E4M3(x / s)
+//
+// Division by a power of two is exact, so each value is rounded once and the
+// result does not depend on how a block is split over lanes.
+#include "zc_experts_kernels.h"
+
+namespace zc {
+
+namespace {
+
+constexpr uint32_t kWaveCols = 1024;  // columns of one wave: 16 per lane, 8 blocks
+
+template <typename T>
+struct Pack16 {
+    union {
+        xu32x4 w[sizeof(T)];  // 16 values
+        T v[16];
+    };
+};
+
+// Blocks of 1 x 128.  A wave casts 1024 columns of one token, 16 per lane, so
+// a block is 8 lanes and its bytes leave in one 16-byte store per lane; the
+// stores go to every row of the token.  Rows whose start is not a multiple of
+// 16 bytes, and a last piece of fewer than 16 values, are read one element
+// per lane (consecutive lanes, consecutive addresses) and turned over in LDS.
+template <typename T>
+__global__ __launch_bounds__(256) void cast_rows(CastRowsArgs a, uint32_t pieces, uint32_t token_blocks) {
+    __shared__ __align__(16) T turn[4][kWaveCols];
+    const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x >> 6);
+    if (blockIdx.x >= token_blocks) {  // padding rows of one expert
+        const uint32_t e = blockIdx.x - token_blocks;
+        const uint32_t lo = (uint32_t)a.offsets[e] + (uint32_t)a.counts[e];
+        uint32_t hi = (uint32_t)a.offsets[e + 1];
+        hi = hi < a.capacity ? hi : a.capacity;
+        for (uint32_t r = lo + wave; r < hi; r += 4) {
+            for (uint32_t c = lane * 16; c < a.data_stride; c += 1024)
+                *reinterpret_cast<xu32x4*>(a.data + (uint64_t)r * a.data_stride + c) = xu32x4{};
+            for (uint32_t c = lane * 4; c < a.scale_stride; c += 256)
+                *reinterpret_cast<uint32_t*>(a.scale + (uint64_t)r * a.scale_stride + c) = 0x7F7F7F7Fu;
+        }
+        return;
+    }
+    const uint64_t item = (uint64_t)blockIdx.x * 4 + wave;
+    const uint32_t t = (uint32_t)(item / pieces), piece = (uint32_t)(item % pieces);
+    uint32_t tokens = a.tokens;
+    if (a.used) {
+        const int32_t u = *a.used;
+        tokens = u < 0 ? 0 : (uint32_t)u < tokens ? (uint32_t)u : tokens;
+    }
+    if (t >= tokens) return;
+    const uint32_t c0 = piece * kWaveCols, c = c0 + lane * 16;
+    const T* x = static_cast<const T*>(a.x) + (uint64_t)t * a.x_stride;
+    Pack16<T> p;
+    if (a.wide && c0 + kWaveCols <= a.width) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T); ++i) p.w[i] = reinterpret_cast<const xu32x4*>(x + c)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t j = i * 64 + lane;
+            turn[wave][j] = c0 + j < a.width ? x[c0 + j] : (T)0.0f;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T); ++i) p.w[i] = reinterpret_cast<const xu32x4*>(&turn[wave][lane * 16])[i];
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, finite_bits(to_float(p.v[i])));
+#pragma unroll
+    for (int m = 1; m < 8; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+    const uint32_t b = scale_byte(top);
+    const float inv = inverse_scale(b);
+    xu32x4 q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        q[i] = four_fp8(scaled(to_float(p.v[4 * i]), inv), scaled(to_float(p.v[4 * i + 1]), inv),
+                        scaled(to_float(p.v[4 * i + 2]), inv), scaled(to_float(p.v[4 * i + 3]), inv));
+    // four blocks' bytes per word, in lanes 0 and 32; blocks past the last
+    // are all zeros and so get scale 1
+    uint32_t s = b << (8 * ((lane >> 3) & 3));
+    s |= (uint32_t)__shfl_xor((int)s, 8);
+    s |= (uint32_t)__shfl_xor((int)s, 16);
+    const uint32_t sc = piece * 8 + (lane >> 5) * 4;
+    const bool has_scale = (lane & 31) == 0 && sc < a.scale_stride;
+    auto store = [&](uint64_t r) {
+        if (c < a.data_stride) *reinterpret_cast<xu32x4*>(a.data + r * a.data_stride + c) = q;
+        if (has_scale) *reinterpret_cast<uint32_t*>(a.scale + r * a.scale_stride + sc) = s;
+    };
+    if (!a.row) {
+        store(t);
+        return;
+    }
+    for (uint32_t k = 0; k < a.topk; ++k) {
+        const uint32_t r = (uint32_t)a.row[(uint64_t)t * a.topk + k];
+        if (r < a.capacity) store(r);
+    }
+}
+
+enum CastMode { kWeights, kWeightsTransposed, kColumns };
+
+// One 128 x 128 tile of x per workgroup; a thread has 8 rows by 8 columns, so
+// that turned over its 8 rows are 8 neighbouring bytes.
+template <typename T, CastMode MODE>
+__global__ __launch_bounds__(256) void cast_tile(CastTileArgs a, uint32_t row_tiles, uint32_t col_tiles) {
+    constexpr bool TURN = MODE != kWeights;
+    __shared__ __align__(16) uint8_t turn[TURN ? 128 * 144 : 16];
+    __shared__ uint32_t tops[MODE == kColumns ? 16 * 128 : 4];
+    const uint32_t tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
+    uint32_t bt = blockIdx.x;
+    const uint32_t ct = bt % col_tiles;
+    bt /= col_tiles;
+    const uint32_t rt = bt % row_tiles, e = bt / row_tiles;
+    // x as it lies: [xrows, xcols]
+    const uint32_t xrows = MODE == kWeightsTransposed ? a.cols : a.rows;
+    const uint32_t xcols = MODE == kWeightsTransposed ? a.rows : a.cols;
+    uint32_t limit = xrows;
+    if (MODE == kColumns && a.used) {
+        const int32_t u = *a.used;
+        limit = u < 0 ? 0 : (uint32_t)u < limit ? (uint32_t)u : limit;
+        if (rt * 128 >= limit) return;
+    }
+    const T* x = static_cast<const T*>(a.x) + (MODE == kColumns ? 0 : (uint64_t)e * xrows * xcols);
+    const uint64_t stride = MODE == kColumns ? a.x_stride : xcols;
+    const uint32_t c0 = ct * 128 + cg * 8, r0 = rt * 128 + rg * 8;
+    union {
+        xu32x4 w[sizeof(T) / 2];
+        T v[8];
+    } p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const T* xr = x + (r0 + i) * stride + c0;
+        if (r0 + i < limit && a.wide && c0 + 8 <= xcols) {
+#pragma unroll
+            for (int h = 0; h < (int)sizeof(T) / 2; ++h) p[i].w[h] = reinterpret_cast<const xu32x4*>(xr)[h];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[i].v[j] = r0 + i < limit && c0 + j < xcols ? xr[j] : (T)0.0f;
+        }
+    }
+    uint32_t sbyte[8];
+    float inv[8];
+    if (MODE == kColumns) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max(top, finite_bits(to_float(p[i].v[j])));
+            tops[rg * 128 + cg * 8 + j] = top;
+        }
+        __syncthreads();
+        if (tid < 128) {
+            uint32_t top = 0;
+            for (int g = 0; g < 16; ++g) top = max(top, tops[g * 128 + tid]);
+            tops[tid] = scale_byte(top);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) inv[j] = inverse_scale(sbyte[j] = tops[cg * 8 + j]);
+    } else {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = max(top, finite_bits(to_float(p[i].v[j])));
+        for (int m = 32; m; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+        if ((tid & 63) == 0) tops[tid >> 6] = top;
+        __syncthreads();
+        const uint32_t b = scale_byte(max(max(tops[0], tops[1]), max(tops[2], tops[3])));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) inv[j] = inverse_scale(sbyte[j] = b);
+    }
+    // the result's rows and columns of blocks, and its tile
+    const uint32_t orow_tiles = MODE == kWeights ? row_tiles : col_tiles;
+    const uint32_t or0 = (MODE == kWeights ? rt : ct) * 128, ob = MODE == kWeights ? ct : rt;
+    const uint32_t orows = MODE == kColumns ? a.cols : a.rows;
+    const uint32_t blocks = MODE == kWeights ? col_tiles : row_tiles;
+    uint8_t* data = a.data + (uint64_t)e * orows * a.data_stride;
+    if (MODE == kWeights) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const xu32x2 q = {four_fp8(scaled(to_float(p[i].v[0]), inv[0]), scaled(to_float(p[i].v[1]), inv[1]),
+                                       scaled(to_float(p[i].v[2]), inv[2]), scaled(to_float(p[i].v[3]), inv[3])),
+                              four_fp8(scaled(to_float(p[i].v[4]), inv[4]), scaled(to_float(p[i].v[5]), inv[5]),
+                                       scaled(to_float(p[i].v[6]), inv[6]), scaled(to_float(p[i].v[7]), inv[7]))};
+            if (r0 + i < orows) *reinterpret_cast<xu32x2*>(data + (uint64_t)(r0 + i) * a.data_stride + c0) = q;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const xu32x2 q = {four_fp8(scaled(to_float(p[0].v[j]), inv[j]), scaled(to_float(p[1].v[j]), inv[j]),
+                                       scaled(to_float(p[2].v[j]), inv[j]), scaled(to_float(p[3].v[j]), inv[j])),
+                              four_fp8(scaled(to_float(p[4].v[j]), inv[j]), scaled(to_float(p[5].v[j]), inv[j]),
+                                       scaled(to_float(p[6].v[j]), inv[j]), scaled(to_float(p[7].v[j]), inv[j]))};
+            *reinterpret_cast<xu32x2*>(turn + (cg * 8 + j) * 144 + rg * 8) = q;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t r = i * 32 + (tid >> 3), c = (tid & 7) * 16;
+            if (or0 + r < orows)
+                *reinterpret_cast<xu32x4*>(data + (uint64_t)(or0 + r) * a.data_stride + ob * 128 + c) =
+                    *reinterpret_cast<const xu32x4*>(turn + r * 144 + c);
+        }
+    }
+    // scales, and ones past the last block
+    if (MODE == kColumns) {
+        if (rg == 0)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j < orows) {
+                    uint8_t* s = a.scale + (uint64_t)(c0 + j) * a.scale_stride;
+                    s[ob] = (uint8_t)sbyte[j];
+                    if (ob == blocks - 1)
+                        for (uint32_t b = blocks; b < a.scale_stride; ++b) s[b] = 127;
+                }
+    } else if (tid == 0) {
+        uint8_t* s = a.scale + ((uint64_t)e * orow_tiles + or0 / 128) * a.scale_stride;
+        s[ob] = (uint8_t)sbyte[0];
+        if (ob == blocks - 1)
+            for (uint32_t b = blocks; b < a.scale_stride; ++b) s[b] = 127;
+    }
+}
+
+template <typename T>
+void rows_type(const CastRowsArgs& a, hipStream_t stream) {
+    const uint32_t pieces = (a.data_stride + kWaveCols - 1) / kWaveCols;
+    const uint32_t token_blocks = (uint32_t)(((uint64_t)a.tokens * pieces + 3) / 4);
+    hipLaunchKernelGGL(cast_rows<T>, dim3(token_blocks + (a.row ? a.experts : 0)), dim3(256), 0, stream, a, pieces,
+                       token_blocks);
+}
+
+template <typename T>
+void weights_type(const CastTileArgs& a, hipStream_t stream) {
+    const uint32_t nt = (a.rows + 127) / 128, kt = (a.cols + 127) / 128;
+    if (a.transpose)
+        hipLaunchKernelGGL((cast_tile<T, kWeightsTransposed>), dim3(nt * kt * a.experts), dim3(256), 0, stream, a, kt, nt);
+    else
+        hipLaunchKernelGGL((cast_tile<T, kWeights>), dim3(nt * kt * a.experts), dim3(256), 0, stream, a, nt, kt);
+}
+
+template <typename T>
+void columns_type(const CastTileArgs& a, hipStream_t stream) {
+    const uint32_t rt = (a.rows + 127) / 128, ct = (a.cols + 127) / 128;
+    hipLaunchKernelGGL((cast_tile<T, kColumns>), dim3(rt * ct), dim3(256), 0, stream, a, rt, ct);
+}
+
+}  // namespace
+
+void launch_cast_rows(const CastRowsArgs& a, uint32_t dtype, hipStream_t stream) {
+    if (dtype == ZC_BF16) rows_type<__bf16>(a, stream);
+    else if (dtype == ZC_FP16) rows_type<_Float16>(a, stream);
+    else rows_type<float>(a, stream);
+}
+
+void launch_cast_weights(const CastTileArgs& a, uint32_t dtype, hipStream_t stream) {
+    if (dtype == ZC_BF16) weights_type<__bf16>(a, stream);
+    else if (dtype == ZC_FP16) weights_type<_Float16>(a, stream);
+    else weights_type<float>(a, stream);
+}
+
+void launch_cast_columns(const CastTileArgs& a, uint32_t dtype, hipStream_t stream) {
+    if (dtype == ZC_BF16) columns_type<__bf16>(a, stream);
+    else if (dtype == ZC_FP16) columns_type<_Float16>(a, stream);
+    else columns_type<float>(a, stream);
+}
+
+}  // namespace zc

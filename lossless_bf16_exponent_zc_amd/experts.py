@@ -1,0 +1,353 @@
+"""ctypes binding of the expert operators (the C ABI in include/zc_experts.h).
+
+Around the compressed all-to-all: ``ExpertPlan`` sorts tokens by expert
+(route, dispatch, dispatch_fp8), brings rows back with the router's weights
+(combine) and takes the gradients of both (combine_backward; the gradient of
+dispatch is combine without weights).  ``quantize_rows`` / ``_weights`` /
+``_columns`` cast to 8-bit blocks of 128; ``expert_product`` and
+``expert_weight_grad`` multiply such blocks, expert by expert.
+
+Argument marshalling and checks only, as in ``binding``: every buffer is the
+caller's, every call enqueues on the current (or the given) stream.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from . import binding
+from .binding import ZC_ERR_CAPACITY, ZC_ERR_INVALID_ARG, ZC_ERR_UNSUPPORTED, ZcError
+
+# Every symbol include/zc_experts.h declares.
+EXPERT_EXPORTS = (
+    "zc_route_rows", "zc_route_workspace_bytes", "zc_route", "zc_dispatch", "zc_dispatch_fp8",
+    "zc_combine", "zc_combine_backward", "zc_quantize_rows", "zc_quantize_weights",
+    "zc_quantize_columns", "zc_expert_product", "zc_expert_weight_grad",
+)
+
+BLOCK = 128  # values per scale
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_FP8, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+_lib = None
+
+
+def lib() -> ctypes.CDLL:
+    """libzc.so with the expert operators' signatures set."""
+    global _lib
+    if _lib is not None:
+        return _lib
+    L = binding.lib()
+    vp, u32, u64, i = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int
+    args = {
+        "zc_route_rows": [u64, u32, u32, u32],
+        "zc_route_workspace_bytes": [u64, u32, u32],
+        "zc_route": [vp, u64, u32, u32, u32, vp, vp, vp, vp, u64, vp, u64, vp],
+        "zc_dispatch": [vp, u64, u32, u64, u32, u32, u32, vp, vp, vp, vp, u64, u64, vp],
+        "zc_dispatch_fp8": [vp, u64, u32, u64, u32, u32, u32, vp, vp, vp, vp, vp, u64, vp],
+        "zc_combine": [vp, u64, vp, u32, u64, u32, u32, vp, u64, vp, u64, vp],
+        "zc_combine_backward": [vp, u64, vp, u64, vp, u32, u64, u32, u32, u32, vp, vp, vp, u64, vp, u64, vp, vp],
+        "zc_quantize_rows": [vp, u64, u32, u64, u32, vp, vp, vp, vp],
+        "zc_quantize_weights": [vp, u32, u32, u32, u32, i, vp, vp, vp],
+        "zc_quantize_columns": [vp, u64, u32, u64, u32, vp, vp, vp, vp],
+        "zc_expert_product": [vp, vp, u64, vp, vp, u32, u32, u32, vp, vp, vp, u64, u32, vp],
+        "zc_expert_weight_grad": [vp, vp, vp, vp, u64, u32, u32, u32, vp, vp, u32, vp],
+    }
+    for name in EXPERT_EXPORTS:
+        f = getattr(L, name)
+        f.argtypes = args[name]
+        f.restype = u64 if name in ("zc_route_rows", "zc_route_workspace_bytes") else i
+    _lib = L
+    return L
+
+
+def _call(name: str, *args):
+    rc = getattr(lib(), name)(*args)
+    if rc:
+        raise ZcError(rc, name)
+
+
+def _stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _bad(what: str, why: str, code: int = ZC_ERR_INVALID_ARG):
+    raise ZcError(code, f"{what}: {why}")
+
+
+def _matrix(t, what: str, width: int, rows: int, dtype=None):
+    """A GPU matrix of `width` columns, contiguous along them, of `dtype` (or
+    one of the three row types) with at least `rows` rows."""
+    if not getattr(t, "is_cuda", False):
+        _bad(what, "not a GPU tensor")
+    if t.dim() != 2 or t.shape[1] != width:
+        _bad(what, f"shape {tuple(t.shape)}, (rows, {width}) expected")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        _bad(what, f"type {t.dtype}" + (f", {dtype} expected" if dtype is not None else ""))
+    if (width > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < width):
+        _bad(what, f"strides {t.stride()}: rows must be contiguous and apart")
+    if t.shape[0] < rows:
+        _bad(what, f"{t.shape[0]} rows, {rows} needed", ZC_ERR_CAPACITY)
+    return t
+
+
+def _row_stride(t) -> int:
+    return max(t.stride(0), t.shape[1])
+
+
+def _flat(t, what: str, dtype, count: int):
+    """A contiguous GPU tensor of `dtype` with at least `count` elements."""
+    if not getattr(t, "is_cuda", False):
+        _bad(what, "not a GPU tensor")
+    if t.dtype != dtype:
+        _bad(what, f"type {t.dtype}, {dtype} expected")
+    if not t.is_contiguous():
+        _bad(what, "not contiguous")
+    if t.numel() < count:
+        _bad(what, f"{t.numel()} elements, {count} needed", ZC_ERR_CAPACITY)
+    return t.data_ptr()
+
+
+def _up(n: int, m: int) -> int:
+    return -(-n // m) * m
+
+
+class Fp8Blocks(NamedTuple):
+    """A matrix (or one per expert) in 8-bit blocks of 128: ``data`` E4M3
+    [..., rows, up(cols, 128)], ``scale`` E8M0 [..., scale rows,
+    up(ceil(cols / 128), 4)], ``cols`` the columns that hold values."""
+    data: torch.Tensor
+    scale: torch.Tensor
+    cols: int
+
+    def float(self, rows_per_scale: int = 1) -> torch.Tensor:
+        """The values the blocks stand for, in 32 bits (128 rows per scale
+        for weights)."""
+        s = self.scale.float()[..., :self.data.shape[-1] // BLOCK]
+        if rows_per_scale > 1:
+            s = s.repeat_interleave(rows_per_scale, -2)[..., :self.data.shape[-2], :]
+        v = self.data.float().unflatten(-1, (-1, BLOCK)) * s[..., None]
+        return v.flatten(-2)[..., :self.cols]
+
+
+def _empty_blocks(lead, scale_lead, cols: int, device) -> Fp8Blocks:
+    return Fp8Blocks(torch.zeros(*lead, _up(cols, BLOCK), dtype=_FP8, device=device),
+                     torch.zeros(*scale_lead, _up(-(-cols // BLOCK), 4), dtype=torch.uint8,
+                                 device=device).view(_E8M0), cols)
+
+
+def empty_fp8_rows(rows: int, cols: int, device="cuda") -> Fp8Blocks:
+    """A blocked [rows, cols] for quantize_rows and dispatch_fp8 (1 x 128)."""
+    return _empty_blocks((rows,), (rows,), cols, device)
+
+
+def empty_fp8_weights(experts: int, n: int, k: int, device="cuda") -> Fp8Blocks:
+    """A blocked [experts, n, k] for quantize_weights (128 x 128)."""
+    return _empty_blocks((experts, n), (experts, -(-n // BLOCK)), k, device)
+
+
+def empty_fp8_columns(rows: int, cols: int, device="cuda") -> Fp8Blocks:
+    """A blocked [cols, rows] for quantize_columns of a [rows, cols] matrix."""
+    return _empty_blocks((cols,), (cols,), rows, device)
+
+
+def _blocks(f: Fp8Blocks, what: str, lead, scale_lead, cols: int):
+    """Pointers of data and scale of blocks of the given shape.  The first
+    dimension may be longer."""
+    if f.cols != cols:
+        _bad(what, f"{f.cols} columns, {cols} expected")
+    out = []
+    for t, dtype, dims, width in ((f.data, _FP8, lead, _up(cols, BLOCK)),
+                                  (f.scale, _E8M0, scale_lead, _up(-(-cols // BLOCK), 4))):
+        if not getattr(t, "is_cuda", False):
+            _bad(what, "not a GPU tensor")
+        if t.dtype != dtype:
+            _bad(what, f"type {t.dtype}, {dtype} expected")
+        if not t.is_contiguous():
+            _bad(what, "not contiguous")
+        if t.dim() != len(dims) + 1 or tuple(t.shape[1:]) != tuple(dims[1:]) + (width,):
+            _bad(what, f"shape {tuple(t.shape)}, {tuple(dims) + (width,)} expected")
+        if t.shape[0] < dims[0]:
+            _bad(what, f"{t.shape[0]} rows, {dims[0]} needed", ZC_ERR_CAPACITY)
+        out.append(t.data_ptr())
+    return out
+
+
+class Routing(NamedTuple):
+    """Where slots go: ``offsets`` [experts + 1] (first row of each expert's
+    segment, and the end), ``counts`` [experts], ``row`` [tokens, topk] (-1
+    without a row), ``slot`` [rows] (-1 for a padding row); int32."""
+    offsets: torch.Tensor
+    counts: torch.Tensor
+    row: torch.Tensor
+    slot: torch.Tensor
+
+
+class ExpertPlan:
+    """Sizes of one routing: tokens, choices per token, experts, and the
+    multiple that segments begin at (1 packs them, as a codec ``Plan`` with
+    one segment per expert wants them; ``expert_weight_grad`` wants 128)."""
+
+    def __init__(self, tokens: int, topk: int, experts: int, align: int = 1):
+        self.tokens, self.topk, self.experts, self.align = int(tokens), int(topk), int(experts), int(align)
+        if min(self.tokens, self.topk, self.experts, self.align) < 0:
+            _bad("ExpertPlan", "negative size")
+        self.rows = lib().zc_route_rows(self.tokens, self.topk, self.experts, self.align)
+        self.workspace_bytes = lib().zc_route_workspace_bytes(self.tokens, self.topk, self.experts)
+        if self.workspace_bytes == 0 or (self.rows == 0 and self.tokens):
+            _bad("ExpertPlan", f"{tokens} tokens, {topk} choices, {experts} experts, align {align}",
+                 ZC_ERR_UNSUPPORTED)
+        if self.align & (self.align - 1) or not 1 <= self.align <= 1024:
+            _bad("ExpertPlan", f"align {align}", ZC_ERR_UNSUPPORTED)
+
+    # buffers (torch allocation only) -------------------------------------
+    def empty_routing(self, device="cuda") -> Routing:
+        z = lambda *s: torch.zeros(*s, dtype=torch.int32, device=device)
+        return Routing(z(self.experts + 1), z(self.experts), z(self.tokens, self.topk), z(self.rows))
+
+    def empty_workspace(self, device="cuda"):
+        return torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
+
+    def empty_rows(self, hidden: int, dtype=torch.bfloat16, device="cuda"):
+        return torch.zeros(self.rows, hidden, dtype=dtype, device=device)
+
+    def empty_fp8(self, hidden: int, device="cuda") -> Fp8Blocks:
+        return empty_fp8_rows(self.rows, hidden, device)
+
+    # checks ---------------------------------------------------------------
+    def _routing(self, r: Routing):
+        i32 = torch.int32
+        return (_flat(r.offsets, "offsets", i32, self.experts + 1), _flat(r.counts, "counts", i32, self.experts),
+                _flat(r.row, "row", i32, self.tokens * self.topk))
+
+    def _weights(self, w):
+        return 0 if w is None else _flat(w, "weights", torch.float32, self.tokens * self.topk)
+
+    # calls ----------------------------------------------------------------
+    def route(self, ids, routing: Routing, ws, stream=None):
+        """Enqueue the sorting of ids (int32 [tokens, topk]; outside
+        0..experts-1: no row) into routing."""
+        p = _flat(ids, "ids", torch.int32, self.tokens * self.topk)
+        off, cnt, row = self._routing(routing)
+        slot = _flat(routing.slot, "slot", torch.int32, self.rows)
+        w = _flat(ws, "workspace", torch.uint8, self.workspace_bytes)
+        _call("zc_route", p, self.tokens, self.topk, self.experts, self.align, off, cnt, row, slot,
+              routing.slot.numel(), w, ws.numel(), _stream(stream))
+
+    def dispatch(self, x, routing: Routing, rows, stream=None):
+        """Enqueue rows[row of (t, k)] = x[t]; padding rows are zeros."""
+        _matrix(x, "x", x.shape[-1], self.tokens)
+        _matrix(rows, "rows", x.shape[1], self.rows, x.dtype)
+        off, cnt, row = self._routing(routing)
+        _call("zc_dispatch", x.data_ptr(), _row_stride(x), _DTYPES[x.dtype], self.tokens, self.topk, self.experts,
+              x.shape[1], off, cnt, row, rows.data_ptr(), _row_stride(rows), rows.shape[0], _stream(stream))
+
+    def dispatch_fp8(self, x, routing: Routing, out: Fp8Blocks, stream=None):
+        """Enqueue dispatch with the rows stored as 1 x 128 blocks."""
+        _matrix(x, "x", x.shape[-1], self.tokens)
+        data, scale = _blocks(out, "out", (self.rows,), (self.rows,), x.shape[1])
+        off, cnt, row = self._routing(routing)
+        _call("zc_dispatch_fp8", x.data_ptr(), _row_stride(x), _DTYPES[x.dtype], self.tokens, self.topk,
+              self.experts, x.shape[1], off, cnt, row, data, scale, min(out.data.shape[0], out.scale.shape[0]),
+              _stream(stream))
+
+    def combine(self, rows, weights, routing: Routing, y, stream=None):
+        """Enqueue y[t] = sum over k of weights[t, k] * rows[row of (t, k)];
+        weights None: ones, which makes it the gradient of dispatch."""
+        _matrix(y, "y", y.shape[-1], self.tokens)
+        _matrix(rows, "rows", y.shape[1], self.rows, y.dtype)
+        _, _, row = self._routing(routing)
+        _call("zc_combine", rows.data_ptr(), _row_stride(rows), self._weights(weights), _DTYPES[y.dtype],
+              self.tokens, self.topk, y.shape[1], row, rows.shape[0], y.data_ptr(), _row_stride(y),
+              _stream(stream))
+
+    def combine_backward(self, dy, rows, weights, routing: Routing, drows, dweights, stream=None):
+        """Enqueue the gradient of combine: drows (padding rows zeros) and
+        dweights (float32 [tokens, topk]); either may be None, and rows with
+        dweights."""
+        _matrix(dy, "dy", dy.shape[-1], self.tokens)
+        off, cnt, row = self._routing(routing)
+        if drows is None and dweights is None:
+            _bad("combine_backward", "no gradient asked for")
+        capacity = []
+        if drows is not None:
+            _matrix(drows, "drows", dy.shape[1], self.rows, dy.dtype)
+            capacity.append(drows.shape[0])
+        if dweights is not None:
+            if rows is None:
+                _bad("combine_backward", "dweights needs rows")
+            _matrix(rows, "rows", dy.shape[1], self.rows, dy.dtype)
+            capacity.append(rows.shape[0])
+        _call("zc_combine_backward", dy.data_ptr(), _row_stride(dy), rows.data_ptr() if dweights is not None else 0,
+              _row_stride(rows) if dweights is not None else 0, self._weights(weights), _DTYPES[dy.dtype],
+              self.tokens, self.topk, self.experts, dy.shape[1], off, cnt, row, min(capacity),
+              drows.data_ptr() if drows is not None else 0, _row_stride(drows) if drows is not None else 0,
+              self._weights(dweights), _stream(stream))
+
+
+def _used(used):
+    return 0 if used is None else _flat(used, "used", torch.int32, 1)
+
+
+def quantize_rows(x, out: Fp8Blocks, used=None, stream=None):
+    """Enqueue the cast of x [rows, cols] to 1 x 128 blocks.  used: None or a
+    device int32 (e.g. ``routing.offsets[-1:]``); rows from there on are left."""
+    _matrix(x, "x", x.shape[-1], 0)
+    rows, cols = x.shape
+    data, scale = _blocks(out, "out", (rows,), (rows,), cols)
+    _call("zc_quantize_rows", x.data_ptr(), _row_stride(x), _DTYPES[x.dtype], rows, cols, _used(used), data, scale,
+          _stream(stream))
+
+
+def quantize_weights(w, out: Fp8Blocks, transpose: bool = False, stream=None):
+    """Enqueue the cast of w [experts, n, k] (transpose: [experts, k, n]) to
+    the 128 x 128 blocks of [experts, n, k]."""
+    if w.dim() != 3 or w.dtype not in _DTYPES:
+        _bad("w", f"shape {tuple(w.shape)}, type {w.dtype}")
+    e, n, k = w.shape if not transpose else (w.shape[0], w.shape[2], w.shape[1])
+    p = _flat(w, "w", w.dtype, 0)
+    data, scale = _blocks(out, "out", (e, n), (e, -(-n // BLOCK)), k)
+    _call("zc_quantize_weights", p, _DTYPES[w.dtype], e, n, k, int(bool(transpose)), data, scale, _stream(stream))
+
+
+def quantize_columns(x, out: Fp8Blocks, used=None, stream=None):
+    """Enqueue the cast of x [rows, cols] in blocks of 128 rows of a column,
+    stored as the blocked [cols, rows]."""
+    _matrix(x, "x", x.shape[-1], 0)
+    rows, cols = x.shape
+    data, scale = _blocks(out, "out", (cols,), (cols,), rows)
+    _call("zc_quantize_columns", x.data_ptr(), _row_stride(x), _DTYPES[x.dtype], rows, cols, _used(used), data,
+          scale, _stream(stream))
+
+
+def expert_product(a: Fp8Blocks, w: Fp8Blocks, out, offsets=None, counts=None, stream=None):
+    """Enqueue out[r] = A[r] W[e]^T for the rows r of every expert's segment;
+    a: 1 x 128 blocks [rows, k], w: 128 x 128 blocks [experts, n, k], out
+    [rows, n].  offsets None: one expert, all rows."""
+    if w.data.dim() != 3 or a.data.dim() != 2:
+        _bad("expert_product", "a is [rows, k], w is [experts, n, k]")
+    (experts, n, _), rows = w.data.shape, out.shape[0]
+    _matrix(out, "out", n, 0)
+    ap, asp = _blocks(a, "a", (rows,), (rows,), w.cols)
+    wp, wsp = _blocks(w, "w", (experts, n), (experts, -(-n // BLOCK)), w.cols)
+    off = 0 if offsets is None else _flat(offsets, "offsets", torch.int32, experts + 1)
+    cnt = 0 if counts is None else _flat(counts, "counts", torch.int32, experts)
+    _call("zc_expert_product", ap, asp, rows, wp, wsp, experts, n, w.cols, off, cnt, out.data_ptr(),
+          _row_stride(out), _DTYPES[out.dtype], _stream(stream))
+
+
+def expert_weight_grad(y: Fp8Blocks, x: Fp8Blocks, dw, offsets=None, stream=None):
+    """Enqueue dw[e] = Y_e X_e^T over the rows of every expert's segment
+    (segments begin at multiples of 128); y: blocked [n, rows], x: blocked
+    [k, rows] from quantize_columns, dw [experts, n, k]."""
+    if dw.dim() != 3 or dw.dtype not in _DTYPES:
+        _bad("dw", f"shape {tuple(dw.shape)}, type {dw.dtype}")
+    experts, n, k = dw.shape
+    p = _flat(dw, "dw", dw.dtype, 0)
+    yp, ysp = _blocks(y, "y", (n,), (n,), x.cols)
+    xp, xsp = _blocks(x, "x", (k,), (k,), x.cols)
+    off = 0 if offsets is None else _flat(offsets, "offsets", torch.int32, experts + 1)
+    _call("zc_expert_weight_grad", yp, ysp, xp, xsp, x.cols, experts, n, k, off, p, _DTYPES[dw.dtype],
+          _stream(stream))
