@@ -244,7 +244,8 @@ zc_status zc_expert_product(const void* d_a, const void* d_a_scale, uint64_t row
         return ZC_ERR_INVALID_ARG;
     const ProductArgs a{static_cast<const uint8_t*>(d_a), static_cast<const uint8_t*>(d_a_scale),
                         static_cast<const uint8_t*>(d_w), static_cast<const uint8_t*>(d_w_scale), d_offsets, d_counts,
-                        d_out, out_stride, (uint32_t)rows, experts, n, stored(k), scales(k), scales(k), out_dtype};
+                        d_out, out_stride, (uint32_t)rows, experts, n, stored(k), scales(k), scales(k), out_dtype,
+                        aligned(d_out, 16) && out_stride * elem_bytes(out_dtype) % 16 == 0};
     launch_product(a, stream);
     return launch_status();
 }
@@ -261,7 +262,8 @@ zc_status zc_expert_weight_grad(const void* d_y, const void* d_y_scale, const vo
         return ZC_ERR_INVALID_ARG;
     const WeightGradArgs a{static_cast<const uint8_t*>(d_y), static_cast<const uint8_t*>(d_y_scale),
                            static_cast<const uint8_t*>(d_x), static_cast<const uint8_t*>(d_x_scale), d_offsets, d_dw,
-                           stored((uint32_t)rows), experts, n, k, scales((uint32_t)rows), out_dtype};
+                           stored((uint32_t)rows), experts, n, k, scales((uint32_t)rows), out_dtype,
+                           aligned(d_dw, 16) && (uint64_t)k * elem_bytes(out_dtype) % 16 == 0};
     launch_weight_grad(a, stream);
     return launch_status();
 }

@@ -83,6 +83,7 @@ struct ProductArgs {
     uint32_t rows, experts, n, k;  // k: stored, a multiple of 128
     uint32_t a_scale_stride, w_scale_stride;
     uint32_t out_dtype;
+    uint32_t wide;           // out and its rows start at 16-byte addresses
 };
 
 struct WeightGradArgs {
@@ -95,6 +96,7 @@ struct WeightGradArgs {
     uint32_t rows;           // stored, a multiple of 128
     uint32_t experts, n, k, scale_stride;
     uint32_t out_dtype;
+    uint32_t wide;
 };
 
 uint64_t route_tiles(uint64_t nslots);

@@ -20,18 +20,17 @@ __device__ __forceinline__ i32x8 two(xu32x4 lo, xu32x4 hi) {
     return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
-// One tile of a product, whichever product it is.
+// One tile of a product, whichever product it is: rows of the token side
+// against rows of the weight side, over `blocks` blocks.
 struct Tile {
-    const uint8_t* a;        // first row of the token side, at its first block
-    const uint8_t* as;       // its scales
-    const uint8_t* w;        // first row of the weight side
-    const uint8_t* ws;       // scales of the weight side's row 0
-    uint32_t a_rows, w_rows; // rows that exist from there on
-    uint32_t w0;             // index of the weight side's first row (for its scales)
+    const uint8_t* a;         // first row of the token side, at its first block
+    const uint8_t* w;         // first row of the weight side, at its first block
+    const uint8_t* as;        // scale rows of the token side, from its first row
+    const uint8_t* ws;        // scale rows of the weight side, from its first row's
+    uint32_t a_rows, w_rows;  // rows that exist from there on
+    uint32_t a_stride, w_stride, as_stride, ws_stride;
+    uint32_t first_block;     // of the scale rows
     uint32_t blocks;
-    uint64_t a_stride, w_stride;
-    uint32_t as_stride, ws_stride;
-    uint32_t w_shift;        // rows per scale row of the weight side, as a shift: 7 or 0
 };
 
 // Expert and first row of the `index`-th tile of `m` rows, over all experts'
@@ -86,103 +85,339 @@ __device__ __forceinline__ Found find_tile(const ProductArgs& p, uint32_t index,
     return Found{0, 0, 0, 0, false};
 }
 
+// The shape of a tile: 4 waves as WM x WN, each TM x TN instruction tiles of
+// 16 x 16; S stages of one block (128 bytes of every row) in LDS.  WROW: every
+// row of the weight side has its own scales (else one per 128 rows).
+template <int WM_, int TM_, int TN_, int S_, bool WROW_>
+struct Shape {
+    static constexpr int WM = WM_, WN = 4 / WM_, TM = TM_, TN = TN_, S = S_;
+    static constexpr bool WROW = WROW_;
+    static constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
+    static constexpr int kScaleAt = (BM + BN) * 128;
+    static constexpr int kStage = kScaleAt + 1024 + (WROW ? 1024 : 0);
+    static constexpr int kLoads = (BM + BN) / 32 + 1 + (WROW ? 1 : 0);  // per wave and stage
+    static constexpr int kLds = S * kStage;
+};
+
+// Where a tile's results go.
 template <typename T>
-__device__ __forceinline__ void store4(T* out, const f32x4& v, uint32_t n) {
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i)
-        if (i < n) out[i] = (T)v[i];
+struct Out {
+    T* out;              // row 0, column 0 of the tile
+    uint64_t stride;     // elements
+    uint32_t rows, cols; // of the tile that exist
+    uint32_t wide;       // rows start at 16-byte addresses
+};
+
+// From here to the kernels the code uses types and registers that only the
+// device has; the host's pass over this file sees the kernels' names alone.
+#if defined(__HIP_DEVICE_COMPILE__)
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+template <int N>
+__device__ __forceinline__ void wait_loads_and_barrier() {
+    // at most N loads to LDS outstanding and no read of LDS, in every wave
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void store_out(void* out, uint32_t dtype, uint64_t at, const f32x4& v, uint32_t n) {
-    if (dtype == ZC_BF16) store4(static_cast<__bf16*>(out) + at, v, n);
-    else if (dtype == ZC_FP16) store4(static_cast<_Float16*>(out) + at, v, n);
-    else store4(static_cast<float*>(out) + at, v, n);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, 0xFFFFFFFFu, 0x00020000);
 }
 
-// 16 weight rows by 64 token rows of a tile, from memory to the unit.
-__device__ __forceinline__ void wave_tile(const Tile& t, uint32_t w_first, f32x4* acc) {
-    const uint32_t lane = __lane_id(), r = lane & 15, g = lane >> 4;
-    const uint32_t wr = w_first + r < t.w_rows ? w_first + r : t.w_rows - 1;
-    const uint8_t* w = t.w + wr * t.w_stride + g * 32;
-    const uint8_t* ws = t.ws + (uint64_t)((t.w0 + wr) >> t.w_shift) * t.ws_stride;
-    const uint8_t* a[4];
-    const uint8_t* as[4];
+// Row of the weight side that lane row m (0..15) of instruction tile i holds:
+// two neighbouring tiles interleave in fours, so that a lane's results of the
+// two are 8 neighbouring columns (one 16-byte store in 16-bit types).
+__device__ __forceinline__ constexpr uint32_t weight_row(uint32_t i, uint32_t m) {
+    return (i >> 1) * 32 + (m >> 2) * 8 + (i & 1) * 4 + (m & 3);
+}
+
+// Where 16-byte piece c of a row lies: rows of 128 bytes all start in the same
+// bank, so the pieces turn with the row.  Token rows are read 16 in order,
+// weight rows as above; both orders see eight different pieces in any eight
+// neighbouring lanes.
+__device__ __forceinline__ uint32_t turn_a(uint32_t row) { return row & 7; }
+__device__ __forceinline__ uint32_t turn_w(uint32_t row) { return (row & 3) * 2 + ((row >> 3) & 1); }
+
+template <typename SH>
+__device__ __forceinline__ void tile_product(const Tile& t, uint8_t* lds, f32x4 (&acc)[SH::TM][SH::TN]) {
+    constexpr int NA = SH::BM / 32, NW = SH::BN / 32;
+    const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x >> 6);
+    const uint32_t r = lane & 15, g = lane >> 4;
+    // a load moves 8 rows: lane l brings the piece that belongs at l's place
+    uint32_t at_a[NA], at_w[NW];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t ar = i * 16 + r < t.a_rows ? i * 16 + r : t.a_rows - 1;
-        a[i] = t.a + ar * t.a_stride + g * 32;
-        as[i] = t.as + (uint64_t)ar * t.as_stride;
-        acc[i] = f32x4{0, 0, 0, 0};
+    for (int i = 0; i < NA; ++i) {
+        const uint32_t row = (wave * NA + i) * 8 + (lane >> 3);
+        at_a[i] = (row < t.a_rows ? row : t.a_rows - 1) * t.a_stride + (((lane & 7) ^ turn_a(row)) << 4);
     }
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        const uint32_t row = (wave * NW + i) * 8 + (lane >> 3);
+        at_w[i] = (row < t.w_rows ? row : t.w_rows - 1) * t.w_stride + (((lane & 7) ^ turn_w(row)) << 4);
+    }
+    const uint32_t srow = wave * 64 + lane;
+    const uint32_t at_as = (srow < t.a_rows && srow < SH::BM ? srow : t.a_rows - 1 < SH::BM ? t.a_rows - 1 : 0) * t.as_stride;
+    const uint32_t at_ws = (srow < t.w_rows ? srow : t.w_rows - 1) * t.ws_stride;
+    const __amdgpu_buffer_rsrc_t ra = buffer(t.a), rw = buffer(t.w), ras = buffer(t.as), rws = buffer(t.ws);
+
+    auto load = [&](uint32_t block, uint32_t slot) {
+        // blocks past the last are loaded again, so that the number of loads
+        // in flight does not depend on where the loop stands
+        block = block < t.blocks ? block : t.blocks - 1;
+        uint8_t* base = lds + slot * SH::kStage;
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(base + (wave * NA + i) * 1024), 16, at_a[i],
+                                                     block * 128, 0, 0);
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(base + SH::BM * 128 + (wave * NW + i) * 1024), 16,
+                                                     at_w[i], block * 128, 0, 0);
+        const uint32_t word = (t.first_block + block) & ~3u;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ras, (lds_void*)(base + SH::kScaleAt + wave * 256), 4, at_as, word, 0, 0);
+        if (SH::WROW)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rws, (lds_void*)(base + SH::kScaleAt + 1024 + wave * 256), 4, at_ws,
+                                                     word, 0, 0);
+    };
+
+    // scales of the weight side where 128 rows share them: the wave's 64 (or
+    // 128) rows have one scale row; a lane keeps 4 of its bytes
+    const uint32_t wave_a = (wave / SH::WN) * SH::TM * 16, wave_w = (wave % SH::WN) * SH::TN * 16;
+    uint32_t ws_words = 0;
+    const uint8_t* ws_row = t.ws + (uint64_t)(wave_w < t.w_rows ? wave_w >> 7 : 0) * t.ws_stride;
+
+    for (int s = 0; s < SH::S - 1; ++s) load(s, s);
+    uint32_t slot = 0;
+    // where a lane's two pieces of a row lie (pieces 2g and 2g + 1)
+    const uint32_t ta = turn_a(r), tw0 = turn_w(weight_row(0, r)), tw1 = turn_w(weight_row(1, r));
+    const uint32_t la = (wave_a + r) * 128;
+    const uint32_t a_lo = la + (((2 * g) ^ ta) << 4), a_hi = la + (((2 * g + 1) ^ ta) << 4);
+    const uint32_t lw0 = SH::BM * 128 + (wave_w + weight_row(0, r)) * 128, lw1 = lw0 + 4 * 128;
+    const uint32_t w0_lo = lw0 + (((2 * g) ^ tw0) << 4), w0_hi = lw0 + (((2 * g + 1) ^ tw0) << 4);
+    const uint32_t w1_lo = lw1 + (((2 * g) ^ tw1) << 4), w1_hi = lw1 + (((2 * g + 1) ^ tw1) << 4);
     for (uint32_t b = 0; b < t.blocks; ++b) {
-        const xu32x4* wp = reinterpret_cast<const xu32x4*>(w + (uint64_t)b * 128);
-        const i32x8 wv = two(wp[0], wp[1]);
-        const int sw = ws[b];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const xu32x4* ap = reinterpret_cast<const xu32x4*>(a[i] + (uint64_t)b * 128);
-            acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, two(ap[0], ap[1]), acc[i], 0, 0, 0, sw, 0,
-                                                                     (int)as[i][b]);
+        // the loads of this block are there, and every wave is done with the
+        // stage that the next load overwrites
+        wait_loads_and_barrier<(SH::S - 2) * SH::kLoads>();
+        const uint32_t fill = slot == 0 ? SH::S - 1 : slot - 1;
+        load(b + SH::S - 1, fill);
+        const uint8_t* base = lds + slot * SH::kStage;
+        const uint32_t sb = t.first_block + b, shift = (sb & 3) * 8;
+        int sw_all = 0;
+        if (!SH::WROW) {
+            const uint32_t word = sb >> 2;
+            if (b == 0 || (sb & 255) == 0)
+                ws_words = (word & ~63u) * 4 + lane * 4 < t.ws_stride
+                               ? reinterpret_cast<const uint32_t*>(ws_row)[(word & ~63u) + lane]
+                               : 0;
+            sw_all = (int)((uint32_t)__builtin_amdgcn_readlane((int)ws_words, word & 63) >> shift);
         }
-    }
-}
-
-__global__ __launch_bounds__(256) void product(ProductArgs p) {
-    const uint32_t lane = __lane_id(), r = lane & 15, g = lane >> 4, wave = uniform(threadIdx.x >> 6);
-    const Found f = find_tile(p, blockIdx.y, 64);
-    if (!f.any) return;
-    const uint32_t n0 = blockIdx.x * 64 + wave * 16;
-    if (n0 >= p.n) return;
-    f32x4 acc[4] = {};
-    if (f.count) {
-        const uint32_t wrows = (p.n + 127) / 128;
-        const Tile t{p.a + (uint64_t)f.row * p.k, p.a_scale + (uint64_t)f.row * p.a_scale_stride,
-                     p.w + (uint64_t)f.expert * p.n * p.k, p.w_scale + (uint64_t)f.expert * wrows * p.w_scale_stride,
-                     f.count, p.n, 0, p.k / 128, p.k, p.k, p.a_scale_stride, p.w_scale_stride, 7};
-        wave_tile(t, n0, acc);
-    }
-    const uint32_t j = n0 + g * 4;
-    if (j >= p.n) return;
-    const uint32_t left = p.n - j;
+        i32x8 wv[SH::TN];
+        int sw[SH::TN];
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i)
-        if (i * 16 + r < f.count) store_out(p.out, p.out_dtype, (uint64_t)(f.row + i * 16 + r) * p.out_stride + j, acc[i], left);
-    if (f.count <= 64)
-        for (uint32_t q = f.row + f.count + r; q < f.end; q += 16)
-            store_out(p.out, p.out_dtype, (uint64_t)q * p.out_stride + j, f32x4{0, 0, 0, 0}, left);
+        for (int i = 0; i < SH::TN; ++i) {
+            const uint32_t step = (i >> 1) * 32 * 128;
+            wv[i] = i & 1 ? two(*(const xu32x4*)(base + w1_lo + step), *(const xu32x4*)(base + w1_hi + step))
+                          : two(*(const xu32x4*)(base + w0_lo + step), *(const xu32x4*)(base + w0_hi + step));
+            sw[i] = SH::WROW ? (int)(*(const uint32_t*)(base + SH::kScaleAt + 1024 + (wave_w + weight_row(i, r)) * 4) >> shift)
+                             : sw_all;
+        }
+#pragma unroll
+        for (int j = 0; j < SH::TM; ++j) {
+            const i32x8 av = two(*(const xu32x4*)(base + a_lo + j * 2048), *(const xu32x4*)(base + a_hi + j * 2048));
+            const int sa = (int)(*(const uint32_t*)(base + SH::kScaleAt + (wave_a + j * 16 + r) * 4) >> shift);
+#pragma unroll
+            for (int i = 0; i < SH::TN; ++i)
+                acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv[i], av, acc[j][i], 0, 0, 0, sw[i], 0, sa);
+        }
+        slot = slot == SH::S - 1 ? 0 : slot + 1;
+    }
+    // no load may still write LDS when the next tile or another workgroup has it
+    wait_loads_and_barrier<0>();
 }
 
-__global__ __launch_bounds__(256) void weight_grad(WeightGradArgs p) {
-    const uint32_t lane = __lane_id(), r = lane & 15, g = lane >> 4, wave = uniform(threadIdx.x >> 6);
-    const uint32_t e = blockIdx.z, i0 = blockIdx.y * 64, j0 = blockIdx.x * 64 + wave * 16;
-    if (j0 >= p.k) return;
+// An accumulator read where it is written down and no earlier: read ahead of
+// the branches below, all of them would not fit the general registers.
+__device__ __forceinline__ f32x4 late(f32x4 v) {
+    asm volatile("" : "+a"(v));
+    return v;
+}
+
+// A tile with all its columns, at aligned rows, leaves from the registers: 8
+// neighbouring columns per lane.  Any other goes over LDS, 16 rows at a time,
+// and leaves row by row, neighbouring lanes in neighbouring columns.
+template <typename T, typename SH>
+__device__ __forceinline__ void store_tile(const Out<T>& o, const f32x4 (&acc)[SH::TM][SH::TN], uint8_t* lds) {
+    const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    const uint32_t m0 = (wave / SH::WN) * SH::TM * 16, n0 = (wave % SH::WN) * SH::TN * 16;
+    if (o.wide && o.cols >= (uint32_t)SH::BN) {
+        T* p = o.out + (m0 + r) * o.stride + n0 + g * 8;
+#pragma unroll
+        for (int j = 0; j < SH::TM; ++j) {
+            if (m0 + j * 16 + r < o.rows) {
+#pragma unroll
+                for (int i = 0; i < SH::TN; i += 2) {
+                    const f32x4 lo = late(acc[j][i]), hi = late(acc[j][i + 1]);
+                    union {
+                        T v[8];
+                        xu32x4 w[sizeof(T) / 2];
+                    } u;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        u.v[q] = (T)lo[q];
+                        u.v[4 + q] = (T)hi[q];
+                    }
+#pragma unroll
+                    for (int q = 0; q < (int)sizeof(T) / 2; ++q) reinterpret_cast<xu32x4*>(p + i * 16)[q] = u.w[q];
+                }
+            }
+            p += 16 * o.stride;
+        }
+        return;
+    }
+    constexpr uint32_t kCols = SH::TN * 16, kPitch = kCols + 4;  // floats
+    float* buf = reinterpret_cast<float*>(lds) + wave * 16 * kPitch;
+    const uint32_t cols = n0 < o.cols ? (o.cols - n0 < kCols ? o.cols - n0 : kCols) : 0;
+#pragma unroll
+    for (int j = 0; j < SH::TM; ++j) {
+#pragma unroll
+        for (int i = 0; i < SH::TN; ++i)
+            *reinterpret_cast<f32x4*>(buf + r * kPitch + (i >> 1) * 32 + g * 8 + (i & 1) * 4) = late(acc[j][i]);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        const uint32_t m = m0 + j * 16, rows = m < o.rows ? (o.rows - m < 16 ? o.rows - m : 16) : 0;
+#pragma unroll 1
+        for (uint32_t q = 0; q < rows; ++q)
+#pragma unroll 1
+            for (uint32_t c = lane; c < cols; c += 64) o.out[(m + q) * o.stride + n0 + c] = (T)buf[q * kPitch + c];
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+}
+
+#endif  // __HIP_DEVICE_COMPILE__
+
+template <typename SH, typename T>
+__device__ __forceinline__ void run_tile(const Tile& t, const Out<T>& o, uint8_t* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    f32x4 acc[SH::TM][SH::TN];
+#pragma unroll
+    for (int j = 0; j < SH::TM; ++j)
+#pragma unroll
+        for (int i = 0; i < SH::TN; ++i) acc[j][i] = f32x4{0, 0, 0, 0};
+    if (t.blocks) tile_product<SH>(t, lds, acc);
+    store_tile<T, SH>(o, acc, lds);
+#endif
+}
+
+constexpr uint32_t kTileRows = 256, kTileCols = 256;
+
+// Workgroup -> (slot of token rows, tile of columns).  Neighbouring workgroup
+// indexes go to different XCDs; the eight XCDs take turns at runs of 32 tiles,
+// 4 slots by 8 columns, so that what an XCD's 32 CUs read at one time is 4 + 8
+// strips of 256 rows, shared through its L2.
+struct Place {
+    uint32_t slot, col;
+};
+__device__ __forceinline__ Place place_of(uint32_t index, uint32_t col_tiles) {
+    const uint32_t xcd = index & 7, l = index >> 3;
+    const uint32_t tile = ((l >> 5) * 8 + xcd) * 32 + (l & 31);
+    const uint32_t group = tile / (4 * col_tiles), in = tile % (4 * col_tiles);
+    return Place{group * 4 + (in & 3), in >> 2};
+}
+
+// One kernel for every length of a segment: a tile takes the shape of the rows
+// it has, so that short segments do not pay for 256 rows and run beside long
+// ones.
+template <typename T>
+__global__ __launch_bounds__(256, 1) void product(ProductArgs p, uint32_t col_tiles) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    const Place where = place_of(blockIdx.x, col_tiles);
+    const Found f = find_tile(p, where.slot, kTileRows);
+    if (!f.any) return;
+    const uint32_t n0 = where.col * kTileCols;
+    const uint32_t wrows = (p.n + 127) / 128;
+    const Out<T> o{static_cast<T*>(p.out) + (uint64_t)f.row * p.out_stride + n0, p.out_stride, f.count, p.n - n0, p.wide};
+    if (f.count) {
+        const Tile t{p.a + (uint64_t)f.row * p.k,
+                     p.w + ((uint64_t)f.expert * p.n + n0) * p.k,
+                     p.a_scale + (uint64_t)f.row * p.a_scale_stride,
+                     p.w_scale + ((uint64_t)f.expert * wrows + n0 / 128) * p.w_scale_stride,
+                     f.count, p.n - n0, p.k, p.k, p.a_scale_stride, p.w_scale_stride, 0, p.k / 128};
+        if (f.count > 128) run_tile<Shape<2, 8, 8, 2, false>>(t, o, lds);
+        else if (f.count > 64) run_tile<Shape<2, 4, 8, 3, false>>(t, o, lds);
+        else if (f.count > 32) run_tile<Shape<1, 4, 4, 3, false>>(t, o, lds);
+        else run_tile<Shape<1, 2, 4, 4, false>>(t, o, lds);
+    }
+    // padding rows after the segment's last tile
+    if (f.count <= kTileRows && threadIdx.x < o.cols)
+        for (uint32_t q = f.count; q < f.end - f.row; ++q) o.out[q * o.stride + threadIdx.x] = (T)0.0f;
+}
+
+template <typename T>
+__global__ __launch_bounds__(256, 1) void weight_grad(WeightGradArgs p, uint32_t row_tiles, uint32_t col_tiles) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    const uint32_t padded = (row_tiles + 3) / 4 * 4;
+    const Place where = place_of(blockIdx.x, col_tiles);
+    const uint32_t e = where.slot / padded, i0 = where.slot % padded * kTileRows, j0 = where.col * kTileCols;
+    if (e >= p.experts || i0 >= p.n) return;
     uint32_t b0 = 0, b1 = p.rows / 128;
     if (p.offsets) {
         b0 = clamp_to(p.offsets[e], 0, p.rows) / 128;
         b1 = (clamp_to(p.offsets[e + 1], b0 * 128, p.rows) + 127) / 128;
     }
-    const Tile t{p.y + (uint64_t)i0 * p.rows + b0 * 128, p.y_scale + (uint64_t)i0 * p.scale_stride + b0,
-                 p.x + b0 * 128, p.x_scale + b0, p.n - i0, p.k, 0, b1 - b0, p.rows, p.rows, p.scale_stride,
-                 p.scale_stride, 0};
-    f32x4 acc[4];
-    wave_tile(t, j0, acc);
-    const uint32_t j = j0 + g * 4;
-    if (j >= p.k) return;
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i)
-        if (i0 + i * 16 + r < p.n)
-            store_out(p.dw, p.out_dtype, ((uint64_t)e * p.n + i0 + i * 16 + r) * p.k + j, acc[i], p.k - j);
+    const Tile t{p.y + (uint64_t)i0 * p.rows + b0 * 128,
+                 p.x + (uint64_t)j0 * p.rows + b0 * 128,
+                 p.y_scale + (uint64_t)i0 * p.scale_stride,
+                 p.x_scale + (uint64_t)j0 * p.scale_stride,
+                 p.n - i0, p.k - j0, p.rows, p.rows, p.scale_stride, p.scale_stride, b0, b1 - b0};
+    const Out<T> o{static_cast<T*>(p.dw) + ((uint64_t)e * p.n + i0) * p.k + j0, p.k, p.n - i0, p.k - j0, p.wide};
+    run_tile<Shape<2, 8, 8, 2, true>>(t, o, lds);
 }
+
+constexpr int kLdsProduct = Shape<1, 2, 4, 4, false>::kLds > Shape<2, 4, 8, 3, false>::kLds ? Shape<1, 2, 4, 4, false>::kLds
+                                                                                           : Shape<2, 4, 8, 3, false>::kLds;
+static_assert(kLdsProduct <= 160 * 1024 && Shape<2, 8, 8, 2, false>::kLds <= kLdsProduct &&
+                  Shape<1, 4, 4, 3, false>::kLds <= kLdsProduct,
+              "one LDS allocation serves every shape");
+constexpr int kLdsGrad = Shape<2, 8, 8, 2, true>::kLds;
+
+// More LDS than the default limit has to be asked for, once per device.
+template <typename K>
+void allow_lds(K kernel, int bytes) {
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+uint32_t runs_of_32(uint64_t tiles) { return (uint32_t)((tiles + 255) / 256 * 256); }
 
 }  // namespace
 
 void launch_product(const ProductArgs& a, hipStream_t stream) {
-    const uint32_t tiles = a.rows / 64 + (a.offsets ? a.experts : 1);
-    hipLaunchKernelGGL(product, dim3((a.n + 63) / 64, tiles), dim3(256), 0, stream, a);
+    const uint32_t cols = (a.n + kTileCols - 1) / kTileCols;
+    const uint64_t slots = (uint64_t)a.rows / kTileRows + (a.offsets ? a.experts : 1);
+    const dim3 grid(runs_of_32((slots + 3) / 4 * 4 * cols));
+    auto launch = [&](auto kernel) {
+        allow_lds(kernel, kLdsProduct);
+        hipLaunchKernelGGL(kernel, grid, dim3(256), kLdsProduct, stream, a, cols);
+    };
+    if (a.out_dtype == ZC_BF16) launch(product<__bf16>);
+    else if (a.out_dtype == ZC_FP16) launch(product<_Float16>);
+    else launch(product<float>);
 }
 
 void launch_weight_grad(const WeightGradArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL(weight_grad, dim3((a.k + 63) / 64, (a.n + 63) / 64, a.experts), dim3(256), 0, stream, a);
+    const uint32_t rows = (a.n + kTileRows - 1) / kTileRows, cols = (a.k + kTileCols - 1) / kTileCols;
+    const uint64_t slots = (uint64_t)a.experts * ((rows + 3) / 4 * 4);
+    const dim3 grid(runs_of_32(slots * cols));
+    auto launch = [&](auto kernel) {
+        allow_lds(kernel, kLdsGrad);
+        hipLaunchKernelGGL(kernel, grid, dim3(256), kLdsGrad, stream, a, rows, cols);
+    };
+    if (a.out_dtype == ZC_BF16) launch(weight_grad<__bf16>);
+    else if (a.out_dtype == ZC_FP16) launch(weight_grad<_Float16>);
+    else launch(weight_grad<float>);
 }
 
 }  // namespace zc
