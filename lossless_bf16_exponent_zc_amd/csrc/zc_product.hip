@@ -86,16 +86,17 @@ __device__ __forceinline__ Found find_tile(const ProductArgs& p, uint32_t index,
 }
 
 // The shape of a tile: 4 waves as WM x WN, each TM x TN instruction tiles of
-// 16 x 16; S stages of one block (128 bytes of every row) in LDS.  WROW: every
-// row of the weight side has its own scales (else one per 128 rows).
+// 16 x 16; S stages of one block (128 bytes of every row, and a word of four
+// scale bytes for each) in LDS.  WROW: every row of the weight side has its
+// own scales (else one per 128 rows).
 template <int WM_, int TM_, int TN_, int S_, bool WROW_>
 struct Shape {
     static constexpr int WM = WM_, WN = 4 / WM_, TM = TM_, TN = TN_, S = S_;
     static constexpr bool WROW = WROW_;
     static constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
     static constexpr int kScaleAt = (BM + BN) * 128;
-    static constexpr int kStage = kScaleAt + 1024 + (WROW ? 1024 : 0);
-    static constexpr int kLoads = (BM + BN) / 32 + 1 + (WROW ? 1 : 0);  // per wave and stage
+    static constexpr int kStage = kScaleAt + 2048;
+    static constexpr int kLoads = (BM + BN) / 32 + 2;  // per wave and stage
     static constexpr int kLds = S * kStage;
 };
 
@@ -131,12 +132,26 @@ __device__ __forceinline__ constexpr uint32_t weight_row(uint32_t i, uint32_t m)
     return (i >> 1) * 32 + (m >> 2) * 8 + (i & 1) * 4 + (m & 3);
 }
 
-// Where 16-byte piece c of a row lies: rows of 128 bytes all start in the same
-// bank, so the pieces turn with the row.  Token rows are read 16 in order,
-// weight rows as above; both orders see eight different pieces in any eight
-// neighbouring lanes.
-__device__ __forceinline__ uint32_t turn_a(uint32_t row) { return row & 7; }
-__device__ __forceinline__ uint32_t turn_w(uint32_t row) { return (row & 3) * 2 + ((row >> 3) & 1); }
+// Piece c (16 bytes) of a row lies at place c ^ turn(row) of its 128 bytes.
+// LDS has 16 such places side by side (64 banks), two rows; a 16-byte read
+// takes 16 lanes at a time, of which 8 have pieces one further than the other
+// 8 (lanes 0-3, 12-15 with 20-27, and so on).  With the row orders in use
+// (token rows as they come, weight rows as above) these turns give the 16
+// lanes 16 different places, for the pieces g and g + 4 of lane group g.
+__device__ __forceinline__ uint32_t turn_a(uint32_t row) { return (row >> 1) & 7; }
+__device__ __forceinline__ uint32_t turn_w(uint32_t row) { return ((row >> 1) & 1) + ((row >> 3) & 3) * 2; }
+
+// acc += the product of 16 weight rows and 16 token rows over one block, with
+// both scales (low bytes).  Written as the instruction itself, so that the
+// accumulator stays where it is: left to choose, the compiler moves the 256
+// accumulators of a wave around between blocks (50 moves a block).  s_nop
+// stands for the wait a scale just computed needs; results are read only
+// after the loop, which waits for them.
+__device__ __forceinline__ void multiply(f32x4& acc, const i32x8& w, const i32x8& a, uint32_t sw, uint32_t sa) {
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+                 : "+a"(acc)
+                 : "v"(w), "v"(a), "v"(sw), "v"(sa));
+}
 
 template <typename SH>
 __device__ __forceinline__ void tile_product(const Tile& t, uint8_t* lds, f32x4 (&acc)[SH::TM][SH::TN]) {
@@ -155,83 +170,108 @@ __device__ __forceinline__ void tile_product(const Tile& t, uint8_t* lds, f32x4 
         const uint32_t row = (wave * NW + i) * 8 + (lane >> 3);
         at_w[i] = (row < t.w_rows ? row : t.w_rows - 1) * t.w_stride + (((lane & 7) ^ turn_w(row)) << 4);
     }
-    const uint32_t srow = wave * 64 + lane;
-    const uint32_t at_as = (srow < t.a_rows && srow < SH::BM ? srow : t.a_rows - 1 < SH::BM ? t.a_rows - 1 : 0) * t.as_stride;
-    const uint32_t at_ws = (srow < t.w_rows ? srow : t.w_rows - 1) * t.ws_stride;
+    const uint32_t srow = wave * 64 + lane;  // whose scales the lane brings
+    const uint32_t last_a = t.a_rows < SH::BM ? t.a_rows - 1 : SH::BM - 1;
+    const uint32_t at_as = (srow < last_a ? srow : last_a) * t.as_stride;
+    const uint32_t wrow = srow < t.w_rows ? srow : t.w_rows - 1;
+    const uint32_t at_ws = (SH::WROW ? wrow : wrow >> 7) * t.ws_stride;
     const __amdgpu_buffer_rsrc_t ra = buffer(t.a), rw = buffer(t.w), ras = buffer(t.as), rws = buffer(t.ws);
 
-    auto load = [&](uint32_t block, uint32_t slot) {
-        // blocks past the last are loaded again, so that the number of loads
-        // in flight does not depend on where the loop stands
-        block = block < t.blocks ? block : t.blocks - 1;
-        uint8_t* base = lds + slot * SH::kStage;
-#pragma unroll
-        for (int i = 0; i < NA; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(base + (wave * NA + i) * 1024), 16, at_a[i],
-                                                     block * 128, 0, 0);
-#pragma unroll
-        for (int i = 0; i < NW; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(base + SH::BM * 128 + (wave * NW + i) * 1024), 16,
-                                                     at_w[i], block * 128, 0, 0);
+    // the n-th of a wave's loads of a block; blocks past the last are loaded
+    // again, so that the loads in flight do not depend on where the loop stands
+    auto load_one = [&](int n, uint32_t block, uint8_t* base) {
         const uint32_t word = (t.first_block + block) & ~3u;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ras, (lds_void*)(base + SH::kScaleAt + wave * 256), 4, at_as, word, 0, 0);
-        if (SH::WROW)
+        if (n < NA)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(base + (wave * NA + n) * 1024), 16, at_a[n],
+                                                     block * 128, 0, 0);
+        else if (n < NA + NW)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(base + SH::BM * 128 + (wave * NW + n - NA) * 1024), 16,
+                                                     at_w[n - NA], block * 128, 0, 0);
+        else if (n == NA + NW)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ras, (lds_void*)(base + SH::kScaleAt + wave * 256), 4, at_as, word, 0, 0);
+        else if (n == NA + NW + 1)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rws, (lds_void*)(base + SH::kScaleAt + 1024 + wave * 256), 4, at_ws,
                                                      word, 0, 0);
     };
+    auto clamped = [&](uint32_t block) { return block < t.blocks ? block : t.blocks - 1; };
 
-    // scales of the weight side where 128 rows share them: the wave's 64 (or
-    // 128) rows have one scale row; a lane keeps 4 of its bytes
     const uint32_t wave_a = (wave / SH::WN) * SH::TM * 16, wave_w = (wave % SH::WN) * SH::TN * 16;
-    uint32_t ws_words = 0;
-    const uint8_t* ws_row = t.ws + (uint64_t)(wave_w < t.w_rows ? wave_w >> 7 : 0) * t.ws_stride;
+    // where a lane's two pieces of a row lie (pieces g and g + 4)
+    const uint32_t a_lo = (wave_a + r) * 128 + ((g ^ turn_a(r)) << 4), a_hi = a_lo ^ 64;
+    const uint32_t w_lo = SH::BM * 128 + (wave_w + weight_row(0, r)) * 128 + ((g ^ turn_w(weight_row(0, r))) << 4);
+    const uint32_t w_hi = w_lo ^ 64;
+    const uint32_t a_scale = SH::kScaleAt + (wave_a + r) * 4;
+    const uint32_t w_scale = SH::kScaleAt + 1024 + (SH::WROW ? wave_w + weight_row(0, r) : wave_w) * 4;
 
-    for (int s = 0; s < SH::S - 1; ++s) load(s, s);
-    uint32_t slot = 0;
-    // where a lane's two pieces of a row lie (pieces 2g and 2g + 1)
-    const uint32_t ta = turn_a(r), tw0 = turn_w(weight_row(0, r)), tw1 = turn_w(weight_row(1, r));
-    const uint32_t la = (wave_a + r) * 128;
-    const uint32_t a_lo = la + (((2 * g) ^ ta) << 4), a_hi = la + (((2 * g + 1) ^ ta) << 4);
-    const uint32_t lw0 = SH::BM * 128 + (wave_w + weight_row(0, r)) * 128, lw1 = lw0 + 4 * 128;
-    const uint32_t w0_lo = lw0 + (((2 * g) ^ tw0) << 4), w0_hi = lw0 + (((2 * g + 1) ^ tw0) << 4);
-    const uint32_t w1_lo = lw1 + (((2 * g) ^ tw1) << 4), w1_hi = lw1 + (((2 * g + 1) ^ tw1) << 4);
+    struct Side {     // 16 rows of one block
+        i32x8 v;
+        uint32_t s;   // four blocks' scale bytes
+    };
+    auto read_a = [&](const uint8_t* base, int j) {
+        return Side{two(*(const xu32x4*)(base + a_lo + j * 2048), *(const xu32x4*)(base + a_hi + j * 2048)),
+                    *(const uint32_t*)(base + a_scale + j * 64)};
+    };
+    auto read_w = [&](const uint8_t* base, int i, Side& x) {
+        const uint32_t row = (i >> 1) * 32 + (i & 1) * 4;
+        x.v = two(*(const xu32x4*)(base + w_lo + row * 128), *(const xu32x4*)(base + w_hi + row * 128));
+        if (SH::WROW || i == 0) x.s = *(const uint32_t*)(base + w_scale + row * 4);
+    };
+
+    uint8_t* base = lds;
+    for (int s = 0; s < SH::S; ++s) {
+#pragma unroll
+        for (int n = 0; n < SH::kLoads; ++n) load_one(n, clamped(s), lds + s * SH::kStage);
+    }
+    wait_loads_and_barrier<(SH::S - 1) * SH::kLoads>();
+    Side w[SH::TN], first = read_a(base, 0);
+#pragma unroll
+    for (int i = 0; i < SH::TN; ++i) read_w(base, i, w[i]);
+
+    // One block a turn.  The weight side and the first token tile are in
+    // registers, further token tiles are read two ahead.  Once the last is
+    // read, and every wave is that far, the stage is free: while the unit
+    // works on the last two token tiles, the block S later is loaded there and
+    // the next block's weight side replaces this one's, piece by piece.
     for (uint32_t b = 0; b < t.blocks; ++b) {
-        // the loads of this block are there, and every wave is done with the
-        // stage that the next load overwrites
-        wait_loads_and_barrier<(SH::S - 2) * SH::kLoads>();
-        const uint32_t fill = slot == 0 ? SH::S - 1 : slot - 1;
-        load(b + SH::S - 1, fill);
-        const uint8_t* base = lds + slot * SH::kStage;
-        const uint32_t sb = t.first_block + b, shift = (sb & 3) * 8;
-        int sw_all = 0;
-        if (!SH::WROW) {
-            const uint32_t word = sb >> 2;
-            if (b == 0 || (sb & 255) == 0)
-                ws_words = (word & ~63u) * 4 + lane * 4 < t.ws_stride
-                               ? reinterpret_cast<const uint32_t*>(ws_row)[(word & ~63u) + lane]
-                               : 0;
-            sw_all = (int)((uint32_t)__builtin_amdgcn_readlane((int)ws_words, word & 63) >> shift);
+        const uint32_t shift = ((t.first_block + b) & 3) * 8;
+        uint32_t sw[SH::TN], sa[3];
+        Side a[3];
+        a[0] = first;
+        a[1] = read_a(base, 1);
+#pragma unroll
+        for (int i = 0; i < SH::TN; ++i) sw[i] = SH::WROW || i == 0 ? w[i].s >> shift : sw[0];
+        sa[0] = a[0].s >> shift;
+#pragma unroll
+        for (int j = 0; j < SH::TM - 2; ++j) {
+            a[(j + 2) % 3] = read_a(base, j + 2);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < SH::TN; ++i) multiply(acc[j][i], w[i].v, a[j % 3].v, sw[i], sa[j % 3]);
+            sa[(j + 1) % 3] = a[(j + 1) % 3].s >> shift;
+            __builtin_amdgcn_sched_barrier(0);
         }
-        i32x8 wv[SH::TN];
-        int sw[SH::TN];
+        constexpr int J = SH::TM - 2, j0 = J % 3, j1 = (J + 1) % 3;
+        if (J == 0) sa[j0] = a[j0].s >> shift;
+        sa[j1] = a[j1].s >> shift;
+        wait_loads_and_barrier<(SH::S - 2) * SH::kLoads>();
+        __builtin_amdgcn_sched_barrier(0);
+        uint8_t* const free = base;
+        const uint32_t ahead = clamped(b + SH::S);
+        base = base == lds + (SH::S - 1) * SH::kStage ? lds : base + SH::kStage;
+        first = read_a(base, 0);
+        constexpr int kEach = (SH::kLoads + SH::TN - 1) / SH::TN;
 #pragma unroll
         for (int i = 0; i < SH::TN; ++i) {
-            const uint32_t step = (i >> 1) * 32 * 128;
-            wv[i] = i & 1 ? two(*(const xu32x4*)(base + w1_lo + step), *(const xu32x4*)(base + w1_hi + step))
-                          : two(*(const xu32x4*)(base + w0_lo + step), *(const xu32x4*)(base + w0_hi + step));
-            sw[i] = SH::WROW ? (int)(*(const uint32_t*)(base + SH::kScaleAt + 1024 + (wave_w + weight_row(i, r)) * 4) >> shift)
-                             : sw_all;
-        }
+            multiply(acc[J][i], w[i].v, a[j0].v, sw[i], sa[j0]);
+            multiply(acc[J + 1][i], w[i].v, a[j1].v, sw[i], sa[j1]);
+            read_w(base, i, w[i]);
 #pragma unroll
-        for (int j = 0; j < SH::TM; ++j) {
-            const i32x8 av = two(*(const xu32x4*)(base + a_lo + j * 2048), *(const xu32x4*)(base + a_hi + j * 2048));
-            const int sa = (int)(*(const uint32_t*)(base + SH::kScaleAt + (wave_a + j * 16 + r) * 4) >> shift);
-#pragma unroll
-            for (int i = 0; i < SH::TN; ++i)
-                acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv[i], av, acc[j][i], 0, 0, 0, sw[i], 0, sa);
+            for (int n = i * kEach; n < (i + 1) * kEach; ++n) load_one(n, ahead, free);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        slot = slot == SH::S - 1 ? 0 : slot + 1;
     }
+    // the last results are written before anything reads them
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
     // no load may still write LDS when the next tile or another workgroup has it
     wait_loads_and_barrier<0>();
 }
