@@ -33,56 +33,136 @@ struct Tile {
     uint32_t blocks;
 };
 
-// Expert and first row of the `index`-th tile of `m` rows, over all experts'
-// segments in order.  Every wave finds it for itself: a lane has one expert.
-struct Found {
-    uint32_t expert, row, count, end;  // count: rows of the segment from `row`; end: where padding ends
-    bool any;
-};
+constexpr uint32_t kTileRows = 256, kTileCols = 256;
+constexpr uint32_t kShort = 128;  // most rows of a short tile
 
 __device__ __forceinline__ uint32_t clamp_to(int32_t v, uint32_t lo, uint32_t hi) {
     return v < (int32_t)lo ? lo : (uint32_t)v > hi ? hi : (uint32_t)v;
 }
 
-__device__ __forceinline__ Found find_tile(const ProductArgs& p, uint32_t index, uint32_t m) {
+// The rows of one tile: `count` of expert's segment from `row` on (there may
+// be more than a tile's), padding after them up to `end`.
+struct Found {
+    uint32_t expert, row, count, end, col;
+    uint32_t any;
+};
+
+// Workgroup -> rows and columns.  A segment is cut into slots of 256 rows; a
+// slot of more than 128 rows is long, what is left is short.  Long slots keep
+// the matrix unit busy and short ones the memory, so a launch of many tiles
+// gives every XCD both in turn (kRuns): its CUs take tiles in runs of 32, 4 slots
+// by 8 columns of one kind, so that what they read at one time is 4 + 8 strips
+// shared through the XCD's L2, and runs of long and short slots alternate in
+// proportion.
+enum Order { kInOrder, kRuns };
+
+struct Slots {
+    uint32_t slot, col;
+    bool is_long, any;
+};
+
+__device__ __forceinline__ Slots slot_of(uint32_t index, uint32_t cols, uint32_t nlong, uint32_t nshort, Order order) {
+    if (order == kInOrder) {
+        const uint32_t s = index / cols;
+        const bool l = s < nlong;
+        return Slots{l ? s : s - nlong, index % cols, l, s < nlong + nshort};
+    }
+    const uint32_t xcd = index & 7, n = index >> 3, run = n >> 5;
+    const uint32_t runs_l = ((nlong + 3) / 4 * cols + 7) / 8, runs_s = ((nshort + 3) / 4 * cols + 7) / 8;
+    const uint32_t mine_l = (runs_l + 7 - xcd) / 8, mine_s = (runs_s + 7 - xcd) / 8, mine = mine_l + mine_s;
+    if (run >= mine) return Slots{0, 0, false, false};
+    uint32_t before, upto;  // long runs before this one, and with it
+    if (mine < 65536) {
+        const uint32_t phase = xcd * mine / 8;
+        before = (run * mine_l + phase) / mine;
+        upto = ((run + 1) * mine_l + phase) / mine;
+    } else {
+        before = run < mine_l ? run : mine_l;
+        upto = run < mine_l ? run + 1 : mine_l;
+    }
+    const bool l = upto > before;
+    const uint32_t tile = ((l ? before : run - before) * 8 + xcd) * 32 + (n & 31);
+    const uint32_t group = tile / (4 * cols), in = tile % (4 * cols), slot = group * 4 + (in & 3);
+    return Slots{slot, in >> 2, l, slot < (l ? nlong : nshort)};
+}
+
+// Long and short slots of a segment.
+__device__ __forceinline__ void slots_in(uint32_t count, bool padding, uint32_t& nlong, uint32_t& nshort) {
+    const uint32_t rest = count % kTileRows;
+    nlong = count / kTileRows + (rest > kShort ? 1 : 0);
+    nshort = rest && rest <= kShort ? 1 : 0;
+    if (!count && padding) nshort = 1;  // a segment of padding only
+}
+
+// Every thread looks at four experts; `shared` has room for 16 words.
+__device__ __forceinline__ Found find_tile(const ProductArgs& p, uint32_t index, uint32_t cols, Order order,
+                                           uint32_t* shared) {
     if (!p.offsets) {
-        const uint64_t r = (uint64_t)index * m;
-        const bool any = r < p.rows;
-        return Found{0, (uint32_t)r, any ? p.rows - (uint32_t)r : 0, p.rows, any};
+        uint32_t nl, ns;
+        slots_in(p.rows, false, nl, ns);
+        const Slots s = slot_of(index, cols, nl, ns, order);
+        const uint32_t row = (s.is_long ? s.slot : nl) * kTileRows;
+        return Found{0, row, p.rows - row, p.rows, s.col, s.any};
     }
-    const uint32_t lane = __lane_id();
-    uint32_t before = 0;
-    for (uint32_t e0 = 0; e0 < p.experts; e0 += 64) {
-        const uint32_t e = e0 + lane;
-        uint32_t lo = 0, count = 0, end = 0;
-        if (e < p.experts) {
-            lo = clamp_to(p.offsets[e], 0, p.rows);
-            end = clamp_to(p.offsets[e + 1], lo, p.rows);
-            count = p.counts ? clamp_to(p.counts[e], 0, end - lo) : end - lo;
+    const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x >> 6);
+    uint32_t lo[4], count[4], end[4], nl[4], ns[4], sum_l = 0, sum_s = 0;
+    const uint32_t e0 = threadIdx.x * 4;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        lo[q] = count[q] = end[q] = nl[q] = ns[q] = 0;
+        if (e0 + q < p.experts) {
+            const int32_t o0 = p.offsets[e0 + q], o1 = p.offsets[e0 + q + 1];
+            const int32_t c = p.counts ? p.counts[e0 + q] : 0x7FFFFFFF;
+            lo[q] = clamp_to(o0, 0, p.rows);
+            end[q] = clamp_to(o1, lo[q], p.rows);
+            count[q] = clamp_to(c, 0, end[q] - lo[q]);
+            slots_in(count[q], end[q] > lo[q], nl[q], ns[q]);
         }
-        uint32_t tiles = (count + m - 1) / m;
-        if (end > lo && tiles == 0) tiles = 1;  // a segment of padding only
-        uint32_t sum = tiles;
-        for (uint32_t d = 1; d < 64; d <<= 1) {
-            const uint32_t t = __shfl_up(sum, d);
-            if (lane >= d) sum += t;
-        }
-        const uint64_t past = __ballot(before + sum > index);
-        if (past) {
-            const uint32_t at = __ffsll((unsigned long long)past) - 1;
-            const uint32_t in = uniform(index - before - (uint32_t)__shfl((int)(sum - tiles), at));
-            Found f;
-            f.expert = uniform(e0 + at);
-            const uint32_t l = uniform(__shfl((int)lo, at)), c = uniform(__shfl((int)count, at));
-            f.end = uniform(__shfl((int)end, at));
-            f.row = l + in * m;
-            f.count = c > in * m ? c - in * m : 0;
-            f.any = true;
-            return f;
-        }
-        before += uniform(__shfl((int)sum, 63));
+        sum_l += nl[q];
+        sum_s += ns[q];
     }
-    return Found{0, 0, 0, 0, false};
+    uint32_t run_l = sum_l, run_s = sum_s;
+    for (uint32_t d = 1; d < 64; d <<= 1) {
+        const uint32_t tl = __shfl_up(run_l, d), ts = __shfl_up(run_s, d);
+        if (lane >= d) {
+            run_l += tl;
+            run_s += ts;
+        }
+    }
+    if (lane == 63) {
+        shared[wave * 2] = run_l;
+        shared[wave * 2 + 1] = run_s;
+    }
+    __syncthreads();
+    uint32_t before_l = run_l - sum_l, before_s = run_s - sum_s, all_l = 0, all_s = 0;
+#pragma unroll
+    for (uint32_t v = 0; v < 4; ++v) {
+        if (v < wave) {
+            before_l += shared[v * 2];
+            before_s += shared[v * 2 + 1];
+        }
+        all_l += shared[v * 2];
+        all_s += shared[v * 2 + 1];
+    }
+    const Slots s = slot_of(index, cols, uniform(all_l), uniform(all_s), order);
+    if (!s.any) return Found{0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t in = s.slot - (s.is_long ? before_l : before_s);
+        if (in < (s.is_long ? nl[q] : ns[q])) {  // one thread of the workgroup
+            const uint32_t skip = (s.is_long ? in : nl[q]) * kTileRows;
+            shared[8] = e0 + q;
+            shared[9] = lo[q] + skip;
+            shared[10] = count[q] - skip;
+            shared[11] = end[q];
+        }
+        before_l += nl[q];
+        before_s += ns[q];
+    }
+    __syncthreads();
+    const Found f{uniform(shared[8]), uniform(shared[9]), uniform(shared[10]), uniform(shared[11]), s.col, 1};
+    __syncthreads();  // the tile's first loads may write where this was
+    return f;
 }
 
 // The shape of a tile: 4 waves as WM x WN, each TM x TN instruction tiles of
@@ -367,8 +447,6 @@ __device__ __forceinline__ void run_tile(const Tile& t, const Out<T>& o, uint8_t
 #endif
 }
 
-constexpr uint32_t kTileRows = 256, kTileCols = 256;
-
 // Workgroup -> (slot of token rows, tile of columns).  Neighbouring workgroup
 // indexes go to different XCDs; the eight XCDs take turns at runs of 32 tiles,
 // 4 slots by 8 columns, so that what an XCD's 32 CUs read at one time is 4 + 8
@@ -387,12 +465,11 @@ __device__ __forceinline__ Place place_of(uint32_t index, uint32_t col_tiles) {
 // it has, so that short segments do not pay for 256 rows and run beside long
 // ones.
 template <typename T>
-__global__ __launch_bounds__(256, 1) void product(ProductArgs p, uint32_t col_tiles) {
+__global__ __launch_bounds__(256, 1) void product(ProductArgs p, uint32_t col_tiles, Order order) {
     extern __shared__ __align__(16) uint8_t lds[];
-    const Place where = place_of(blockIdx.x, col_tiles);
-    const Found f = find_tile(p, where.slot, kTileRows);
+    const Found f = find_tile(p, blockIdx.x, col_tiles, order, reinterpret_cast<uint32_t*>(lds));
     if (!f.any) return;
-    const uint32_t n0 = where.col * kTileCols;
+    const uint32_t n0 = f.col * kTileCols;
     const uint32_t wrows = (p.n + 127) / 128;
     const Out<T> o{static_cast<T*>(p.out) + (uint64_t)f.row * p.out_stride + n0, p.out_stride, f.count, p.n - n0, p.wide};
     if (f.count) {
@@ -452,10 +529,13 @@ uint32_t runs_of_32(uint64_t tiles) { return (uint32_t)((tiles + 255) / 256 * 25
 void launch_product(const ProductArgs& a, hipStream_t stream) {
     const uint32_t cols = (a.n + kTileCols - 1) / kTileCols;
     const uint64_t slots = (uint64_t)a.rows / kTileRows + (a.offsets ? a.experts : 1);
-    const dim3 grid(runs_of_32((slots + 3) / 4 * 4 * cols));
+    const Order order = slots * cols > 512 ? kRuns : kInOrder;
+    // runs: each kind's slots rounded up to 4, its tiles to runs of 32, its
+    // runs to the 8 XCDs
+    const dim3 grid(order == kRuns ? (uint32_t)((((slots + 6) / 4 * cols + 14) / 8 + 14) / 8 * 256) : (uint32_t)(slots * cols));
     auto launch = [&](auto kernel) {
         allow_lds(kernel, kLdsProduct);
-        hipLaunchKernelGGL(kernel, grid, dim3(256), kLdsProduct, stream, a, cols);
+        hipLaunchKernelGGL(kernel, grid, dim3(256), kLdsProduct, stream, a, cols, order);
     };
     if (a.out_dtype == ZC_BF16) launch(product<__bf16>);
     else if (a.out_dtype == ZC_FP16) launch(product<_Float16>);
