@@ -33,8 +33,20 @@ struct Tile {
     uint32_t blocks;
 };
 
-constexpr uint32_t kTileRows = 256, kTileCols = 256;
-constexpr uint32_t kShort = 128;  // most rows of a short tile
+// How segments are cut: into slots of kRows rows; what is left is a slot of its
+// own, a short one up to kShort rows.
+struct WideCut {
+    static constexpr uint32_t kRows = 256, kCols = 256, kShort = 128;
+};
+struct MidCut {
+    static constexpr uint32_t kRows = 128, kCols = 128, kShort = 0;
+};
+struct SmallCut {
+    static constexpr uint32_t kRows = 64, kCols = 64, kShort = 0;
+};
+struct FewCut {
+    static constexpr uint32_t kRows = 64, kCols = 32, kShort = 0;
+};
 
 __device__ __forceinline__ uint32_t clamp_to(int32_t v, uint32_t lo, uint32_t hi) {
     return v < (int32_t)lo ? lo : (uint32_t)v > hi ? hi : (uint32_t)v;
@@ -47,13 +59,13 @@ struct Found {
     uint32_t any;
 };
 
-// Workgroup -> rows and columns.  A segment is cut into slots of 256 rows; a
-// slot of more than 128 rows is long, what is left is short.  Long slots keep
-// the matrix unit busy and short ones the memory, so a launch of many tiles
-// gives every XCD both in turn (kRuns): its CUs take tiles in runs of 32, 4 slots
-// by 8 columns of one kind, so that what they read at one time is 4 + 8 strips
-// shared through the XCD's L2, and runs of long and short slots alternate in
-// proportion.
+// Workgroup -> rows and columns.  Long slots keep the matrix unit busy and
+// short ones the memory, so a launch of many tiles gives every XCD both in
+// turn (kRuns): its CUs take tiles in runs of 32, 4 slots by 8 columns of one
+// kind, so that what they read at one time is 4 + 8 strips shared through the
+// XCD's L2, and runs of long and short slots alternate in proportion (65,536
+// rows, Zipf counts on 256 experts, n 4096, k 7168: 2.57 ms; kinds as the
+// experts come: 2.64).
 enum Order { kInOrder, kRuns };
 
 struct Slots {
@@ -87,21 +99,23 @@ __device__ __forceinline__ Slots slot_of(uint32_t index, uint32_t cols, uint32_t
 }
 
 // Long and short slots of a segment.
+template <typename Cut>
 __device__ __forceinline__ void slots_in(uint32_t count, bool padding, uint32_t& nlong, uint32_t& nshort) {
-    const uint32_t rest = count % kTileRows;
-    nlong = count / kTileRows + (rest > kShort ? 1 : 0);
-    nshort = rest && rest <= kShort ? 1 : 0;
+    const uint32_t rest = count % Cut::kRows;
+    nlong = count / Cut::kRows + (rest > Cut::kShort ? 1 : 0);
+    nshort = rest && rest <= Cut::kShort ? 1 : 0;
     if (!count && padding) nshort = 1;  // a segment of padding only
 }
 
 // Every thread looks at four experts; `shared` has room for 16 words.
+template <typename Cut>
 __device__ __forceinline__ Found find_tile(const ProductArgs& p, uint32_t index, uint32_t cols, Order order,
                                            uint32_t* shared) {
     if (!p.offsets) {
         uint32_t nl, ns;
-        slots_in(p.rows, false, nl, ns);
+        slots_in<Cut>(p.rows, false, nl, ns);
         const Slots s = slot_of(index, cols, nl, ns, order);
-        const uint32_t row = (s.is_long ? s.slot : nl) * kTileRows;
+        const uint32_t row = (s.is_long ? s.slot : nl) * Cut::kRows;
         return Found{0, row, p.rows - row, p.rows, s.col, s.any};
     }
     const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x >> 6);
@@ -116,7 +130,7 @@ __device__ __forceinline__ Found find_tile(const ProductArgs& p, uint32_t index,
             lo[q] = clamp_to(o0, 0, p.rows);
             end[q] = clamp_to(o1, lo[q], p.rows);
             count[q] = clamp_to(c, 0, end[q] - lo[q]);
-            slots_in(count[q], end[q] > lo[q], nl[q], ns[q]);
+            slots_in<Cut>(count[q], end[q] > lo[q], nl[q], ns[q]);
         }
         sum_l += nl[q];
         sum_s += ns[q];
@@ -150,7 +164,7 @@ __device__ __forceinline__ Found find_tile(const ProductArgs& p, uint32_t index,
     for (int q = 0; q < 4; ++q) {
         const uint32_t in = s.slot - (s.is_long ? before_l : before_s);
         if (in < (s.is_long ? nl[q] : ns[q])) {  // one thread of the workgroup
-            const uint32_t skip = (s.is_long ? in : nl[q]) * kTileRows;
+            const uint32_t skip = (s.is_long ? in : nl[q]) * Cut::kRows;
             shared[8] = e0 + q;
             shared[9] = lo[q] + skip;
             shared[10] = count[q] - skip;
@@ -447,6 +461,8 @@ __device__ __forceinline__ void run_tile(const Tile& t, const Out<T>& o, uint8_t
 #endif
 }
 
+constexpr uint32_t kTileRows = 256, kTileCols = 256;
+
 // Workgroup -> (slot of token rows, tile of columns).  Neighbouring workgroup
 // indexes go to different XCDs; the eight XCDs take turns at runs of 32 tiles,
 // 4 slots by 8 columns, so that what an XCD's 32 CUs read at one time is 4 + 8
@@ -461,15 +477,24 @@ __device__ __forceinline__ Place place_of(uint32_t index, uint32_t col_tiles) {
     return Place{group * 4 + (in & 3), in >> 2};
 }
 
-// One kernel for every length of a segment: a tile takes the shape of the rows
-// it has, so that short segments do not pay for 256 rows and run beside long
-// ones.
+// Padding rows after the segment's last slot; cols of them from o.
 template <typename T>
+__device__ __forceinline__ void zero_padding(const Out<T>& o, const Found& f, uint32_t rows, uint32_t cols) {
+    const uint32_t c = threadIdx.x % cols;
+    if (f.count <= rows && c < o.cols)
+        for (uint32_t q = f.count + threadIdx.x / cols; q < f.end - f.row; q += 256 / cols)
+            o.out[q * o.stride + c] = (T)0.0f;
+}
+
+// One kernel for every length of a segment: a tile takes the shape of the rows
+// it has, so that short segments do not pay for a whole slot and run beside
+// long ones.
+template <typename T, typename Cut>
 __global__ __launch_bounds__(256, 1) void product(ProductArgs p, uint32_t col_tiles, Order order) {
     extern __shared__ __align__(16) uint8_t lds[];
-    const Found f = find_tile(p, blockIdx.x, col_tiles, order, reinterpret_cast<uint32_t*>(lds));
+    const Found f = find_tile<Cut>(p, blockIdx.x, col_tiles, order, reinterpret_cast<uint32_t*>(lds));
     if (!f.any) return;
-    const uint32_t n0 = f.col * kTileCols;
+    const uint32_t n0 = f.col * Cut::kCols;
     const uint32_t wrows = (p.n + 127) / 128;
     const Out<T> o{static_cast<T*>(p.out) + (uint64_t)f.row * p.out_stride + n0, p.out_stride, f.count, p.n - n0, p.wide};
     if (f.count) {
@@ -478,14 +503,111 @@ __global__ __launch_bounds__(256, 1) void product(ProductArgs p, uint32_t col_ti
                      p.a_scale + (uint64_t)f.row * p.a_scale_stride,
                      p.w_scale + ((uint64_t)f.expert * wrows + n0 / 128) * p.w_scale_stride,
                      f.count, p.n - n0, p.k, p.k, p.a_scale_stride, p.w_scale_stride, 0, p.k / 128};
-        if (f.count > 128) run_tile<Shape<2, 8, 8, 2, false>>(t, o, lds);
-        else if (f.count > 64) run_tile<Shape<2, 4, 8, 3, false>>(t, o, lds);
-        else if (f.count > 32) run_tile<Shape<1, 4, 4, 3, false>>(t, o, lds);
-        else run_tile<Shape<1, 2, 4, 4, false>>(t, o, lds);
+        if constexpr (Cut::kRows == 256) {
+            if (f.count > 128) run_tile<Shape<2, 8, 8, 2, false>>(t, o, lds);
+            else if (f.count > 64) run_tile<Shape<2, 4, 8, 3, false>>(t, o, lds);
+            else if (f.count > 32) run_tile<Shape<1, 4, 4, 3, false>>(t, o, lds);
+            else run_tile<Shape<1, 2, 4, 4, false>>(t, o, lds);
+        } else if constexpr (Cut::kRows == 64) {
+            run_tile<Shape<2, 2, 2, 8, false>>(t, o, lds);
+        } else {
+            if (f.count > 64) run_tile<Shape<2, 4, 4, 4, false>>(t, o, lds);
+            else run_tile<Shape<1, 4, 2, 4, false>>(t, o, lds);
+        }
     }
-    // padding rows after the segment's last tile
-    if (f.count <= kTileRows && threadIdx.x < o.cols)
-        for (uint32_t q = f.count; q < f.end - f.row; ++q) o.out[q * o.stride + threadIdx.x] = (T)0.0f;
+    zero_padding(o, f, Cut::kRows, Cut::kCols);
+}
+
+// Few rows, or few tiles: 32 columns of up to 16 * TM rows per workgroup, the
+// four waves taking every fourth block, straight from memory to the unit, and
+// adding up in LDS in their order.  Nothing here is used twice but the rows,
+// so staging would only hold loads back; narrow tiles put the weights of a few
+// experts on all CUs (one CU draws about 50 GB/s from memory, however many
+// loads it has in flight).
+template <typename T, int TM>
+__device__ __forceinline__ void few_tile(const ProductArgs& p, const Found& f, uint32_t n0, const Out<T>& o, float* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    const uint32_t left = p.n - n0, blocks = p.k / 128;
+    const uint8_t* w[2];
+    const uint8_t* a[TM];
+    const uint8_t* as[TM];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t row = weight_row(i, r);
+        w[i] = p.w + ((uint64_t)f.expert * p.n + n0 + (row < left ? row : left - 1)) * p.k + wave * 128 + g * 16;
+    }
+    const uint8_t* ws = p.w_scale + ((uint64_t)f.expert * ((p.n + 127) / 128) + n0 / 128) * p.w_scale_stride + wave;
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+        const uint32_t row = j * 16 + r;
+        const uint64_t at = f.row + (row < f.count ? row : f.count - 1);
+        a[j] = p.a + at * p.k + wave * 128 + g * 16;
+        as[j] = p.a_scale + at * p.a_scale_stride + wave;
+    }
+    f32x4 acc[TM][2];
+#pragma unroll
+    for (int j = 0; j < TM; ++j) acc[j][0] = acc[j][1] = f32x4{0, 0, 0, 0};
+    auto piece = [](const uint8_t* q) { return two(*(const xu32x4*)q, *(const xu32x4*)(q + 64)); };
+    constexpr int U = TM == 1 ? 8 : TM == 2 ? 4 : 2;
+#pragma unroll U
+    for (uint32_t b = wave; b < blocks; b += 4) {
+        const uint32_t at = (b >> 2) * 512, sat = b & ~3u;
+        const i32x8 w0 = piece(w[0] + at), w1 = piece(w[1] + at);
+        const int sw = ws[sat];
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+            const i32x8 v = piece(a[j] + at);
+            const int sa = as[j][sat];
+            acc[j][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w0, v, acc[j][0], 0, 0, 0, sw, 0, sa);
+            acc[j][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w1, v, acc[j][1], 0, 0, 0, sw, 0, sa);
+        }
+    }
+    constexpr uint32_t kPitch = 36;
+    float* mine = lds + wave * TM * 16 * kPitch;
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<f32x4*>(mine + (j * 16 + r) * kPitch + g * 8 + i * 4) = acc[j][i];
+    __syncthreads();
+    const uint32_t c = (threadIdx.x & 15) * 2;
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+        const uint32_t row = j * 16 + (threadIdx.x >> 4);
+        float v[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v[h] += lds[(q * TM * 16 + row) * kPitch + c + h];
+        if (row < f.count) {
+            T* out = o.out + row * o.stride + c;
+            if (o.wide && c + 1 < o.cols) {
+                struct alignas(2 * sizeof(T)) Two {
+                    T v[2];
+                };
+                *reinterpret_cast<Two*>(out) = Two{{(T)v[0], (T)v[1]}};
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (c + h < o.cols) out[h] = (T)v[h];
+            }
+        }
+    }
+#endif
+}
+
+template <typename T>
+__global__ __launch_bounds__(256, 2) void product_few(ProductArgs p, uint32_t col_tiles) {
+    __shared__ __align__(16) float lds[4 * 64 * 36];
+    const Found f = find_tile<FewCut>(p, blockIdx.x, col_tiles, kInOrder, reinterpret_cast<uint32_t*>(lds));
+    if (!f.any) return;
+    const uint32_t n0 = f.col * FewCut::kCols;
+    const Out<T> o{static_cast<T*>(p.out) + (uint64_t)f.row * p.out_stride + n0, p.out_stride, f.count, p.n - n0, p.wide};
+    if (f.count > 32) few_tile<T, 4>(p, f, n0, o, lds);
+    else if (f.count > 16) few_tile<T, 2>(p, f, n0, o, lds);
+    else if (f.count) few_tile<T, 1>(p, f, n0, o, lds);
+    zero_padding(o, f, FewCut::kRows, FewCut::kCols);
 }
 
 template <typename T>
@@ -514,6 +636,9 @@ constexpr int kLdsProduct = Shape<1, 2, 4, 4, false>::kLds > Shape<2, 4, 8, 3, f
 static_assert(kLdsProduct <= 160 * 1024 && Shape<2, 8, 8, 2, false>::kLds <= kLdsProduct &&
                   Shape<1, 4, 4, 3, false>::kLds <= kLdsProduct,
               "one LDS allocation serves every shape");
+constexpr int kLdsMid = Shape<2, 4, 4, 4, false>::kLds;
+static_assert(Shape<1, 4, 2, 4, false>::kLds <= kLdsMid, "one LDS allocation serves every shape");
+constexpr int kLdsSmall = Shape<2, 2, 2, 8, false>::kLds;
 constexpr int kLdsGrad = Shape<2, 8, 8, 2, true>::kLds;
 
 // More LDS than the default limit has to be asked for, once per device.
@@ -526,20 +651,57 @@ uint32_t runs_of_32(uint64_t tiles) { return (uint32_t)((tiles + 255) / 256 * 25
 
 }  // namespace
 
-void launch_product(const ProductArgs& a, hipStream_t stream) {
-    const uint32_t cols = (a.n + kTileCols - 1) / kTileCols;
-    const uint64_t slots = (uint64_t)a.rows / kTileRows + (a.offsets ? a.experts : 1);
-    const Order order = slots * cols > 512 ? kRuns : kInOrder;
-    // runs: each kind's slots rounded up to 4, its tiles to runs of 32, its
-    // runs to the 8 XCDs
-    const dim3 grid(order == kRuns ? (uint32_t)((((slots + 6) / 4 * cols + 14) / 8 + 14) / 8 * 256) : (uint32_t)(slots * cols));
-    auto launch = [&](auto kernel) {
-        allow_lds(kernel, kLdsProduct);
-        hipLaunchKernelGGL(kernel, grid, dim3(256), kLdsProduct, stream, a, cols, order);
+namespace {
+
+// Which cut, from what the host knows: rows, experts, n (not the counts).
+// Measured, in us, at n 4096, k 7168 where not said (wide / mid / small / few):
+//   few    up to 4 rows an expert and 32 more: 16 rows, 1 expert 28/24/20/13;
+//          64 rows, 8 experts, n 14336, k 4096 116/110/117/95; 128 rows, 32
+//          experts 164/163/181/164, but 512 rows there 234/174/201/217
+//   wide   from 128 tiles of 256 whole rows: 4096 rows, 1 expert 94/156/324/644;
+//          2048 rows 78/72; 16384 rows, 16 experts, n 512, k 1024 22/32
+//   small  where mid has at most 64 tiles: 128 rows, 1 expert 49/33/22/25; 256
+//          rows 70/33/24/46, but 512 rows 70/34/44/85
+//   mid    else: 1024 rows, 32 experts 241/180/230/290
+template <typename T>
+void product_as(const ProductArgs& a, hipStream_t stream) {
+    const uint64_t segments = a.offsets ? a.experts : 1;
+    const uint64_t used = a.experts < a.rows ? a.experts : a.rows;  // segments that can have rows
+    auto cols = [&](uint32_t c) { return (a.n + c - 1) / c; };
+    auto in_order = [&](auto kernel, auto cut, int lds) {
+        typedef decltype(cut) Cut;
+        const uint64_t grid = (a.rows / Cut::kRows + segments) * cols(Cut::kCols);
+        allow_lds(kernel, lds);
+        hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(256), lds, stream, a, cols(Cut::kCols), kInOrder);
     };
-    if (a.out_dtype == ZC_BF16) launch(product<__bf16>);
-    else if (a.out_dtype == ZC_FP16) launch(product<_Float16>);
-    else launch(product<float>);
+    if (a.rows <= 4 * a.experts + 32) {
+        hipLaunchKernelGGL((product_few<T>), dim3((uint32_t)((a.rows / FewCut::kRows + segments) * cols(FewCut::kCols))),
+                           dim3(256), 0, stream, a, cols(FewCut::kCols));
+    } else if ((uint64_t)(a.rows / WideCut::kRows) * cols(WideCut::kCols) >= 128) {
+        const uint64_t s = a.rows / WideCut::kRows + segments, c = cols(WideCut::kCols);
+        if (s * c <= 512) {
+            in_order(product<T, WideCut>, WideCut{}, kLdsProduct);
+        } else {
+            // runs: each kind's slots rounded up to 4, its tiles to runs of 32,
+            // its runs to the 8 XCDs
+            const uint64_t grid = (((s + 6) / 4 * c + 14) / 8 + 14) / 8 * 256;
+            allow_lds(product<T, WideCut>, kLdsProduct);
+            hipLaunchKernelGGL((product<T, WideCut>), dim3((uint32_t)grid), dim3(256), kLdsProduct, stream, a, (uint32_t)c,
+                               kRuns);
+        }
+    } else if ((a.rows / MidCut::kRows + used) * cols(MidCut::kCols) <= 64) {
+        in_order(product<T, SmallCut>, SmallCut{}, kLdsSmall);
+    } else {
+        in_order(product<T, MidCut>, MidCut{}, kLdsMid);
+    }
+}
+
+}  // namespace
+
+void launch_product(const ProductArgs& a, hipStream_t stream) {
+    if (a.out_dtype == ZC_BF16) product_as<__bf16>(a, stream);
+    else if (a.out_dtype == ZC_FP16) product_as<_Float16>(a, stream);
+    else product_as<float>(a, stream);
 }
 
 void launch_weight_grad(const WeightGradArgs& a, hipStream_t stream) {

@@ -30,8 +30,20 @@ EXPERT_EXPORTS = (
 BLOCK = 128  # values per scale
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _FP8, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+_I32, _F32 = torch.int32, torch.float32
 
 _lib = None
+
+
+class _Calls:
+    """The library's functions as attributes, set on the first use."""
+
+    def __getattr__(self, name):
+        lib()
+        return object.__getattribute__(self, name)
+
+
+_zc = _Calls()
 
 
 def lib() -> ctypes.CDLL:
@@ -59,49 +71,59 @@ def lib() -> ctypes.CDLL:
         f = getattr(L, name)
         f.argtypes = args[name]
         f.restype = u64 if name in ("zc_route_rows", "zc_route_workspace_bytes") else i
+        setattr(_zc, name, f)
     _lib = L
     return L
 
 
-def _call(name: str, *args):
-    rc = getattr(lib(), name)(*args)
-    if rc:
-        raise ZcError(rc, name)
-
-
-def _stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
-
+# The checks below run before every call, and a call's kernels take a few
+# microseconds on small inputs: they read each attribute once and say what is
+# wrong only when something is.
 
 def _bad(what: str, why: str, code: int = ZC_ERR_INVALID_ARG):
     raise ZcError(code, f"{what}: {why}")
 
 
-def _matrix(t, what: str, width: int, rows: int, dtype=None):
-    """A GPU matrix of `width` columns, contiguous along them, of `dtype` (or
-    one of the three row types) with at least `rows` rows."""
+def _failed(rc: int, name: str):
+    raise ZcError(rc, name)
+
+
+def _stream(stream):
+    # current_stream() builds a Stream object, 3 us; its handle alone is 0.1
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+
+
+def _matrix(t, what: str, rows: int, dtype=None, width=None):
+    """(pointer, row stride, rows, width) of a GPU matrix that is contiguous
+    along its columns, of `dtype` (or one of the three row types), with at
+    least `rows` rows and exactly `width` columns."""
     if not getattr(t, "is_cuda", False):
         _bad(what, "not a GPU tensor")
-    if t.dim() != 2 or t.shape[1] != width:
-        _bad(what, f"shape {tuple(t.shape)}, (rows, {width}) expected")
-    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
-        _bad(what, f"type {t.dtype}" + (f", {dtype} expected" if dtype is not None else ""))
-    if (width > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < width):
-        _bad(what, f"strides {t.stride()}: rows must be contiguous and apart")
-    if t.shape[0] < rows:
-        _bad(what, f"{t.shape[0]} rows, {rows} needed", ZC_ERR_CAPACITY)
-    return t
-
-
-def _row_stride(t) -> int:
-    return max(t.stride(0), t.shape[1])
+    d = t.dtype
+    if d is not dtype and (dtype is not None or d not in _DTYPES):
+        _bad(what, f"type {d}" + (f", {dtype} expected" if dtype is not None else ""))
+    shape = t.shape
+    if len(shape) != 2 or (width is not None and shape[1] != width):
+        _bad(what, f"shape {tuple(shape)}, (rows, {'columns' if width is None else width}) expected")
+    n, w = shape
+    s, one = t.stride()
+    if s < w:
+        if n > 1:
+            _bad(what, f"strides {(s, one)}: rows overlap")
+        s = w
+    if one != 1 and w > 1:
+        _bad(what, f"strides {(s, one)}: columns must be contiguous")
+    if n < rows:
+        _bad(what, f"{n} rows, {rows} needed", ZC_ERR_CAPACITY)
+    return t.data_ptr(), s, n, w
 
 
 def _flat(t, what: str, dtype, count: int):
-    """A contiguous GPU tensor of `dtype` with at least `count` elements."""
+    """Pointer of a contiguous GPU tensor of `dtype` with at least `count`
+    elements."""
     if not getattr(t, "is_cuda", False):
         _bad(what, "not a GPU tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         _bad(what, f"type {t.dtype}, {dtype} expected")
     if not t.is_contiguous():
         _bad(what, "not contiguous")
@@ -153,26 +175,29 @@ def empty_fp8_columns(rows: int, cols: int, device="cuda") -> Fp8Blocks:
     return _empty_blocks((cols,), (cols,), rows, device)
 
 
-def _blocks(f: Fp8Blocks, what: str, lead, scale_lead, cols: int):
+def _part(t, what: str, dtype, dims, width: int):
+    if not getattr(t, "is_cuda", False):
+        _bad(what, "not a GPU tensor")
+    if t.dtype is not dtype:
+        _bad(what, f"type {t.dtype}, {dtype} expected")
+    if not t.is_contiguous():
+        _bad(what, "not contiguous")
+    shape = t.shape
+    if len(shape) != len(dims) + 1 or shape[-1] != width or (len(dims) > 1 and shape[1] != dims[1]):
+        _bad(what, f"shape {tuple(shape)}, {tuple(dims) + (width,)} expected")
+    if shape[0] < dims[0]:
+        _bad(what, f"{shape[0]} rows, {dims[0]} needed", ZC_ERR_CAPACITY)
+    return t.data_ptr()
+
+
+def _blocks(f: Fp8Blocks, what: str, cols: int, lead, scale_lead=None):
     """Pointers of data and scale of blocks of the given shape.  The first
     dimension may be longer."""
-    if f.cols != cols:
-        _bad(what, f"{f.cols} columns, {cols} expected")
-    out = []
-    for t, dtype, dims, width in ((f.data, _FP8, lead, _up(cols, BLOCK)),
-                                  (f.scale, _E8M0, scale_lead, _up(-(-cols // BLOCK), 4))):
-        if not getattr(t, "is_cuda", False):
-            _bad(what, "not a GPU tensor")
-        if t.dtype != dtype:
-            _bad(what, f"type {t.dtype}, {dtype} expected")
-        if not t.is_contiguous():
-            _bad(what, "not contiguous")
-        if t.dim() != len(dims) + 1 or tuple(t.shape[1:]) != tuple(dims[1:]) + (width,):
-            _bad(what, f"shape {tuple(t.shape)}, {tuple(dims) + (width,)} expected")
-        if t.shape[0] < dims[0]:
-            _bad(what, f"{t.shape[0]} rows, {dims[0]} needed", ZC_ERR_CAPACITY)
-        out.append(t.data_ptr())
-    return out
+    data, scale, have = f
+    if have != cols:
+        _bad(what, f"{have} columns, {cols} expected")
+    return (_part(data, what, _FP8, lead, (cols + 127) // 128 * 128),
+            _part(scale, what, _E8M0, scale_lead or lead, (cols + 511) // 512 * 4))
 
 
 class Routing(NamedTuple):
@@ -218,87 +243,95 @@ class ExpertPlan:
 
     # checks ---------------------------------------------------------------
     def _routing(self, r: Routing):
-        i32 = torch.int32
-        return (_flat(r.offsets, "offsets", i32, self.experts + 1), _flat(r.counts, "counts", i32, self.experts),
-                _flat(r.row, "row", i32, self.tokens * self.topk))
+        return (_flat(r[0], "offsets", _I32, self.experts + 1), _flat(r[1], "counts", _I32, self.experts),
+                _flat(r[2], "row", _I32, self.tokens * self.topk))
 
     def _weights(self, w):
-        return 0 if w is None else _flat(w, "weights", torch.float32, self.tokens * self.topk)
+        return 0 if w is None else _flat(w, "weights", _F32, self.tokens * self.topk)
 
     # calls ----------------------------------------------------------------
     def route(self, ids, routing: Routing, ws, stream=None):
         """Enqueue the sorting of ids (int32 [tokens, topk]; outside
         0..experts-1: no row) into routing."""
-        p = _flat(ids, "ids", torch.int32, self.tokens * self.topk)
+        p = _flat(ids, "ids", _I32, self.tokens * self.topk)
         off, cnt, row = self._routing(routing)
-        slot = _flat(routing.slot, "slot", torch.int32, self.rows)
+        slot = routing[3]
+        s = _flat(slot, "slot", _I32, self.rows)
         w = _flat(ws, "workspace", torch.uint8, self.workspace_bytes)
-        _call("zc_route", p, self.tokens, self.topk, self.experts, self.align, off, cnt, row, slot,
-              routing.slot.numel(), w, ws.numel(), _stream(stream))
+        rc = _zc.zc_route(p, self.tokens, self.topk, self.experts, self.align, off, cnt, row, s, slot.numel(), w,
+                          ws.numel(), _stream(stream))
+        if rc:
+            _failed(rc, "zc_route")
 
     def dispatch(self, x, routing: Routing, rows, stream=None):
         """Enqueue rows[row of (t, k)] = x[t]; padding rows are zeros."""
-        _matrix(x, "x", x.shape[-1], self.tokens)
-        _matrix(rows, "rows", x.shape[1], self.rows, x.dtype)
+        p, stride, _, hidden = _matrix(x, "x", self.tokens)
+        d = x.dtype
+        q, out_stride, n, _ = _matrix(rows, "rows", self.rows, d, hidden)
         off, cnt, row = self._routing(routing)
-        _call("zc_dispatch", x.data_ptr(), _row_stride(x), _DTYPES[x.dtype], self.tokens, self.topk, self.experts,
-              x.shape[1], off, cnt, row, rows.data_ptr(), _row_stride(rows), rows.shape[0], _stream(stream))
+        rc = _zc.zc_dispatch(p, stride, _DTYPES[d], self.tokens, self.topk, self.experts, hidden, off, cnt, row, q,
+                             out_stride, n, _stream(stream))
+        if rc:
+            _failed(rc, "zc_dispatch")
 
     def dispatch_fp8(self, x, routing: Routing, out: Fp8Blocks, stream=None):
         """Enqueue dispatch with the rows stored as 1 x 128 blocks."""
-        _matrix(x, "x", x.shape[-1], self.tokens)
-        data, scale = _blocks(out, "out", (self.rows,), (self.rows,), x.shape[1])
+        p, stride, _, hidden = _matrix(x, "x", self.tokens)
+        data, scale = _blocks(out, "out", hidden, (self.rows,))
         off, cnt, row = self._routing(routing)
-        _call("zc_dispatch_fp8", x.data_ptr(), _row_stride(x), _DTYPES[x.dtype], self.tokens, self.topk,
-              self.experts, x.shape[1], off, cnt, row, data, scale, min(out.data.shape[0], out.scale.shape[0]),
-              _stream(stream))
+        rc = _zc.zc_dispatch_fp8(p, stride, _DTYPES[x.dtype], self.tokens, self.topk, self.experts, hidden, off, cnt,
+                                 row, data, scale, min(out[0].shape[0], out[1].shape[0]), _stream(stream))
+        if rc:
+            _failed(rc, "zc_dispatch_fp8")
 
     def combine(self, rows, weights, routing: Routing, y, stream=None):
         """Enqueue y[t] = sum over k of weights[t, k] * rows[row of (t, k)];
         weights None: ones, which makes it the gradient of dispatch."""
-        _matrix(y, "y", y.shape[-1], self.tokens)
-        _matrix(rows, "rows", y.shape[1], self.rows, y.dtype)
-        _, _, row = self._routing(routing)
-        _call("zc_combine", rows.data_ptr(), _row_stride(rows), self._weights(weights), _DTYPES[y.dtype],
-              self.tokens, self.topk, y.shape[1], row, rows.shape[0], y.data_ptr(), _row_stride(y),
-              _stream(stream))
+        q, y_stride, _, hidden = _matrix(y, "y", self.tokens)
+        d = y.dtype
+        p, stride, n, _ = _matrix(rows, "rows", self.rows, d, hidden)
+        row = _flat(routing[2], "row", _I32, self.tokens * self.topk)
+        rc = _zc.zc_combine(p, stride, self._weights(weights), _DTYPES[d], self.tokens, self.topk, hidden, row, n, q,
+                            y_stride, _stream(stream))
+        if rc:
+            _failed(rc, "zc_combine")
 
     def combine_backward(self, dy, rows, weights, routing: Routing, drows, dweights, stream=None):
         """Enqueue the gradient of combine: drows (padding rows zeros) and
         dweights (float32 [tokens, topk]); either may be None, and rows with
         dweights."""
-        _matrix(dy, "dy", dy.shape[-1], self.tokens)
+        p, stride, _, hidden = _matrix(dy, "dy", self.tokens)
+        d = dy.dtype
         off, cnt, row = self._routing(routing)
         if drows is None and dweights is None:
             _bad("combine_backward", "no gradient asked for")
-        capacity = []
+        q = q_stride = r = r_stride = 0
+        n = m = 1 << 31
         if drows is not None:
-            _matrix(drows, "drows", dy.shape[1], self.rows, dy.dtype)
-            capacity.append(drows.shape[0])
+            q, q_stride, n, _ = _matrix(drows, "drows", self.rows, d, hidden)
         if dweights is not None:
             if rows is None:
                 _bad("combine_backward", "dweights needs rows")
-            _matrix(rows, "rows", dy.shape[1], self.rows, dy.dtype)
-            capacity.append(rows.shape[0])
-        _call("zc_combine_backward", dy.data_ptr(), _row_stride(dy), rows.data_ptr() if dweights is not None else 0,
-              _row_stride(rows) if dweights is not None else 0, self._weights(weights), _DTYPES[dy.dtype],
-              self.tokens, self.topk, self.experts, dy.shape[1], off, cnt, row, min(capacity),
-              drows.data_ptr() if drows is not None else 0, _row_stride(drows) if drows is not None else 0,
-              self._weights(dweights), _stream(stream))
+            r, r_stride, m, _ = _matrix(rows, "rows", self.rows, d, hidden)
+        rc = _zc.zc_combine_backward(p, stride, r, r_stride, self._weights(weights), _DTYPES[d], self.tokens,
+                                     self.topk, self.experts, hidden, off, cnt, row, min(n, m), q, q_stride,
+                                     self._weights(dweights), _stream(stream))
+        if rc:
+            _failed(rc, "zc_combine_backward")
 
 
 def _used(used):
-    return 0 if used is None else _flat(used, "used", torch.int32, 1)
+    return 0 if used is None else _flat(used, "used", _I32, 1)
 
 
 def quantize_rows(x, out: Fp8Blocks, used=None, stream=None):
     """Enqueue the cast of x [rows, cols] to 1 x 128 blocks.  used: None or a
     device int32 (e.g. ``routing.offsets[-1:]``); rows from there on are left."""
-    _matrix(x, "x", x.shape[-1], 0)
-    rows, cols = x.shape
-    data, scale = _blocks(out, "out", (rows,), (rows,), cols)
-    _call("zc_quantize_rows", x.data_ptr(), _row_stride(x), _DTYPES[x.dtype], rows, cols, _used(used), data, scale,
-          _stream(stream))
+    p, stride, rows, cols = _matrix(x, "x", 0)
+    data, scale = _blocks(out, "out", cols, (rows,))
+    rc = _zc.zc_quantize_rows(p, stride, _DTYPES[x.dtype], rows, cols, _used(used), data, scale, _stream(stream))
+    if rc:
+        _failed(rc, "zc_quantize_rows")
 
 
 def quantize_weights(w, out: Fp8Blocks, transpose: bool = False, stream=None):
@@ -306,36 +339,43 @@ def quantize_weights(w, out: Fp8Blocks, transpose: bool = False, stream=None):
     the 128 x 128 blocks of [experts, n, k]."""
     if w.dim() != 3 or w.dtype not in _DTYPES:
         _bad("w", f"shape {tuple(w.shape)}, type {w.dtype}")
-    e, n, k = w.shape if not transpose else (w.shape[0], w.shape[2], w.shape[1])
+    e, n, k = w.shape
+    if transpose:
+        n, k = k, n
     p = _flat(w, "w", w.dtype, 0)
-    data, scale = _blocks(out, "out", (e, n), (e, -(-n // BLOCK)), k)
-    _call("zc_quantize_weights", p, _DTYPES[w.dtype], e, n, k, int(bool(transpose)), data, scale, _stream(stream))
+    data, scale = _blocks(out, "out", k, (e, n), (e, (n + 127) // 128))
+    rc = _zc.zc_quantize_weights(p, _DTYPES[w.dtype], e, n, k, 1 if transpose else 0, data, scale, _stream(stream))
+    if rc:
+        _failed(rc, "zc_quantize_weights")
 
 
 def quantize_columns(x, out: Fp8Blocks, used=None, stream=None):
     """Enqueue the cast of x [rows, cols] in blocks of 128 rows of a column,
     stored as the blocked [cols, rows]."""
-    _matrix(x, "x", x.shape[-1], 0)
-    rows, cols = x.shape
-    data, scale = _blocks(out, "out", (cols,), (cols,), rows)
-    _call("zc_quantize_columns", x.data_ptr(), _row_stride(x), _DTYPES[x.dtype], rows, cols, _used(used), data,
-          scale, _stream(stream))
+    p, stride, rows, cols = _matrix(x, "x", 0)
+    data, scale = _blocks(out, "out", rows, (cols,))
+    rc = _zc.zc_quantize_columns(p, stride, _DTYPES[x.dtype], rows, cols, _used(used), data, scale, _stream(stream))
+    if rc:
+        _failed(rc, "zc_quantize_columns")
 
 
 def expert_product(a: Fp8Blocks, w: Fp8Blocks, out, offsets=None, counts=None, stream=None):
     """Enqueue out[r] = A[r] W[e]^T for the rows r of every expert's segment;
     a: 1 x 128 blocks [rows, k], w: 128 x 128 blocks [experts, n, k], out
     [rows, n].  offsets None: one expert, all rows."""
-    if w.data.dim() != 3 or a.data.dim() != 2:
+    shape, k = w[0].shape, w[2]
+    if len(shape) != 3:
         _bad("expert_product", "a is [rows, k], w is [experts, n, k]")
-    (experts, n, _), rows = w.data.shape, out.shape[0]
-    _matrix(out, "out", n, 0)
-    ap, asp = _blocks(a, "a", (rows,), (rows,), w.cols)
-    wp, wsp = _blocks(w, "w", (experts, n), (experts, -(-n // BLOCK)), w.cols)
-    off = 0 if offsets is None else _flat(offsets, "offsets", torch.int32, experts + 1)
-    cnt = 0 if counts is None else _flat(counts, "counts", torch.int32, experts)
-    _call("zc_expert_product", ap, asp, rows, wp, wsp, experts, n, w.cols, off, cnt, out.data_ptr(),
-          _row_stride(out), _DTYPES[out.dtype], _stream(stream))
+    experts, n = shape[0], shape[1]
+    q, stride, rows, _ = _matrix(out, "out", 0, None, n)
+    ap, asp = _blocks(a, "a", k, (rows,))
+    wp, wsp = _blocks(w, "w", k, (experts, n), (experts, (n + 127) // 128))
+    off = 0 if offsets is None else _flat(offsets, "offsets", _I32, experts + 1)
+    cnt = 0 if counts is None else _flat(counts, "counts", _I32, experts)
+    rc = _zc.zc_expert_product(ap, asp, rows, wp, wsp, experts, n, k, off, cnt, q, stride, _DTYPES[out.dtype],
+                               _stream(stream))
+    if rc:
+        _failed(rc, "zc_expert_product")
 
 
 def expert_weight_grad(y: Fp8Blocks, x: Fp8Blocks, dw, offsets=None, stream=None):
@@ -345,9 +385,11 @@ def expert_weight_grad(y: Fp8Blocks, x: Fp8Blocks, dw, offsets=None, stream=None
     if dw.dim() != 3 or dw.dtype not in _DTYPES:
         _bad("dw", f"shape {tuple(dw.shape)}, type {dw.dtype}")
     experts, n, k = dw.shape
+    rows = x[2]
     p = _flat(dw, "dw", dw.dtype, 0)
-    yp, ysp = _blocks(y, "y", (n,), (n,), x.cols)
-    xp, xsp = _blocks(x, "x", (k,), (k,), x.cols)
-    off = 0 if offsets is None else _flat(offsets, "offsets", torch.int32, experts + 1)
-    _call("zc_expert_weight_grad", yp, ysp, xp, xsp, x.cols, experts, n, k, off, p, _DTYPES[dw.dtype],
-          _stream(stream))
+    yp, ysp = _blocks(y, "y", rows, (n,))
+    xp, xsp = _blocks(x, "x", rows, (k,))
+    off = 0 if offsets is None else _flat(offsets, "offsets", _I32, experts + 1)
+    rc = _zc.zc_expert_weight_grad(yp, ysp, xp, xsp, rows, experts, n, k, off, p, _DTYPES[dw.dtype], _stream(stream))
+    if rc:
+        _failed(rc, "zc_expert_weight_grad")
