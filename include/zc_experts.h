@@ -57,7 +57,8 @@ typedef enum zc_dtype { ZC_BF16 = 0, ZC_FP16 = 1, ZC_FP32 = 2 } zc_dtype;
 /* Limits: experts 1..1024, topk 1..64, align a power of two 1..1024, rows
  * below 2^31, row widths below 2^24.  zc_route_rows gives the rows that hold
  * every possible routing, up(slots + min(experts, slots) * (align - 1), align),
- * or 0 where a limit is passed. */
+ * or 0 where a limit is passed.  A call whose launch would pass 2^32 threads is
+ * refused with ZC_ERR_UNSUPPORTED. */
 uint64_t zc_route_rows(uint64_t tokens, uint32_t topk, uint32_t experts, uint32_t align);
 uint64_t zc_route_workspace_bytes(uint64_t tokens, uint32_t topk, uint32_t experts);
 
@@ -75,7 +76,9 @@ zc_status zc_route(const int32_t *d_ids, uint64_t tokens, uint32_t topk, uint32_
                    hipStream_t stream);
 
 /* d_rows[row of (t, k)] = d_x[t] for every slot with a row; padding rows are
- * zeros.  d_offsets, d_counts, d_row: as zc_route wrote them. */
+ * zeros.  d_offsets, d_counts, d_row: as zc_route wrote them.  d_counts NULL,
+ * here and in the calls below: there are no padding rows (zc_route with align
+ * 1), and nothing looks for them. */
 zc_status zc_dispatch(const void *d_x, uint64_t x_stride, uint32_t dtype, uint64_t tokens,
                       uint32_t topk, uint32_t experts, uint32_t hidden, const int32_t *d_offsets,
                       const int32_t *d_counts, const int32_t *d_row, void *d_rows,

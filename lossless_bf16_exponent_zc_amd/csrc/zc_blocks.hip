@@ -14,27 +14,28 @@ constexpr uint32_t kWaveCols = 1024;  // columns of one wave: 16 per lane, 8 blo
 
 template <typename T>
 struct Pack16 {
+    typedef xu32x4 __attribute__((aligned(2))) Word;  // at any element's address
     union {
         xu32x4 w[sizeof(T)];  // 16 values
         T v[16];
     };
 };
 
+constexpr uint32_t kPadSplit = 4;  // workgroups for the padding rows of an expert
+
 // Blocks of 1 x 128.  A wave casts 1024 columns of one token, 16 per lane, so
 // a block is 8 lanes and its bytes leave in one 16-byte store per lane; the
-// stores go to every row of the token.  Rows whose start is not a multiple of
-// 16 bytes, and a last piece of fewer than 16 values, are read one element
-// per lane (consecutive lanes, consecutive addresses) and turned over in LDS.
-template <typename T>
-__global__ __launch_bounds__(256) void cast_rows(CastRowsArgs a, uint32_t pieces, uint32_t token_blocks) {
-    __shared__ __align__(16) T turn[4][kWaveCols];
+// stores go to every row of the token, past the caches (PAST) where the rows
+// are more than the L2s hold.  The workgroups of the padding rows come first.
+template <typename T, bool PAST>
+__global__ __launch_bounds__(256) void cast_rows(CastRowsArgs a, uint32_t pieces, uint32_t pad_blocks) {
     const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x >> 6);
-    if (blockIdx.x >= token_blocks) {  // padding rows of one expert
-        const uint32_t e = blockIdx.x - token_blocks;
+    if (blockIdx.x < pad_blocks) {
+        const uint32_t e = blockIdx.x / kPadSplit, first = blockIdx.x % kPadSplit * 4 + wave;
         const uint32_t lo = (uint32_t)a.offsets[e] + (uint32_t)a.counts[e];
         uint32_t hi = (uint32_t)a.offsets[e + 1];
         hi = hi < a.capacity ? hi : a.capacity;
-        for (uint32_t r = lo + wave; r < hi; r += 4) {
+        for (uint32_t r = lo + first; r < hi; r += kPadSplit * 4) {
             for (uint32_t c = lane * 16; c < a.data_stride; c += 1024)
                 *reinterpret_cast<xu32x4*>(a.data + (uint64_t)r * a.data_stride + c) = xu32x4{};
             for (uint32_t c = lane * 4; c < a.scale_stride; c += 256)
@@ -42,7 +43,7 @@ __global__ __launch_bounds__(256) void cast_rows(CastRowsArgs a, uint32_t pieces
         }
         return;
     }
-    const uint64_t item = (uint64_t)blockIdx.x * 4 + wave;
+    const uint64_t item = (uint64_t)(blockIdx.x - pad_blocks) * 4 + wave;
     const uint32_t t = (uint32_t)(item / pieces), piece = (uint32_t)(item % pieces);
     uint32_t tokens = a.tokens;
     if (a.used) {
@@ -50,23 +51,15 @@ __global__ __launch_bounds__(256) void cast_rows(CastRowsArgs a, uint32_t pieces
         tokens = u < 0 ? 0 : (uint32_t)u < tokens ? (uint32_t)u : tokens;
     }
     if (t >= tokens) return;
-    const uint32_t c0 = piece * kWaveCols, c = c0 + lane * 16;
+    const uint32_t c = piece * kWaveCols + lane * 16;
     const T* x = static_cast<const T*>(a.x) + (uint64_t)t * a.x_stride;
     Pack16<T> p;
-    if (a.wide && c0 + kWaveCols <= a.width) {
+    if (c + 16 <= a.width) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T); ++i) p.w[i] = reinterpret_cast<const xu32x4*>(x + c)[i];
+        for (int i = 0; i < (int)sizeof(T); ++i) p.w[i] = reinterpret_cast<const typename Pack16<T>::Word*>(x + c)[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint32_t j = i * 64 + lane;
-            turn[wave][j] = c0 + j < a.width ? x[c0 + j] : (T)0.0f;
-        }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T); ++i) p.w[i] = reinterpret_cast<const xu32x4*>(&turn[wave][lane * 16])[i];
+        for (int i = 0; i < 16; ++i) p.v[i] = c + i < a.width ? x[c + i] : (T)0.0f;
     }
     uint32_t top = 0;
 #pragma unroll
@@ -88,7 +81,11 @@ __global__ __launch_bounds__(256) void cast_rows(CastRowsArgs a, uint32_t pieces
     const uint32_t sc = piece * 8 + (lane >> 5) * 4;
     const bool has_scale = (lane & 31) == 0 && sc < a.scale_stride;
     auto store = [&](uint64_t r) {
-        if (c < a.data_stride) *reinterpret_cast<xu32x4*>(a.data + r * a.data_stride + c) = q;
+        xu32x4* out = reinterpret_cast<xu32x4*>(a.data + r * a.data_stride + c);
+        if (c < a.data_stride) {
+            if (PAST) __builtin_nontemporal_store(q, out);
+            else *out = q;
+        }
         if (has_scale) *reinterpret_cast<uint32_t*>(a.scale + r * a.scale_stride + sc) = s;
     };
     if (!a.row) {
@@ -134,9 +131,9 @@ __global__ __launch_bounds__(256) void cast_tile(CastTileArgs a, uint32_t row_ti
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const T* xr = x + (r0 + i) * stride + c0;
-        if (r0 + i < limit && a.wide && c0 + 8 <= xcols) {
+        if (r0 + i < limit && c0 + 8 <= xcols) {
 #pragma unroll
-            for (int h = 0; h < (int)sizeof(T) / 2; ++h) p[i].w[h] = reinterpret_cast<const xu32x4*>(xr)[h];
+            for (int h = 0; h < (int)sizeof(T) / 2; ++h) p[i].w[h] = reinterpret_cast<const typename Pack16<T>::Word*>(xr)[h];
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) p[i].v[j] = r0 + i < limit && c0 + j < xcols ? xr[j] : (T)0.0f;
@@ -227,46 +224,56 @@ __global__ __launch_bounds__(256) void cast_tile(CastTileArgs a, uint32_t row_ti
 }
 
 template <typename T>
-void rows_type(const CastRowsArgs& a, hipStream_t stream) {
+zc_status rows_type(const CastRowsArgs& a, hipStream_t stream) {
     const uint32_t pieces = (a.data_stride + kWaveCols - 1) / kWaveCols;
-    const uint32_t token_blocks = (uint32_t)(((uint64_t)a.tokens * pieces + 3) / 4);
-    hipLaunchKernelGGL(cast_rows<T>, dim3(token_blocks + (a.row ? a.experts : 0)), dim3(256), 0, stream, a, pieces,
-                       token_blocks);
+    const uint64_t blocks = ((uint64_t)a.tokens * pieces + 3) / 4;
+    const uint32_t pads = a.counts ? a.experts * kPadSplit : 0;
+    if (!fits(blocks + pads)) return ZC_ERR_UNSUPPORTED;
+    auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((uint32_t)blocks + pads), dim3(256), 0, stream, a, pieces, pads);
+        return ZC_OK;
+    };
+    const bool past = (uint64_t)a.tokens * a.topk * a.data_stride >= (64ull << 20);
+    return past ? launch(cast_rows<T, true>) : launch(cast_rows<T, false>);
 }
 
 template <typename T>
-void weights_type(const CastTileArgs& a, hipStream_t stream) {
+zc_status weights_type(const CastTileArgs& a, hipStream_t stream) {
     const uint32_t nt = (a.rows + 127) / 128, kt = (a.cols + 127) / 128;
+    if (!fits((uint64_t)nt * kt * a.experts)) return ZC_ERR_UNSUPPORTED;
     if (a.transpose)
         hipLaunchKernelGGL((cast_tile<T, kWeightsTransposed>), dim3(nt * kt * a.experts), dim3(256), 0, stream, a, kt, nt);
     else
         hipLaunchKernelGGL((cast_tile<T, kWeights>), dim3(nt * kt * a.experts), dim3(256), 0, stream, a, nt, kt);
+    return ZC_OK;
 }
 
 template <typename T>
-void columns_type(const CastTileArgs& a, hipStream_t stream) {
+zc_status columns_type(const CastTileArgs& a, hipStream_t stream) {
     const uint32_t rt = (a.rows + 127) / 128, ct = (a.cols + 127) / 128;
+    if (!fits((uint64_t)rt * ct)) return ZC_ERR_UNSUPPORTED;
     hipLaunchKernelGGL((cast_tile<T, kColumns>), dim3(rt * ct), dim3(256), 0, stream, a, rt, ct);
+    return ZC_OK;
 }
 
 }  // namespace
 
-void launch_cast_rows(const CastRowsArgs& a, uint32_t dtype, hipStream_t stream) {
-    if (dtype == ZC_BF16) rows_type<__bf16>(a, stream);
-    else if (dtype == ZC_FP16) rows_type<_Float16>(a, stream);
-    else rows_type<float>(a, stream);
+zc_status launch_cast_rows(const CastRowsArgs& a, uint32_t dtype, hipStream_t stream) {
+    if (dtype == ZC_BF16) return rows_type<__bf16>(a, stream);
+    if (dtype == ZC_FP16) return rows_type<_Float16>(a, stream);
+    return rows_type<float>(a, stream);
 }
 
-void launch_cast_weights(const CastTileArgs& a, uint32_t dtype, hipStream_t stream) {
-    if (dtype == ZC_BF16) weights_type<__bf16>(a, stream);
-    else if (dtype == ZC_FP16) weights_type<_Float16>(a, stream);
-    else weights_type<float>(a, stream);
+zc_status launch_cast_weights(const CastTileArgs& a, uint32_t dtype, hipStream_t stream) {
+    if (dtype == ZC_BF16) return weights_type<__bf16>(a, stream);
+    if (dtype == ZC_FP16) return weights_type<_Float16>(a, stream);
+    return weights_type<float>(a, stream);
 }
 
-void launch_cast_columns(const CastTileArgs& a, uint32_t dtype, hipStream_t stream) {
-    if (dtype == ZC_BF16) columns_type<__bf16>(a, stream);
-    else if (dtype == ZC_FP16) columns_type<_Float16>(a, stream);
-    else columns_type<float>(a, stream);
+zc_status launch_cast_columns(const CastTileArgs& a, uint32_t dtype, hipStream_t stream) {
+    if (dtype == ZC_BF16) return columns_type<__bf16>(a, stream);
+    if (dtype == ZC_FP16) return columns_type<_Float16>(a, stream);
+    return columns_type<float>(a, stream);
 }
 
 }  // namespace zc

@@ -26,7 +26,9 @@ uint64_t route_rows(uint64_t tokens, uint32_t topk, uint32_t experts, uint32_t a
     return up64(slots + used * (align - 1), align);
 }
 
-zc_status launch_status() { return hipGetLastError() == hipSuccess ? ZC_OK : ZC_ERR_HIP; }
+zc_status finished(zc_status launched) {
+    return launched != ZC_OK ? launched : hipGetLastError() == hipSuccess ? ZC_OK : ZC_ERR_HIP;
+}
 
 // Shapes that every row call shares; ZC_OK, or why not.
 zc_status check_rows(uint32_t dtype, uint64_t tokens, uint32_t topk, uint32_t hidden, uint64_t row_capacity) {
@@ -42,6 +44,11 @@ bool bad_matrix(const void* p, uint64_t stride, uint32_t width, uint32_t dtype) 
 }
 
 bool bad_words(const void* p) { return !p || !aligned(p, 4); }
+
+// offsets are read for the padding rows alone, which counts stand for
+bool bad_segments(const int32_t* offsets, const int32_t* counts) {
+    return counts && (!aligned(counts, 4) || bad_words(offsets));
+}
 
 }  // namespace
 
@@ -71,8 +78,7 @@ zc_status zc_route(const int32_t* d_ids, uint64_t tokens, uint32_t topk, uint32_
     const uint32_t n = (uint32_t)(tokens * topk);
     const RouteArgs a{d_ids, n, experts, align, (uint32_t)row_capacity, d_offsets, d_counts, d_row, d_slot,
                       static_cast<uint32_t*>(d_ws), (uint32_t)route_tiles(n)};
-    launch_route(a, stream);
-    return launch_status();
+    return finished(launch_route(a, stream));
 }
 
 zc_status zc_dispatch(const void* d_x, uint64_t x_stride, uint32_t dtype, uint64_t tokens, uint32_t topk,
@@ -83,7 +89,7 @@ zc_status zc_dispatch(const void* d_x, uint64_t x_stride, uint32_t dtype, uint64
     if (!experts || experts > kMaxExperts) return ZC_ERR_UNSUPPORTED;
     if (!tokens || !row_capacity) return ZC_OK;
     if (bad_matrix(d_x, x_stride, hidden, dtype) || bad_matrix(d_rows, rows_stride, hidden, dtype) ||
-        bad_words(d_offsets) || bad_words(d_counts) || bad_words(d_row))
+        bad_words(d_row) || bad_segments(d_offsets, d_counts))
         return ZC_ERR_INVALID_ARG;
     const uint32_t eb = elem_bytes(dtype);
     RowArgs a{};
@@ -99,8 +105,7 @@ zc_status zc_dispatch(const void* d_x, uint64_t x_stride, uint32_t dtype, uint64
     a.experts = experts;
     a.width = hidden;
     a.capacity = (uint32_t)row_capacity;
-    launch_dispatch(a, eb, stream);
-    return launch_status();
+    return finished(launch_dispatch(a, dtype, stream));
 }
 
 zc_status zc_dispatch_fp8(const void* d_x, uint64_t x_stride, uint32_t dtype, uint64_t tokens, uint32_t topk,
@@ -111,14 +116,13 @@ zc_status zc_dispatch_fp8(const void* d_x, uint64_t x_stride, uint32_t dtype, ui
     if (!experts || experts > kMaxExperts) return ZC_ERR_UNSUPPORTED;
     if (!tokens || !row_capacity) return ZC_OK;
     if (bad_matrix(d_x, x_stride, hidden, dtype) || !d_data || !aligned(d_data, 16) || !d_scale ||
-        !aligned(d_scale, 16) || bad_words(d_offsets) || bad_words(d_counts) || bad_words(d_row))
+        !aligned(d_scale, 16) || bad_words(d_row) || bad_segments(d_offsets, d_counts))
         return ZC_ERR_INVALID_ARG;
     const uint32_t eb = elem_bytes(dtype);
     const CastRowsArgs a{d_x, x_stride, static_cast<uint8_t*>(d_data), static_cast<uint8_t*>(d_scale), d_row,
                          d_offsets, d_counts, nullptr, (uint32_t)tokens, topk, experts, hidden, stored(hidden),
-                         scales(hidden), (uint32_t)row_capacity, aligned(d_x, 16) && x_stride * eb % 16 == 0};
-    launch_cast_rows(a, dtype, stream);
-    return launch_status();
+                         scales(hidden), (uint32_t)row_capacity};
+    return finished(launch_cast_rows(a, dtype, stream));
 }
 
 zc_status zc_combine(const void* d_rows, uint64_t rows_stride, const float* d_weights, uint32_t dtype,
@@ -141,8 +145,7 @@ zc_status zc_combine(const void* d_rows, uint64_t rows_stride, const float* d_we
     a.topk = topk;
     a.width = hidden;
     a.capacity = (uint32_t)row_capacity;
-    launch_combine(a, dtype, stream);
-    return launch_status();
+    return finished(launch_combine(a, dtype, stream));
 }
 
 zc_status zc_combine_backward(const void* d_dy, uint64_t dy_stride, const void* d_rows, uint64_t rows_stride,
@@ -156,7 +159,7 @@ zc_status zc_combine_backward(const void* d_dy, uint64_t dy_stride, const void* 
     if (!tokens) return ZC_OK;
     if (bad_matrix(d_dy, dy_stride, hidden, dtype) || bad_words(d_row) || (d_weights && !aligned(d_weights, 4)))
         return ZC_ERR_INVALID_ARG;
-    if (d_drows && (bad_matrix(d_drows, drows_stride, hidden, dtype) || bad_words(d_offsets) || bad_words(d_counts)))
+    if (d_drows && (bad_matrix(d_drows, drows_stride, hidden, dtype) || bad_segments(d_offsets, d_counts)))
         return ZC_ERR_INVALID_ARG;
     if (d_dweights &&
         (!aligned(d_dweights, 4) || (row_capacity && bad_matrix(d_rows, rows_stride, hidden, dtype))))
@@ -179,8 +182,7 @@ zc_status zc_combine_backward(const void* d_dy, uint64_t dy_stride, const void* 
     a.experts = experts;
     a.width = hidden;
     a.capacity = (uint32_t)row_capacity;
-    launch_combine_backward(a, dtype, stream);
-    return launch_status();
+    return finished(launch_combine_backward(a, dtype, stream));
 }
 
 zc_status zc_quantize_rows(const void* d_x, uint64_t x_stride, uint32_t dtype, uint64_t rows, uint32_t cols,
@@ -194,9 +196,8 @@ zc_status zc_quantize_rows(const void* d_x, uint64_t x_stride, uint32_t dtype, u
     const uint32_t eb = elem_bytes(dtype);
     const CastRowsArgs a{d_x, x_stride, static_cast<uint8_t*>(d_data), static_cast<uint8_t*>(d_scale), nullptr,
                          nullptr, nullptr, d_used, (uint32_t)rows, 1, 0, cols, stored(cols), scales(cols),
-                         (uint32_t)rows, aligned(d_x, 16) && x_stride * eb % 16 == 0};
-    launch_cast_rows(a, dtype, stream);
-    return launch_status();
+                         (uint32_t)rows};
+    return finished(launch_cast_rows(a, dtype, stream));
 }
 
 zc_status zc_quantize_weights(const void* d_w, uint32_t dtype, uint32_t experts, uint32_t n, uint32_t k,
@@ -206,12 +207,9 @@ zc_status zc_quantize_weights(const void* d_w, uint32_t dtype, uint32_t experts,
     if ((uint64_t)experts * (stored(n) / 128) * (stored(k) / 128) > kMaxRows) return ZC_ERR_UNSUPPORTED;
     if (bad_matrix(d_w, k, k, dtype) || !d_data || !aligned(d_data, 16) || !d_scale || !aligned(d_scale, 16))
         return ZC_ERR_INVALID_ARG;
-    const uint32_t eb = elem_bytes(dtype), xcols = transpose ? n : k;
     const CastTileArgs a{d_w, 0, static_cast<uint8_t*>(d_data), static_cast<uint8_t*>(d_scale), nullptr, n, k,
-                         experts, stored(k), scales(k), transpose ? 1u : 0u,
-                         aligned(d_w, 16) && (uint64_t)xcols * eb % 16 == 0};
-    launch_cast_weights(a, dtype, stream);
-    return launch_status();
+                         experts, stored(k), scales(k), transpose ? 1u : 0u};
+    return finished(launch_cast_weights(a, dtype, stream));
 }
 
 zc_status zc_quantize_columns(const void* d_x, uint64_t x_stride, uint32_t dtype, uint64_t rows, uint32_t cols,
@@ -224,10 +222,8 @@ zc_status zc_quantize_columns(const void* d_x, uint64_t x_stride, uint32_t dtype
         return ZC_ERR_INVALID_ARG;
     const uint32_t eb = elem_bytes(dtype);
     const CastTileArgs a{d_x, x_stride, static_cast<uint8_t*>(d_data), static_cast<uint8_t*>(d_scale), d_used,
-                         (uint32_t)rows, cols, 1, stored((uint32_t)rows), scales((uint32_t)rows), 0,
-                         aligned(d_x, 16) && x_stride * eb % 16 == 0};
-    launch_cast_columns(a, dtype, stream);
-    return launch_status();
+                         (uint32_t)rows, cols, 1, stored((uint32_t)rows), scales((uint32_t)rows), 0};
+    return finished(launch_cast_columns(a, dtype, stream));
 }
 
 zc_status zc_expert_product(const void* d_a, const void* d_a_scale, uint64_t rows, const void* d_w,
@@ -246,8 +242,7 @@ zc_status zc_expert_product(const void* d_a, const void* d_a_scale, uint64_t row
                         static_cast<const uint8_t*>(d_w), static_cast<const uint8_t*>(d_w_scale), d_offsets, d_counts,
                         d_out, out_stride, (uint32_t)rows, experts, n, stored(k), scales(k), scales(k), out_dtype,
                         aligned(d_out, 16) && out_stride * elem_bytes(out_dtype) % 16 == 0};
-    launch_product(a, stream);
-    return launch_status();
+    return finished(launch_product(a, stream));
 }
 
 zc_status zc_expert_weight_grad(const void* d_y, const void* d_y_scale, const void* d_x, const void* d_x_scale,
@@ -264,8 +259,7 @@ zc_status zc_expert_weight_grad(const void* d_y, const void* d_y_scale, const vo
                            static_cast<const uint8_t*>(d_x), static_cast<const uint8_t*>(d_x_scale), d_offsets, d_dw,
                            stored((uint32_t)rows), experts, n, k, scales((uint32_t)rows), out_dtype,
                            aligned(d_dw, 16) && (uint64_t)k * elem_bytes(out_dtype) % 16 == 0};
-    launch_weight_grad(a, stream);
-    return launch_status();
+    return finished(launch_weight_grad(a, stream));
 }
 
 }  // extern "C"

@@ -35,7 +35,7 @@ struct RowArgs {  // dispatch, combine and the gradient of combine
     const float* weights;  // or null
     float* dweights;       // or null
     const int32_t* offsets;
-    const int32_t* counts;
+    const int32_t* counts; // or null: no padding rows
     const int32_t* row;
     uint64_t x_stride, rows_stride, out_stride;  // in bytes
     uint32_t tokens, topk, experts;
@@ -55,7 +55,6 @@ struct CastRowsArgs {
     uint32_t tokens, topk, experts, width;
     uint32_t data_stride, scale_stride;
     uint32_t capacity;
-    uint32_t wide;         // rows start at 16-byte addresses
 };
 
 struct CastTileArgs {
@@ -68,7 +67,6 @@ struct CastTileArgs {
     uint32_t experts;
     uint32_t data_stride, scale_stride;
     uint32_t transpose;
-    uint32_t wide;
 };
 
 struct ProductArgs {
@@ -99,26 +97,25 @@ struct WeightGradArgs {
     uint32_t wide;
 };
 
+// Each enqueues its kernels, or returns ZC_ERR_UNSUPPORTED and enqueues none
+// where the launch would have more workgroups than a launch may (2^32 threads).
 uint64_t route_tiles(uint64_t nslots);
-void launch_route(const RouteArgs& a, hipStream_t stream);
-void launch_dispatch(const RowArgs& a, uint32_t elem_bytes, hipStream_t stream);
-void launch_combine(const RowArgs& a, uint32_t dtype, hipStream_t stream);
-void launch_combine_backward(const RowArgs& a, uint32_t dtype, hipStream_t stream);
-void launch_cast_rows(const CastRowsArgs& a, uint32_t dtype, hipStream_t stream);
-void launch_cast_weights(const CastTileArgs& a, uint32_t dtype, hipStream_t stream);
-void launch_cast_columns(const CastTileArgs& a, uint32_t dtype, hipStream_t stream);
-void launch_product(const ProductArgs& a, hipStream_t stream);
-void launch_weight_grad(const WeightGradArgs& a, hipStream_t stream);
+zc_status launch_route(const RouteArgs& a, hipStream_t stream);
+zc_status launch_dispatch(const RowArgs& a, uint32_t dtype, hipStream_t stream);
+zc_status launch_combine(const RowArgs& a, uint32_t dtype, hipStream_t stream);
+zc_status launch_combine_backward(const RowArgs& a, uint32_t dtype, hipStream_t stream);
+zc_status launch_cast_rows(const CastRowsArgs& a, uint32_t dtype, hipStream_t stream);
+zc_status launch_cast_weights(const CastTileArgs& a, uint32_t dtype, hipStream_t stream);
+zc_status launch_cast_columns(const CastTileArgs& a, uint32_t dtype, hipStream_t stream);
+zc_status launch_product(const ProductArgs& a, hipStream_t stream);
+zc_status launch_weight_grad(const WeightGradArgs& a, hipStream_t stream);
+
+// Whether a launch may have this many workgroups of 256 threads.
+inline bool fits(uint64_t workgroups) { return workgroups < (1ull << 24); }
 
 // -------------------------------------------------------- device helpers
 typedef uint32_t xu32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t xu32x2 __attribute__((ext_vector_type(2)));
-
-template <int BYTES> struct Word;
-template <> struct Word<16> { typedef xu32x4 type; };
-template <> struct Word<8> { typedef xu32x2 type; };
-template <> struct Word<4> { typedef uint32_t type; };
-template <> struct Word<2> { typedef uint16_t type; };
 
 __host__ __device__ constexpr uint32_t up_to(uint32_t n, uint32_t m) { return (n + m - 1) / m * m; }
 

@@ -664,57 +664,60 @@ namespace {
 //          rows 70/33/24/46, but 512 rows 70/34/44/85
 //   mid    else: 1024 rows, 32 experts 241/180/230/290
 template <typename T>
-void product_as(const ProductArgs& a, hipStream_t stream) {
+zc_status product_as(const ProductArgs& a, hipStream_t stream) {
     const uint64_t segments = a.offsets ? a.experts : 1;
     const uint64_t used = a.experts < a.rows ? a.experts : a.rows;  // segments that can have rows
     auto cols = [&](uint32_t c) { return (a.n + c - 1) / c; };
     auto in_order = [&](auto kernel, auto cut, int lds) {
         typedef decltype(cut) Cut;
         const uint64_t grid = (a.rows / Cut::kRows + segments) * cols(Cut::kCols);
+        if (!fits(grid)) return ZC_ERR_UNSUPPORTED;
         allow_lds(kernel, lds);
         hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(256), lds, stream, a, cols(Cut::kCols), kInOrder);
+        return ZC_OK;
     };
     if (a.rows <= 4 * a.experts + 32) {
-        hipLaunchKernelGGL((product_few<T>), dim3((uint32_t)((a.rows / FewCut::kRows + segments) * cols(FewCut::kCols))),
-                           dim3(256), 0, stream, a, cols(FewCut::kCols));
-    } else if ((uint64_t)(a.rows / WideCut::kRows) * cols(WideCut::kCols) >= 128) {
-        const uint64_t s = a.rows / WideCut::kRows + segments, c = cols(WideCut::kCols);
-        if (s * c <= 512) {
-            in_order(product<T, WideCut>, WideCut{}, kLdsProduct);
-        } else {
-            // runs: each kind's slots rounded up to 4, its tiles to runs of 32,
-            // its runs to the 8 XCDs
-            const uint64_t grid = (((s + 6) / 4 * c + 14) / 8 + 14) / 8 * 256;
-            allow_lds(product<T, WideCut>, kLdsProduct);
-            hipLaunchKernelGGL((product<T, WideCut>), dim3((uint32_t)grid), dim3(256), kLdsProduct, stream, a, (uint32_t)c,
-                               kRuns);
-        }
-    } else if ((a.rows / MidCut::kRows + used) * cols(MidCut::kCols) <= 64) {
-        in_order(product<T, SmallCut>, SmallCut{}, kLdsSmall);
-    } else {
-        in_order(product<T, MidCut>, MidCut{}, kLdsMid);
+        const uint64_t grid = (a.rows / FewCut::kRows + segments) * cols(FewCut::kCols);
+        if (!fits(grid)) return ZC_ERR_UNSUPPORTED;
+        hipLaunchKernelGGL((product_few<T>), dim3((uint32_t)grid), dim3(256), 0, stream, a, cols(FewCut::kCols));
+        return ZC_OK;
     }
+    if ((uint64_t)(a.rows / WideCut::kRows) * cols(WideCut::kCols) >= 128) {
+        const uint64_t s = a.rows / WideCut::kRows + segments, c = cols(WideCut::kCols);
+        if (s * c <= 512) return in_order(product<T, WideCut>, WideCut{}, kLdsProduct);
+        // runs: each kind's slots rounded up to 4, its tiles to runs of 32, its
+        // runs to the 8 XCDs
+        const uint64_t grid = (((s + 6) / 4 * c + 14) / 8 + 14) / 8 * 256;
+        if (!fits(grid)) return ZC_ERR_UNSUPPORTED;
+        allow_lds(product<T, WideCut>, kLdsProduct);
+        hipLaunchKernelGGL((product<T, WideCut>), dim3((uint32_t)grid), dim3(256), kLdsProduct, stream, a, (uint32_t)c, kRuns);
+        return ZC_OK;
+    }
+    if ((a.rows / MidCut::kRows + used) * cols(MidCut::kCols) <= 64) return in_order(product<T, SmallCut>, SmallCut{}, kLdsSmall);
+    return in_order(product<T, MidCut>, MidCut{}, kLdsMid);
 }
 
 }  // namespace
 
-void launch_product(const ProductArgs& a, hipStream_t stream) {
-    if (a.out_dtype == ZC_BF16) product_as<__bf16>(a, stream);
-    else if (a.out_dtype == ZC_FP16) product_as<_Float16>(a, stream);
-    else product_as<float>(a, stream);
+zc_status launch_product(const ProductArgs& a, hipStream_t stream) {
+    if (a.out_dtype == ZC_BF16) return product_as<__bf16>(a, stream);
+    if (a.out_dtype == ZC_FP16) return product_as<_Float16>(a, stream);
+    return product_as<float>(a, stream);
 }
 
-void launch_weight_grad(const WeightGradArgs& a, hipStream_t stream) {
+zc_status launch_weight_grad(const WeightGradArgs& a, hipStream_t stream) {
     const uint32_t rows = (a.n + kTileRows - 1) / kTileRows, cols = (a.k + kTileCols - 1) / kTileCols;
     const uint64_t slots = (uint64_t)a.experts * ((rows + 3) / 4 * 4);
+    if (!fits(slots * cols + 256)) return ZC_ERR_UNSUPPORTED;
     const dim3 grid(runs_of_32(slots * cols));
     auto launch = [&](auto kernel) {
         allow_lds(kernel, kLdsGrad);
         hipLaunchKernelGGL(kernel, grid, dim3(256), kLdsGrad, stream, a, rows, cols);
+        return ZC_OK;
     };
-    if (a.out_dtype == ZC_BF16) launch(weight_grad<__bf16>);
-    else if (a.out_dtype == ZC_FP16) launch(weight_grad<_Float16>);
-    else launch(weight_grad<float>);
+    if (a.out_dtype == ZC_BF16) return launch(weight_grad<__bf16>);
+    if (a.out_dtype == ZC_FP16) return launch(weight_grad<_Float16>);
+    return launch(weight_grad<float>);
 }
 
 }  // namespace zc

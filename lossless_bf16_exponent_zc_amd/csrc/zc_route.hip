@@ -193,16 +193,17 @@ __global__ __launch_bounds__(256) void route_place(RouteArgs a) {
 
 uint64_t route_tiles(uint64_t nslots) { return nslots <= kSmall ? 0 : (nslots + kTile - 1) / kTile; }
 
-void launch_route(const RouteArgs& a, hipStream_t stream) {
+zc_status launch_route(const RouteArgs& a, hipStream_t stream) {
     if (a.tiles == 0) {
         uint32_t nwaves = (a.nslots + 63) / 64;
         nwaves = nwaves < 1 ? 1 : nwaves > 16 ? 16 : nwaves;
         hipLaunchKernelGGL(route_small, dim3(1), dim3(1024), nwaves * a.experts * 4u, stream, a, nwaves);
-        return;
+        return ZC_OK;
     }
     hipLaunchKernelGGL(route_count, dim3(a.tiles), dim3(256), a.experts * 4u, stream, a);
     hipLaunchKernelGGL(route_scan, dim3(a.experts), dim3(256), 0, stream, a);
     hipLaunchKernelGGL(route_place, dim3(a.tiles), dim3(256), 4u * a.experts * 4u, stream, a);
+    return ZC_OK;  // at most 2^21 tiles
 }
 
 }  // namespace zc

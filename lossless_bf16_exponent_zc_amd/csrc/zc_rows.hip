@@ -8,140 +8,165 @@
 // written or read from there, so nothing is fetched twice and every sum has a
 // fixed order.  Bound by memory: dispatch moves (1 + topk) rows per token,
 // combine the same, the gradient 1 + 2 topk.
+//
+// Rows are moved in 16-byte words wherever they start (the memory takes words
+// at any element's address; a copy of odd rows of 7169 16-bit values runs at
+// 4.1 TB/s so and at 3.2 by elements); the last, shorter word of a row goes
+// by elements.
 #include "zc_experts_kernels.h"
 
 namespace zc {
 
 namespace {
 
-// Threads of a workgroup: tx columns (in words) by 256 / tx tokens, tx a
-// power of two.  From 64 columns on a wave has one token, whose rows and
-// weights are then scalar loads.
-struct Split {
-    uint32_t log_tx;
-    uint32_t words;         // words per row
-    uint32_t token_blocks;  // workgroups along x before those of the padding rows
-};
-
-template <bool WAVE>
-__device__ __forceinline__ uint32_t token_of(const Split& s) {
-    const uint32_t ty = threadIdx.x >> s.log_tx;
-    return blockIdx.x * (256u >> s.log_tx) + (WAVE ? uniform(ty) : ty);
-}
-
-// Zeros in the padding rows of expert e.  A workgroup per (expert, column
-// block), as the launch's last workgroups.
-template <typename W>
-__device__ __forceinline__ void zero_padding(const RowArgs& a, const Split& s, uint32_t e, int unroll) {
-    const uint32_t tx = 1u << s.log_tx, ty = threadIdx.x >> s.log_tx, nty = 256u >> s.log_tx;
-    const uint32_t lo = (uint32_t)a.offsets[e] + (uint32_t)a.counts[e];
-    uint32_t hi = (uint32_t)a.offsets[e + 1];
-    hi = hi < a.capacity ? hi : a.capacity;
-    for (uint32_t r = lo + ty; r < hi; r += nty) {
-        W* out = reinterpret_cast<W*>(static_cast<uint8_t*>(a.out) + r * a.out_stride);
-        for (int u = 0; u < unroll; ++u) {
-            const uint32_t j = (blockIdx.y * unroll + u) * tx + (threadIdx.x & (tx - 1));
-            if (j < s.words) out[j] = W{};
-        }
-    }
-}
-
-template <int VB, int U, bool WAVE>
-__global__ __launch_bounds__(256) void dispatch_rows(RowArgs a, Split s) {
-    typedef typename Word<VB>::type W;
-    if (blockIdx.x >= s.token_blocks) {
-        zero_padding<W>(a, s, blockIdx.x - s.token_blocks, U);
-        return;
-    }
-    const uint32_t t = token_of<WAVE>(s), tx = 1u << s.log_tx;
-    if (t >= a.tokens) return;
-    const W* x = reinterpret_cast<const W*>(static_cast<const uint8_t*>(a.x) + t * a.x_stride);
-    const uint32_t j0 = blockIdx.y * U * tx + (threadIdx.x & (tx - 1));
-    W v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (j0 + u * tx < s.words) v[u] = x[j0 + u * tx];
-    const int32_t* row = a.row + (uint64_t)t * a.topk;
-    for (uint32_t k = 0; k < a.topk; ++k) {
-        const uint32_t r = (uint32_t)row[k];
-        if (r >= a.capacity) continue;
-        W* out = reinterpret_cast<W*>(static_cast<uint8_t*>(a.out) + r * a.out_stride);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (j0 + u * tx < s.words) out[j0 + u * tx] = v[u];
-    }
-}
-
-template <typename T, int VB>
+template <typename T>
 struct Pack {
-    static constexpr int N = VB / (int)sizeof(T);
-    typedef typename Word<VB>::type W;
+    static constexpr int N = 16 / (int)sizeof(T);
+    typedef xu32x4 __attribute__((aligned(2))) Word;
     union {
-        W w;
+        xu32x4 w;
         T v[N];
     };
 };
 
-template <typename T, int VB, int U, bool WAVE>
+// What a launch moves past the caches (nontemporal), by its size:
+//   stores from 64 MB on, which the L2s (32 MB) cannot hold for a reader
+//     (940 MB of dispatched rows 207 -> 177 us; the same rows' gradients
+//     237 -> 181; 33 MB 8.6 -> 9.3);
+//   loads from 512 MB on, which the Infinity Cache (256 MB) cannot hold from
+//     their writer (940 MB combined 190 -> 174 us; 33 MB 7.7 -> 9.7).
+// PAST in the kernels below.
+
+// A word of a row, or its last `n` values.
+template <typename T, bool PAST>
+__device__ __forceinline__ Pack<T> load(const T* p, uint32_t n) {
+    typedef Pack<T> P;
+    P x;
+    if (n >= P::N) {
+        if (PAST) x.w = __builtin_nontemporal_load(reinterpret_cast<const typename P::Word*>(p));
+        else x.w = *reinterpret_cast<const typename P::Word*>(p);
+    } else {
+#pragma unroll
+        for (uint32_t i = 0; i < P::N; ++i) x.v[i] = i < n ? p[i] : (T)0.0f;
+    }
+    return x;
+}
+
+template <typename T, bool PAST>
+__device__ __forceinline__ void store(T* p, const Pack<T>& x, uint32_t n) {
+    typedef Pack<T> P;
+    if (n >= P::N) {
+        if (PAST) __builtin_nontemporal_store(x.w, reinterpret_cast<typename P::Word*>(p));
+        else *reinterpret_cast<typename P::Word*>(p) = x.w;
+    } else {
+#pragma unroll
+        for (uint32_t i = 0; i < P::N; ++i)
+            if (i < n) p[i] = x.v[i];
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ T* row_of(const void* base, uint64_t row, uint64_t stride_bytes) {
+    return reinterpret_cast<T*>(const_cast<uint8_t*>(static_cast<const uint8_t*>(base)) + row * stride_bytes);
+}
+
+// How a launch is cut: workgroups of tx columns (words) by 256 / tx tokens, tx
+// a power of two; the column blocks of a token are neighbours.  From 64
+// columns on a wave has one token, whose rows and weights are then scalar
+// loads.
+struct Split {
+    uint32_t log_tx;
+    uint32_t col_blocks;
+    uint32_t blocks;
+    uint32_t pad_blocks;  // workgroups of the padding rows, before the others
+};
+
+struct Place {
+    uint32_t token, col;  // col: first element
+};
+
+template <typename T, bool WAVE>
+__device__ __forceinline__ Place place_of(const Split& s) {
+    const uint32_t block = blockIdx.x - s.pad_blocks;
+    const uint32_t ty = threadIdx.x >> s.log_tx, tx = threadIdx.x & ((1u << s.log_tx) - 1);
+    const uint32_t tb = block / s.col_blocks, cb = block % s.col_blocks;
+    return Place{tb * (256u >> s.log_tx) + (WAVE ? uniform(ty) : ty), ((cb << s.log_tx) + tx) * Pack<T>::N};
+}
+
+// Zeros in the padding rows, kPadSplit workgroups for each expert, a wave for
+// a row.  They are the launch's first workgroups: as its last they ran alone
+// at the end (4756 padding rows of 10 KB added 34 us to a dispatch of 80).
+constexpr uint32_t kPadSplit = 4;
+
+template <typename T>
+__device__ __forceinline__ void zero_padding(const RowArgs& a) {
+    const uint32_t e = blockIdx.x / kPadSplit, first = blockIdx.x % kPadSplit * 4 + uniform(threadIdx.x >> 6);
+    const uint32_t lo = (uint32_t)a.offsets[e] + (uint32_t)a.counts[e];
+    uint32_t hi = (uint32_t)a.offsets[e + 1];
+    hi = hi < a.capacity ? hi : a.capacity;
+    Pack<T> zero;
+    zero.w = xu32x4{};
+    for (uint32_t r = lo + first; r < hi; r += kPadSplit * 4) {
+        T* out = row_of<T>(a.out, r, a.out_stride);
+        for (uint32_t c = __lane_id() * Pack<T>::N; c < a.width; c += 64 * Pack<T>::N)
+            store<T, false>(out + c, zero, a.width - c);
+    }
+}
+
+template <typename T, bool WAVE, bool PAST>
+__global__ __launch_bounds__(256) void dispatch_rows(RowArgs a, Split s) {
+    if (blockIdx.x < s.pad_blocks) {
+        zero_padding<T>(a);
+        return;
+    }
+    const Place at = place_of<T, WAVE>(s);
+    if (at.token >= a.tokens || at.col >= a.width) return;
+    const Pack<T> x = load<T, false>(row_of<const T>(a.x, at.token, a.x_stride) + at.col, a.width - at.col);
+    const int32_t* row = a.row + (uint64_t)at.token * a.topk;
+    for (uint32_t k = 0; k < a.topk; ++k) {
+        const uint32_t r = (uint32_t)row[k];
+        if (r < a.capacity) store<T, PAST>(row_of<T>(a.out, r, a.out_stride) + at.col, x, a.width - at.col);
+    }
+}
+
+template <typename T, bool WAVE, bool PAST>
 __global__ __launch_bounds__(256) void combine_rows(RowArgs a, Split s) {
-    typedef Pack<T, VB> P;
-    const uint32_t t = token_of<WAVE>(s), tx = 1u << s.log_tx;
-    if (t >= a.tokens) return;
-    const uint32_t j0 = blockIdx.y * U * tx + (threadIdx.x & (tx - 1));
-    float acc[U][P::N] = {};
-    const int32_t* row = a.row + (uint64_t)t * a.topk;
-    const float* weight = a.weights ? a.weights + (uint64_t)t * a.topk : nullptr;
+    typedef Pack<T> P;
+    const Place at = place_of<T, WAVE>(s);
+    if (at.token >= a.tokens || at.col >= a.width) return;
+    const uint32_t n = a.width - at.col;
+    float acc[P::N] = {};
+    const int32_t* row = a.row + (uint64_t)at.token * a.topk;
+    const float* weight = a.weights ? a.weights + (uint64_t)at.token * a.topk : nullptr;
 #pragma unroll 4
     for (uint32_t k = 0; k < a.topk; ++k) {
         const uint32_t r = (uint32_t)row[k];
         if (r >= a.capacity) continue;
         const float w = weight ? weight[k] : 1.0f;
-        const typename P::W* x =
-            reinterpret_cast<const typename P::W*>(static_cast<const uint8_t*>(a.x) + r * a.x_stride);
+        const P x = load<T, PAST>(row_of<const T>(a.x, r, a.x_stride) + at.col, n);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (j0 + u * tx < s.words) {
-                P p;
-                p.w = x[j0 + u * tx];
-#pragma unroll
-                for (int i = 0; i < P::N; ++i) acc[u][i] = __builtin_fmaf(w, to_float(p.v[i]), acc[u][i]);
-            }
+        for (int i = 0; i < P::N; ++i) acc[i] = __builtin_fmaf(w, to_float(x.v[i]), acc[i]);
     }
-    typename P::W* y = reinterpret_cast<typename P::W*>(static_cast<uint8_t*>(a.out) + t * a.out_stride);
+    P y;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (j0 + u * tx < s.words) {
-            P p;
-#pragma unroll
-            for (int i = 0; i < P::N; ++i) p.v[i] = (T)acc[u][i];
-            y[j0 + u * tx] = p.w;
-        }
+    for (int i = 0; i < P::N; ++i) y.v[i] = (T)acc[i];
+    store<T, PAST>(row_of<T>(a.out, at.token, a.out_stride) + at.col, y, n);
 }
 
 // One workgroup per token; kGroup slots at a time (dy is read again, from
 // the cache, for every further group).
 constexpr int kGroup = 8;
 
-template <typename T, int VB>
-__global__ __launch_bounds__(256) void combine_rows_backward(RowArgs a, Split s) {
-    typedef Pack<T, VB> P;
-    typedef typename P::W W;
+template <typename T, bool PAST>
+__global__ __launch_bounds__(256) void combine_rows_backward(RowArgs a, uint32_t pad_blocks) {
+    typedef Pack<T> P;
     __shared__ float part[4][kGroup];
-    if (blockIdx.x >= s.token_blocks) {
-        for (uint32_t y = 0; y * 256 < s.words; ++y) {
-            const uint32_t e = blockIdx.x - s.token_blocks;
-            const uint32_t lo = (uint32_t)a.offsets[e] + (uint32_t)a.counts[e];
-            uint32_t hi = (uint32_t)a.offsets[e + 1];
-            hi = hi < a.capacity ? hi : a.capacity;
-            const uint32_t j = y * 256 + threadIdx.x;
-            if (j < s.words)
-                for (uint32_t r = lo; r < hi; ++r)
-                    reinterpret_cast<W*>(static_cast<uint8_t*>(a.out) + r * a.out_stride)[j] = W{};
-        }
+    if (blockIdx.x < pad_blocks) {
+        zero_padding<T>(a);
         return;
     }
-    const uint64_t t = blockIdx.x;
-    const W* dy = reinterpret_cast<const W*>(static_cast<const uint8_t*>(a.x) + t * a.x_stride);
+    const uint64_t t = blockIdx.x - pad_blocks;
+    const T* dy = row_of<const T>(a.x, t, a.x_stride);
     for (uint32_t k0 = 0; k0 < a.topk; k0 += kGroup) {
         uint32_t r[kGroup];
         float w[kGroup], acc[kGroup];
@@ -152,15 +177,14 @@ __global__ __launch_bounds__(256) void combine_rows_backward(RowArgs a, Split s)
             w[g] = k < a.topk && a.weights ? a.weights[t * a.topk + k] : 1.0f;
             acc[g] = 0.0f;
         }
-        for (uint32_t j = threadIdx.x; j < s.words; j += 256) {
-            P d;
-            d.w = dy[j];
+        for (uint32_t c = threadIdx.x * P::N; c < a.width; c += 256 * P::N) {
+            const uint32_t n = a.width - c;
+            const P d = load<T, false>(dy + c, n);
 #pragma unroll
             for (int g = 0; g < kGroup; ++g) {
                 if (r[g] >= a.capacity) continue;
                 if (a.dweights) {
-                    P x;
-                    x.w = reinterpret_cast<const W*>(static_cast<const uint8_t*>(a.rows) + r[g] * a.rows_stride)[j];
+                    const P x = load<T, false>(row_of<const T>(a.rows, r[g], a.rows_stride) + c, n);
 #pragma unroll
                     for (int i = 0; i < P::N; ++i)
                         acc[g] = __builtin_fmaf(to_float(d.v[i]), to_float(x.v[i]), acc[g]);
@@ -169,7 +193,7 @@ __global__ __launch_bounds__(256) void combine_rows_backward(RowArgs a, Split s)
                     P o;
 #pragma unroll
                     for (int i = 0; i < P::N; ++i) o.v[i] = (T)(w[g] * to_float(d.v[i]));
-                    reinterpret_cast<W*>(static_cast<uint8_t*>(a.out) + r[g] * a.out_stride)[j] = o.w;
+                    store<T, PAST>(row_of<T>(a.out, r[g], a.out_stride) + c, o, n);
                 }
             }
         }
@@ -189,99 +213,83 @@ __global__ __launch_bounds__(256) void combine_rows_backward(RowArgs a, Split s)
     }
 }
 
-// Widest word (16, 8, 4 or 2 bytes) that every row start and the row width
-// are multiples of.
-uint32_t word_bytes(uint64_t bits) {
-    return bits & 15 ? bits & 7 ? bits & 3 ? 2 : 4 : 8 : 16;
-}
-
-uint64_t addr(const void* p) { return reinterpret_cast<uintptr_t>(p); }
-
-Split split(uint32_t words, uint32_t tokens, uint32_t unroll) {
-    // the widest tx that leaves the fewest threads without a word
-    uint32_t best = 3, waste = ~0u;
-    for (uint32_t lt = 3; lt <= 8; ++lt) {
-        const uint32_t w = up_to(words, unroll << lt) - words;
-        if (w <= waste) {
+// The widest tx that leaves at most an eighth of the threads without a word,
+// or else the fewest.
+Split split(uint32_t words, uint32_t tokens, uint32_t pad_blocks) {
+    uint32_t best = 0, waste = ~0u;
+    for (uint32_t lt = 0; lt <= 8; ++lt) {
+        const uint32_t w = up_to(words, 1u << lt) - words;
+        if (w * 8 <= words || w <= waste) {
             best = lt;
             waste = w;
         }
     }
-    const uint32_t ty = 256u >> best;
-    return Split{best, words, (tokens + ty - 1) / ty};
+    const uint32_t ty = 256u >> best, cols = (words + (1u << best) - 1) >> best;
+    const uint64_t blocks = (uint64_t)((tokens + ty - 1) / ty) * cols;
+    return Split{best, cols, (uint32_t)(blocks < ~0u ? blocks : ~0u), pad_blocks};
 }
 
-template <int VB, int U>
-void dispatch_as(const RowArgs& a, uint32_t bytes, hipStream_t stream) {
-    const Split s = split(bytes / VB, a.tokens, U);
-    const dim3 grid(s.token_blocks + a.experts, (s.words + (U << s.log_tx) - 1) / (U << s.log_tx));
-    if (s.log_tx >= 6) hipLaunchKernelGGL((dispatch_rows<VB, U, true>), grid, dim3(256), 0, stream, a, s);
-    else hipLaunchKernelGGL((dispatch_rows<VB, U, false>), grid, dim3(256), 0, stream, a, s);
-}
+uint32_t pad_blocks(const RowArgs& a) { return a.counts ? a.experts * kPadSplit : 0; }
 
-template <typename T, int VB, int U>
-void combine_as(const RowArgs& a, hipStream_t stream) {
-    const Split s = split(a.width * (uint32_t)sizeof(T) / VB, a.tokens, U);
-    const dim3 grid(s.token_blocks, (s.words + (U << s.log_tx) - 1) / (U << s.log_tx));
-    if (s.log_tx >= 6) hipLaunchKernelGGL((combine_rows<T, VB, U, true>), grid, dim3(256), 0, stream, a, s);
-    else hipLaunchKernelGGL((combine_rows<T, VB, U, false>), grid, dim3(256), 0, stream, a, s);
+template <typename T>
+uint64_t rows_bytes(const RowArgs& a) { return (uint64_t)a.tokens * a.topk * a.width * sizeof(T); }
+
+constexpr uint64_t kStoresPast = 64ull << 20, kLoadsPast = 512ull << 20;
+
+template <typename T>
+zc_status dispatch_as(const RowArgs& a, hipStream_t stream) {
+    const Split s = split((a.width + Pack<T>::N - 1) / Pack<T>::N, a.tokens, pad_blocks(a));
+    if (!fits((uint64_t)s.blocks + s.pad_blocks)) return ZC_ERR_UNSUPPORTED;
+    auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(s.blocks + s.pad_blocks), dim3(256), 0, stream, a, s);
+        return ZC_OK;
+    };
+    const bool past = rows_bytes<T>(a) >= kStoresPast;
+    if (s.log_tx >= 6) return past ? launch(dispatch_rows<T, true, true>) : launch(dispatch_rows<T, true, false>);
+    return past ? launch(dispatch_rows<T, false, true>) : launch(dispatch_rows<T, false, false>);
 }
 
 template <typename T>
-void combine_type(const RowArgs& a, hipStream_t stream) {
-    const uint64_t bits = addr(a.x) | addr(a.out) | a.x_stride | a.out_stride | (a.width * sizeof(T));
-    switch (word_bytes(bits)) {
-        case 16: combine_as<T, 16, 1>(a, stream); break;
-        case 8: combine_as<T, 8, 2>(a, stream); break;
-        case 4: combine_as<T, 4, 4>(a, stream); break;
-        default:
-            if constexpr (sizeof(T) == 2) combine_as<T, 2, 4>(a, stream);
-    }
-}
-
-template <typename T, int VB>
-void backward_as(const RowArgs& a, hipStream_t stream) {
-    const Split s{8, a.width * (uint32_t)sizeof(T) / VB, a.tokens};
-    const dim3 grid(a.tokens + (a.out ? a.experts : 0));
-    hipLaunchKernelGGL((combine_rows_backward<T, VB>), grid, dim3(256), 0, stream, a, s);
+zc_status combine_as(const RowArgs& a, hipStream_t stream) {
+    const Split s = split((a.width + Pack<T>::N - 1) / Pack<T>::N, a.tokens, 0);
+    if (!fits(s.blocks)) return ZC_ERR_UNSUPPORTED;
+    auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(s.blocks), dim3(256), 0, stream, a, s);
+        return ZC_OK;
+    };
+    const bool past = rows_bytes<T>(a) >= kLoadsPast;
+    if (s.log_tx >= 6) return past ? launch(combine_rows<T, true, true>) : launch(combine_rows<T, true, false>);
+    return past ? launch(combine_rows<T, false, true>) : launch(combine_rows<T, false, false>);
 }
 
 template <typename T>
-void backward_type(const RowArgs& a, hipStream_t stream) {
-    uint64_t bits = addr(a.x) | a.x_stride | (a.width * sizeof(T));
-    if (a.out) bits |= addr(a.out) | a.out_stride;
-    if (a.dweights) bits |= addr(a.rows) | a.rows_stride;
-    switch (word_bytes(bits)) {
-        case 16: backward_as<T, 16>(a, stream); break;
-        case 8: backward_as<T, 8>(a, stream); break;
-        case 4: backward_as<T, 4>(a, stream); break;
-        default:
-            if constexpr (sizeof(T) == 2) backward_as<T, 2>(a, stream);
-    }
+zc_status backward_as(const RowArgs& a, hipStream_t stream) {
+    const uint32_t pads = a.out ? pad_blocks(a) : 0;
+    if (!fits((uint64_t)a.tokens + pads)) return ZC_ERR_UNSUPPORTED;
+    auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(a.tokens + pads), dim3(256), 0, stream, a, pads);
+        return ZC_OK;
+    };
+    return rows_bytes<T>(a) >= kStoresPast ? launch(combine_rows_backward<T, true>) : launch(combine_rows_backward<T, false>);
 }
 
 }  // namespace
 
-void launch_dispatch(const RowArgs& a, uint32_t elem_bytes, hipStream_t stream) {
-    const uint32_t bytes = a.width * elem_bytes;
-    switch (word_bytes(addr(a.x) | addr(a.out) | a.x_stride | a.out_stride | bytes)) {
-        case 16: dispatch_as<16, 1>(a, bytes, stream); break;
-        case 8: dispatch_as<8, 2>(a, bytes, stream); break;
-        case 4: dispatch_as<4, 4>(a, bytes, stream); break;
-        default: dispatch_as<2, 4>(a, bytes, stream); break;
-    }
+zc_status launch_dispatch(const RowArgs& a, uint32_t dtype, hipStream_t stream) {
+    // a copy: 16-bit values of either type are the same
+    return dtype == ZC_FP32 ? dispatch_as<float>(a, stream) : dispatch_as<_Float16>(a, stream);
 }
 
-void launch_combine(const RowArgs& a, uint32_t dtype, hipStream_t stream) {
-    if (dtype == ZC_BF16) combine_type<__bf16>(a, stream);
-    else if (dtype == ZC_FP16) combine_type<_Float16>(a, stream);
-    else combine_type<float>(a, stream);
+zc_status launch_combine(const RowArgs& a, uint32_t dtype, hipStream_t stream) {
+    if (dtype == ZC_BF16) return combine_as<__bf16>(a, stream);
+    if (dtype == ZC_FP16) return combine_as<_Float16>(a, stream);
+    return combine_as<float>(a, stream);
 }
 
-void launch_combine_backward(const RowArgs& a, uint32_t dtype, hipStream_t stream) {
-    if (dtype == ZC_BF16) backward_type<__bf16>(a, stream);
-    else if (dtype == ZC_FP16) backward_type<_Float16>(a, stream);
-    else backward_type<float>(a, stream);
+zc_status launch_combine_backward(const RowArgs& a, uint32_t dtype, hipStream_t stream) {
+    if (dtype == ZC_BF16) return backward_as<__bf16>(a, stream);
+    if (dtype == ZC_FP16) return backward_as<_Float16>(a, stream);
+    return backward_as<float>(a, stream);
 }
 
 }  // namespace zc

@@ -243,8 +243,12 @@ class ExpertPlan:
 
     # checks ---------------------------------------------------------------
     def _routing(self, r: Routing):
-        return (_flat(r[0], "offsets", _I32, self.experts + 1), _flat(r[1], "counts", _I32, self.experts),
-                _flat(r[2], "row", _I32, self.tokens * self.topk))
+        """Pointers of offsets, counts and row; packed segments have no
+        padding rows, which the library is told by counts 0."""
+        row = _flat(r[2], "row", _I32, self.tokens * self.topk)
+        if self.align == 1:
+            return 0, 0, row
+        return _flat(r[0], "offsets", _I32, self.experts + 1), _flat(r[1], "counts", _I32, self.experts), row
 
     def _weights(self, w):
         return 0 if w is None else _flat(w, "weights", _F32, self.tokens * self.topk)
@@ -254,8 +258,9 @@ class ExpertPlan:
         """Enqueue the sorting of ids (int32 [tokens, topk]; outside
         0..experts-1: no row) into routing."""
         p = _flat(ids, "ids", _I32, self.tokens * self.topk)
-        off, cnt, row = self._routing(routing)
-        slot = routing[3]
+        off = _flat(routing[0], "offsets", _I32, self.experts + 1)
+        cnt = _flat(routing[1], "counts", _I32, self.experts)
+        row, slot = _flat(routing[2], "row", _I32, self.tokens * self.topk), routing[3]
         s = _flat(slot, "slot", _I32, self.rows)
         w = _flat(ws, "workspace", torch.uint8, self.workspace_bytes)
         rc = _zc.zc_route(p, self.tokens, self.topk, self.experts, self.align, off, cnt, row, s, slot.numel(), w,

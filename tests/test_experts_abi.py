@@ -73,8 +73,9 @@ def test_row_call_refusals(L):
         a[i] = v
         return f(*a)
 
-    for i in (0, 7, 8, 9, 10):
+    for i in (0, 7, 9, 10):  # counts may be null: no padding rows
         assert rc(d, good, i, None) == BAD, i
+    assert rc(d, good, 8, P + 1) == BAD
     assert rc(d, good, 0, P + 1) == BAD
     assert rc(d, good, 1, 63) == BAD and rc(d, good, 11, 63) == BAD   # strides shorter than a row
     assert rc(d, good, 2, 3) == BAD and rc(d, good, 6, 0) == BAD
@@ -88,7 +89,7 @@ def test_row_call_refusals(L):
     for i, v in ((0, None), (1, 8), (2, P + 1), (3, 9), (7, None), (9, None), (10, 8)):
         assert rc(L.zc_combine, c, i, v) == BAD, (i, v)
     g = [P, 64, P, 64, None, 0, 8, 2, 4, 64, P, P, P, 16, P, 64, P, None]
-    for i, v in ((0, None), (2, None), (3, 1), (10, None), (11, None), (12, None), (15, 1), (16, P + 2)):
+    for i, v in ((0, None), (2, None), (3, 1), (10, None), (11, P + 1), (12, None), (15, 1), (16, P + 2)):
         assert rc(L.zc_combine_backward, g, i, v) == BAD, (i, v)
     neither = list(g)
     neither[14] = neither[16] = None
