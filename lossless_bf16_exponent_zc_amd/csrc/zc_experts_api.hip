@@ -62,7 +62,7 @@ uint64_t zc_route_rows(uint64_t tokens, uint32_t topk, uint32_t experts, uint32_
 
 uint64_t zc_route_workspace_bytes(uint64_t tokens, uint32_t topk, uint32_t experts) {
     if (!route_limits(tokens, topk, experts, 1)) return 0;
-    return up64(route_tiles(tokens * topk) * experts * 4 + 4, 256);
+    return up64((route_tiles(tokens * topk) + 1) * experts * 4, 256);
 }
 
 zc_status zc_route(const int32_t* d_ids, uint64_t tokens, uint32_t topk, uint32_t experts, uint32_t align,

@@ -8,16 +8,19 @@
 // (log2(experts + 1) of them), and keeps a running count per expert in LDS
 // that only it advances, so the order of rows does not depend on timing.
 //
-// Up to kSmall slots one workgroup does everything in one launch; above,
-// three launches: counts per tile, a scan of each expert's tiles, ranks.
+// Up to kSmall slots one workgroup does everything in one launch.  Above, two:
+// counts per tile, then ranks, for which every workgroup adds up the tiles
+// before its own; from kMostSummed tiles on a launch between them scans the
+// tiles once for all.
 #include "zc_experts_kernels.h"
 
 namespace zc {
 
 namespace {
 
-constexpr uint32_t kTile = 1024;     // slots per workgroup of the large form
-constexpr uint32_t kSmall = 8192;    // slots of the one-launch form
+constexpr uint32_t kTile = 2048;       // slots per workgroup of the large form
+constexpr uint32_t kSmall = 2048;      // slots of the one-launch form
+constexpr uint32_t kMostSummed = 128;  // tiles that a workgroup adds up by itself
 
 // Lanes whose key equals the caller's.
 __device__ __forceinline__ uint64_t same_key(uint32_t key, uint32_t bits) {
@@ -52,36 +55,48 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* part, 
     return before + s - v;
 }
 
-// Slots [lo, hi) of one wave, in order: their rows from the wave's running
-// counts `next` (the row of each expert's next slot).
-__device__ __forceinline__ void place(const RouteArgs& a, uint32_t lo, uint32_t hi, uint32_t* next) {
-    const uint32_t lane = __lane_id(), bits = key_bits(a.experts);
-    for (uint32_t i0 = lo; i0 < hi; i0 += 64) {
-        const uint32_t i = i0 + lane;
-        uint32_t key = a.experts;
-        if (i < hi) {
-            const uint32_t id = (uint32_t)a.ids[i];
-            if (id < a.experts) key = id;
-        }
-        const uint64_t m = same_key(key, bits);
-        const uint32_t first = __ffsll((unsigned long long)m) - 1;
-        uint32_t base = 0;
-        if (lane == first && key < a.experts) base = atomicAdd(&next[key], (uint32_t)__popcll(m));
-        base = __shfl(base, first);
-        if (i < hi) {
-            const uint32_t r = base + __popcll(m & ((1ull << lane) - 1));
-            a.row[i] = key < a.experts ? (int32_t)r : -1;
-            if (key < a.experts) a.slot[r] = (int32_t)i;
+// A wave's slots: 64 * R from `lo` on, below `hi`, R of them per lane (the
+// i-th of a lane is lo + 64 i + lane); their ids are read once, at the start.
+template <int R>
+struct Keys {
+    uint32_t key[R];  // expert, or `experts` for none
+    __device__ __forceinline__ Keys(const RouteArgs& a, uint32_t lo, uint32_t hi) {
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const uint32_t i = lo + q * 64 + __lane_id();
+            const uint32_t id = i < hi ? (uint32_t)a.ids[i] : ~0u;
+            key[q] = id < a.experts ? id : a.experts;
         }
     }
-}
-
-__device__ __forceinline__ void count(const RouteArgs& a, uint32_t lo, uint32_t hi, uint32_t* cnt) {
-    for (uint32_t i = lo + __lane_id(); i < hi; i += 64) {
-        const uint32_t id = (uint32_t)a.ids[i];
-        if (id < a.experts) atomicAdd(&cnt[id], 1u);
+    // adds the slots of each expert to cnt
+    __device__ __forceinline__ void count(const RouteArgs& a, uint32_t* cnt) const {
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+            if (key[q] < a.experts) atomicAdd(&cnt[key[q]], 1u);
     }
-}
+    // writes rows and slots; next: the row of each expert's next slot, which
+    // this wave alone advances
+    __device__ __forceinline__ void place(const RouteArgs& a, uint32_t lo, uint32_t hi, uint32_t* next) const {
+        const uint32_t lane = __lane_id(), bits = key_bits(a.experts);
+        uint32_t first[R], rank[R], base[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const uint64_t m = same_key(key[q], bits);
+            first[q] = __ffsll((unsigned long long)m) - 1;
+            rank[q] = __popcll(m & ((1ull << lane) - 1));
+            base[q] = 0;
+            if (lane == first[q] && key[q] < a.experts) base[q] = atomicAdd(&next[key[q]], (uint32_t)__popcll(m));
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const uint32_t i = lo + q * 64 + lane, r = __shfl(base[q], first[q]) + rank[q];
+            if (i < hi) {
+                a.row[i] = key[q] < a.experts ? (int32_t)r : -1;
+                if (key[q] < a.experts) a.slot[r] = (int32_t)i;
+            }
+        }
+    }
+};
 
 // One workgroup of 1024 threads.  LDS: [waves][experts] counts.
 __global__ __launch_bounds__(1024) void route_small(RouteArgs a, uint32_t nwaves) {
@@ -94,7 +109,8 @@ __global__ __launch_bounds__(1024) void route_small(RouteArgs a, uint32_t nwaves
     const uint32_t lo = wave * each < a.nslots ? wave * each : a.nslots;
     const uint32_t hi = lo + each < a.nslots ? lo + each : a.nslots;
     uint32_t* mine = cnt + wave * a.experts;
-    if (wave < nwaves) count(a, lo, hi, mine);
+    const Keys<kSmall / 1024> keys(a, lo, hi);
+    if (wave < nwaves) keys.count(a, mine);
     __syncthreads();
     uint32_t c = 0;
     if (tid < a.experts)
@@ -115,78 +131,106 @@ __global__ __launch_bounds__(1024) void route_small(RouteArgs a, uint32_t nwaves
     if (tid == 0) a.offsets[a.experts] = (int32_t)total;
     for (uint32_t r = total + tid; r < a.capacity; r += 1024) a.slot[r] = -1;
     __syncthreads();
-    if (wave < nwaves) place(a, lo, hi, mine);
+    if (wave < nwaves) keys.place(a, lo, hi, mine);
 }
 
-__global__ __launch_bounds__(256) void route_count(RouteArgs a) {
+__global__ __launch_bounds__(1024) void route_count(RouteArgs a) {
     extern __shared__ uint32_t cnt[];
-    for (uint32_t i = threadIdx.x; i < a.experts; i += 256) cnt[i] = 0;
+    for (uint32_t i = threadIdx.x; i < a.experts; i += 1024) cnt[i] = 0;
     __syncthreads();
-    const uint32_t lo = blockIdx.x * kTile, hi = lo + kTile < a.nslots ? lo + kTile : a.nslots;
-    for (uint32_t i = lo + threadIdx.x; i < hi; i += 256) {
-        const uint32_t id = (uint32_t)a.ids[i];
+    const uint32_t lo = blockIdx.x * kTile;
+#pragma unroll
+    for (uint32_t q = 0; q < kTile / 1024; ++q) {
+        const uint32_t i = lo + q * 1024 + threadIdx.x;
+        const uint32_t id = i < a.nslots ? (uint32_t)a.ids[i] : ~0u;
         if (id < a.experts) atomicAdd(&cnt[id], 1u);
     }
     __syncthreads();
-    for (uint32_t e = threadIdx.x; e < a.experts; e += 256)
-        a.ws[(uint64_t)e * a.tiles + blockIdx.x] = cnt[e];
+    for (uint32_t e = threadIdx.x; e < a.experts; e += 1024) a.ws[(uint64_t)blockIdx.x * a.experts + e] = cnt[e];
 }
 
-// Workgroup e: exclusive sums over the tiles of expert e, and its count.
-__global__ __launch_bounds__(256) void route_scan(RouteArgs a) {
-    __shared__ uint32_t part[4];
-    uint32_t* c = a.ws + (uint64_t)blockIdx.x * a.tiles;
-    uint32_t carry = 0;
-    for (uint32_t t0 = 0; t0 < a.tiles; t0 += 256) {
-        const uint32_t t = t0 + threadIdx.x;
-        const uint32_t v = t < a.tiles ? c[t] : 0u;
-        uint32_t total;
-        const uint32_t before = block_exclusive(v, part, 4, total);
-        if (t < a.tiles) c[t] = carry + before;
-        carry += total;
+// For 64 experts a workgroup: sums over the tiles before each, in place, and
+// after the last tile's the experts' counts.  16 threads share an expert.
+__global__ __launch_bounds__(1024) void route_scan(RouteArgs a) {
+    __shared__ uint32_t part[16][64];
+    const uint32_t lane = threadIdx.x & 63, seg = threadIdx.x >> 6, e = blockIdx.x * 64 + lane;
+    const uint32_t each = (a.tiles + 15) / 16, lo = seg * each, hi = lo + each < a.tiles ? lo + each : a.tiles;
+    uint32_t sum = 0;
+    if (e < a.experts) {
+#pragma unroll 8
+        for (uint32_t t = lo; t < hi; ++t) sum += a.ws[(uint64_t)t * a.experts + e];
     }
-    if (threadIdx.x == 0) a.counts[blockIdx.x] = (int32_t)carry;
+    part[seg][lane] = sum;
+    __syncthreads();
+    if (e >= a.experts) return;
+    uint32_t before = 0, all = 0;
+    for (uint32_t s = 0; s < 16; ++s) {
+        before += s < seg ? part[s][lane] : 0u;
+        all += part[s][lane];
+    }
+#pragma unroll 8
+    for (uint32_t t = lo; t < hi; ++t) {
+        const uint32_t v = a.ws[(uint64_t)t * a.experts + e];
+        a.ws[(uint64_t)t * a.experts + e] = before;
+        before += v;
+    }
+    if (seg == 0) a.ws[(uint64_t)a.tiles * a.experts + e] = all;
 }
 
 // Workgroup b: offsets (every workgroup for itself), then the rows of its
-// tile.  LDS: [4][experts] counts of the waves, which become next rows.
-__global__ __launch_bounds__(256) void route_place(RouteArgs a) {
+// tile.  LDS: [16][experts] counts of the waves, which become next rows.
+__global__ __launch_bounds__(1024) void route_place(RouteArgs a, bool scanned) {
     extern __shared__ uint32_t cnt[];
-    __shared__ uint32_t part[4];
+    __shared__ uint32_t part[16];
     const uint32_t tid = threadIdx.x, wave = uniform(tid >> 6);
-    for (uint32_t i = tid; i < 4 * a.experts; i += 256) cnt[i] = 0;
+    const uint32_t first = blockIdx.x * kTile + wave * (kTile / 16);
+    const uint32_t lo = first < a.nslots ? first : a.nslots;
+    const uint32_t hi = lo + kTile / 16 < a.nslots ? lo + kTile / 16 : a.nslots;
+    const Keys<kTile / 1024> keys(a, lo, hi);
+    for (uint32_t i = tid; i < 16 * a.experts; i += 1024) cnt[i] = 0;
     __syncthreads();
-    const uint32_t first = blockIdx.x * kTile;
-    const uint32_t lo = first + wave * (kTile / 4) < a.nslots ? first + wave * (kTile / 4) : a.nslots;
-    const uint32_t hi = lo + kTile / 4 < a.nslots ? lo + kTile / 4 : a.nslots;
     uint32_t* mine = cnt + wave * a.experts;
-    count(a, lo, hi, mine);
-    __syncthreads();
-    uint32_t carry = 0;
-    for (uint32_t e0 = 0; e0 < a.experts; e0 += 256) {
-        const uint32_t e = e0 + tid;
-        const uint32_t c = e < a.experts ? (uint32_t)a.counts[e] : 0u;
-        const uint32_t padded = up_to(c, a.align);
-        uint32_t total;
-        const uint32_t off = carry + block_exclusive(padded, part, 4, total);
-        carry += total;
-        if (e < a.experts) {
-            uint32_t next = off + a.ws[(uint64_t)e * a.tiles + blockIdx.x];
-            for (uint32_t w = 0; w < 4; ++w) {
-                const uint32_t t = cnt[w * a.experts + e];
-                cnt[w * a.experts + e] = next;
-                next += t;
+    keys.count(a, mine);
+    uint32_t before = 0, c = 0;  // of expert tid: slots in earlier tiles, and in all
+    if (tid < a.experts) {
+        if (scanned) {
+            before = a.ws[(uint64_t)blockIdx.x * a.experts + tid];
+            c = a.ws[(uint64_t)a.tiles * a.experts + tid];
+        } else {
+#pragma unroll 16
+            for (uint32_t t = 0; t < a.tiles; ++t) {
+                const uint32_t v = a.ws[(uint64_t)t * a.experts + tid];
+                c += v;
+                before += t < blockIdx.x ? v : 0u;
             }
-            if (blockIdx.x == e % a.tiles)
-                for (uint32_t r = off + c; r < off + padded; ++r) a.slot[r] = -1;
-            if (blockIdx.x == 0) a.offsets[e] = (int32_t)off;
         }
     }
-    if (blockIdx.x == 0 && tid == 0) a.offsets[a.experts] = (int32_t)carry;
-    for (uint64_t r = (uint64_t)carry + blockIdx.x * 256u + tid; r < a.capacity; r += (uint64_t)a.tiles * 256u)
+    __syncthreads();
+    const uint32_t padded = up_to(c, a.align);
+    uint32_t total;
+    const uint32_t off = block_exclusive(padded, part, 16, total);
+    if (tid < a.experts) {
+        uint32_t next = off + before;
+        uint32_t v[16];
+#pragma unroll
+        for (uint32_t w = 0; w < 16; ++w) v[w] = cnt[w * a.experts + tid];
+#pragma unroll
+        for (uint32_t w = 0; w < 16; ++w) {
+            cnt[w * a.experts + tid] = next;
+            next += v[w];
+        }
+        if (blockIdx.x == tid % a.tiles)
+            for (uint32_t r = off + c; r < off + padded; ++r) a.slot[r] = -1;
+        if (blockIdx.x == 0) {
+            a.offsets[tid] = (int32_t)off;
+            a.counts[tid] = (int32_t)c;
+        }
+    }
+    if (blockIdx.x == 0 && tid == 0) a.offsets[a.experts] = (int32_t)total;
+    for (uint64_t r = (uint64_t)total + blockIdx.x * 1024u + tid; r < a.capacity; r += (uint64_t)a.tiles * 1024u)
         a.slot[r] = -1;
     __syncthreads();
-    place(a, lo, hi, mine);
+    keys.place(a, lo, hi, mine);
 }
 
 }  // namespace
@@ -200,10 +244,11 @@ zc_status launch_route(const RouteArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL(route_small, dim3(1), dim3(1024), nwaves * a.experts * 4u, stream, a, nwaves);
         return ZC_OK;
     }
-    hipLaunchKernelGGL(route_count, dim3(a.tiles), dim3(256), a.experts * 4u, stream, a);
-    hipLaunchKernelGGL(route_scan, dim3(a.experts), dim3(256), 0, stream, a);
-    hipLaunchKernelGGL(route_place, dim3(a.tiles), dim3(256), 4u * a.experts * 4u, stream, a);
-    return ZC_OK;  // at most 2^21 tiles
+    const bool scan = a.tiles >= kMostSummed;
+    hipLaunchKernelGGL(route_count, dim3(a.tiles), dim3(1024), a.experts * 4u, stream, a);
+    if (scan) hipLaunchKernelGGL(route_scan, dim3((a.experts + 63) / 64), dim3(1024), 0, stream, a);
+    hipLaunchKernelGGL(route_place, dim3(a.tiles), dim3(1024), 16u * a.experts * 4u, stream, a, scan);
+    return ZC_OK;  // at most 2^20 tiles of 2^10 threads
 }
 
 }  // namespace zc

@@ -53,7 +53,7 @@ def routed(tokens, topk, experts, align, seed, drop=0.3):
 ROUTES = [
     (1, 1, 1, 1, 0.0), (1, 1, 1, 128, 1.0), (0, 2, 3, 8, 0.0), (3, 2, 5, 1, 0.3), (64, 8, 256, 1, 0.0),
     (65, 1, 2, 16, 0.5), (1000, 64, 3, 1024, 0.9), (1021, 3, 37, 16, 0.5), (1024, 8, 1024, 1, 0.1),
-    (1025, 8, 1000, 4, 0.1), (3001, 7, 255, 128, 0.3), (4096, 9, 1, 1, 0.0), (5000, 2, 1024, 2, 1.0),
+    (1025, 8, 1000, 4, 0.1), (1024, 8, 5, 1, 0.2), (8195, 1, 1024, 8, 0.2), (3001, 7, 255, 128, 0.3), (4096, 9, 1, 1, 0.0), (5000, 2, 1024, 2, 1.0),
 ]
 
 
@@ -66,6 +66,29 @@ def test_route(tokens, topk, experts, align, drop):
     assert np.array_equal(r.row.cpu().numpy(), row)
     got = r.slot.cpu().numpy()
     assert np.array_equal(got[:off[-1]], slot) and (got[off[-1]:] == -1).all()
+
+
+def test_route_of_many_tiles():
+    """Past the tiles that a workgroup adds up by itself: against a stable
+    sort on the GPU (the plain form goes slot by slot)."""
+    tokens, topk, experts, align = 262145, 5, 300, 64
+    plan, ids, r = routed(tokens, topk, experts, align, seed=11)
+    flat = ids.cuda().reshape(-1).long()
+    key = torch.where((flat >= 0) & (flat < experts), flat, experts)
+    order = torch.argsort(key, stable=True)
+    count = torch.bincount(key, minlength=experts + 1)
+    padded = (count[:experts] + align - 1) // align * align
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int64, device="cuda"), padded.cumsum(0)])
+    assert torch.equal(r.counts.long(), count[:experts]) and torch.equal(r.offsets.long(), offsets)
+    n = int(count[:experts].sum())
+    live = order[:n]
+    want = offsets[key[live]] + torch.arange(n, device="cuda") - (count.cumsum(0) - count)[key[live]]
+    row = torch.full_like(flat, -1)
+    row[live] = want
+    assert torch.equal(r.row.reshape(-1).long(), row)
+    slot = torch.full((plan.rows,), -1, dtype=torch.int64, device="cuda")
+    slot[want] = live
+    assert torch.equal(r.slot.long(), slot)
 
 
 ROWS = [  # tokens, topk, experts, align, hidden, dtype, columns beside x's and the rows'
