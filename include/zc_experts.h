@@ -29,8 +29,10 @@
  * (ones past the last block).  Blocks are
  *   1 x 128     (zc_quantize_rows, zc_dispatch_fp8)      one scale row per row,
  *   128 x 128   (zc_quantize_weights)                    one per 128 rows,
- *   128 rows of one column (zc_quantize_columns), stored transposed: then
- *               the matrix [cols, rows] has blocks of 1 x 128.
+ *   128 rows of one column (zc_quantize_columns), stored block by block: for
+ *               128 rows each, data [cols, 128] (a column's 128 values side by
+ *               side) and up(cols,4) scales, so that a product over the rows
+ *               reads whole strips.
  *
  * Conventions are zc.h's: device memory is the caller's; calls only enqueue
  * work on `stream` (no allocation, no synchronisation, no device memory read
@@ -126,10 +128,10 @@ zc_status zc_quantize_weights(const void *d_w, uint32_t dtype, uint32_t experts,
                               uint32_t k, int transpose, void *d_data, void *d_scale,
                               hipStream_t stream);
 
-/* Casts x [rows, cols] in blocks of 128 rows of one column, stored as the
- * blocked matrix [cols, rows].  d_used: as above; blocks that begin there
- * or later are neither read nor written, rows of the last one past it count
- * as zeros. */
+/* Casts x [rows, cols] in blocks of 128 rows of one column: d_data
+ * [ceil(rows/128), cols, 128], d_scale [ceil(rows/128), up(cols,4)]; rows past
+ * the last are zeros.  d_used: as above; blocks that begin there or later are
+ * neither read nor written, rows of the last one past it count as zeros. */
 zc_status zc_quantize_columns(const void *d_x, uint64_t x_stride, uint32_t dtype, uint64_t rows,
                               uint32_t cols, const int32_t *d_used, void *d_data, void *d_scale,
                               hipStream_t stream);
@@ -154,8 +156,8 @@ zc_status zc_expert_product(const void *d_a, const void *d_a_scale, uint64_t row
 
 /*
  * dW[e][i, j] = sum over the blocks b of 128 rows in expert e's segment of
- * sY[i,b] sX[j,b] <Y[i,b], X[j,b]>: Y blocked [n, rows], X blocked [k, rows]
- * as zc_quantize_columns makes them, dW contiguous [experts, n, k] of
+ * sY[i,b] sX[j,b] <Y[b,i], X[b,j]>: Y and X as zc_quantize_columns makes them
+ * from [rows, n] and [rows, k], dW contiguous [experts, n, k] of
  * out_dtype; an expert without rows gets zeros.  Segments begin at multiples
  * of 128 (zc_route with such an align), padding rows are zeros.  d_offsets
  * NULL: one expert, all rows.

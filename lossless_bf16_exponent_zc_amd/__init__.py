@@ -10,12 +10,12 @@ sorts tokens by expert and brings them back, ``expert_product`` and
 """
 from .binding import (EXPORTS, LIB_PATH, Plan, ZcError, check_buffer, lib, prefer_compressed,
                       reduce_native)
-from .experts import (EXPERT_EXPORTS, ExpertPlan, Fp8Blocks, Routing, empty_fp8_columns,
-                      empty_fp8_rows, empty_fp8_weights, expert_product, expert_weight_grad,
+from .experts import (EXPERT_EXPORTS, ExpertPlan, Fp8Blocks, Fp8Columns, Routing,
+                      empty_fp8_columns, empty_fp8_rows, empty_fp8_weights, expert_product, expert_weight_grad,
                       quantize_columns, quantize_rows, quantize_weights)
 
 __all__ = ["EXPORTS", "LIB_PATH", "Plan", "ZcError", "check_buffer", "lib", "prefer_compressed",
            "reduce_native",
-           "EXPERT_EXPORTS", "ExpertPlan", "Fp8Blocks", "Routing", "empty_fp8_columns",
+           "EXPERT_EXPORTS", "ExpertPlan", "Fp8Blocks", "Fp8Columns", "Routing", "empty_fp8_columns",
            "empty_fp8_rows", "empty_fp8_weights", "expert_product", "expert_weight_grad",
            "quantize_columns", "quantize_rows", "quantize_weights"]

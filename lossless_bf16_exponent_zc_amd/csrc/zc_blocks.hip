@@ -176,7 +176,8 @@ __global__ __launch_bounds__(256) void cast_tile(CastTileArgs a, uint32_t row_ti
     const uint32_t or0 = (MODE == kWeights ? rt : ct) * 128, ob = MODE == kWeights ? ct : rt;
     const uint32_t orows = MODE == kColumns ? a.cols : a.rows;
     const uint32_t blocks = MODE == kWeights ? col_tiles : row_tiles;
-    uint8_t* data = a.data + (uint64_t)e * orows * a.data_stride;
+    // columns: block ob is [cols][128] bytes
+    uint8_t* data = MODE == kColumns ? a.data + (uint64_t)ob * orows * 128 : a.data + (uint64_t)e * orows * a.data_stride;
     if (MODE == kWeights) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -200,21 +201,21 @@ __global__ __launch_bounds__(256) void cast_tile(CastTileArgs a, uint32_t row_ti
         for (int i = 0; i < 4; ++i) {
             const uint32_t r = i * 32 + (tid >> 3), c = (tid & 7) * 16;
             if (or0 + r < orows)
-                *reinterpret_cast<xu32x4*>(data + (uint64_t)(or0 + r) * a.data_stride + ob * 128 + c) =
+                *reinterpret_cast<xu32x4*>(data + (MODE == kColumns ? (uint64_t)(or0 + r) * 128 : (uint64_t)(or0 + r) * a.data_stride + ob * 128) + c) =
                     *reinterpret_cast<const xu32x4*>(turn + r * 144 + c);
         }
     }
-    // scales, and ones past the last block
+    // scales; ones past the last block, or past the last column
     if (MODE == kColumns) {
-        if (rg == 0)
+        if (rg == 0) {
+            const uint32_t c = or0 + cg * 8;
+            uint8_t* s = a.scale + (uint64_t)ob * a.scale_stride + c;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c0 + j < orows) {
-                    uint8_t* s = a.scale + (uint64_t)(c0 + j) * a.scale_stride;
-                    s[ob] = (uint8_t)sbyte[j];
-                    if (ob == blocks - 1)
-                        for (uint32_t b = blocks; b < a.scale_stride; ++b) s[b] = 127;
-                }
+            for (int h = 0; h < 2; ++h)  // columns past the last are zeros, and so have scale 1
+                if (c + h * 4 < a.scale_stride)
+                    *reinterpret_cast<uint32_t*>(s + h * 4) = sbyte[h * 4] | sbyte[h * 4 + 1] << 8 | sbyte[h * 4 + 2] << 16 |
+                                                              sbyte[h * 4 + 3] << 24;
+        }
     } else if (tid == 0) {
         uint8_t* s = a.scale + ((uint64_t)e * orow_tiles + or0 / 128) * a.scale_stride;
         s[ob] = (uint8_t)sbyte[0];

@@ -222,7 +222,7 @@ zc_status zc_quantize_columns(const void* d_x, uint64_t x_stride, uint32_t dtype
         return ZC_ERR_INVALID_ARG;
     const uint32_t eb = elem_bytes(dtype);
     const CastTileArgs a{d_x, x_stride, static_cast<uint8_t*>(d_data), static_cast<uint8_t*>(d_scale), d_used,
-                         (uint32_t)rows, cols, 1, stored((uint32_t)rows), scales((uint32_t)rows), 0};
+                         (uint32_t)rows, cols, 1, 128, up_to(cols, 4), 0};
     return finished(launch_cast_columns(a, dtype, stream));
 }
 
@@ -240,8 +240,7 @@ zc_status zc_expert_product(const void* d_a, const void* d_a_scale, uint64_t row
         return ZC_ERR_INVALID_ARG;
     const ProductArgs a{static_cast<const uint8_t*>(d_a), static_cast<const uint8_t*>(d_a_scale),
                         static_cast<const uint8_t*>(d_w), static_cast<const uint8_t*>(d_w_scale), d_offsets, d_counts,
-                        d_out, out_stride, (uint32_t)rows, experts, n, stored(k), scales(k), scales(k), out_dtype,
-                        aligned(d_out, 16) && out_stride * elem_bytes(out_dtype) % 16 == 0};
+                        d_out, out_stride, (uint32_t)rows, experts, n, stored(k), scales(k), scales(k), out_dtype};
     return finished(launch_product(a, stream));
 }
 
@@ -257,8 +256,7 @@ zc_status zc_expert_weight_grad(const void* d_y, const void* d_y_scale, const vo
         return ZC_ERR_INVALID_ARG;
     const WeightGradArgs a{static_cast<const uint8_t*>(d_y), static_cast<const uint8_t*>(d_y_scale),
                            static_cast<const uint8_t*>(d_x), static_cast<const uint8_t*>(d_x_scale), d_offsets, d_dw,
-                           stored((uint32_t)rows), experts, n, k, scales((uint32_t)rows), out_dtype,
-                           aligned(d_dw, 16) && (uint64_t)k * elem_bytes(out_dtype) % 16 == 0};
+                           stored((uint32_t)rows), experts, n, k, up_to(n, 4), up_to(k, 4), out_dtype};
     return finished(launch_weight_grad(a, stream));
 }
 

@@ -65,7 +65,7 @@ struct CastTileArgs {
     const int32_t* used;
     uint32_t rows, cols;   // weights: n, k of the result; columns: rows, cols of x
     uint32_t experts;
-    uint32_t data_stride, scale_stride;
+    uint32_t data_stride, scale_stride;  // columns: scale_stride alone
     uint32_t transpose;
 };
 
@@ -81,20 +81,19 @@ struct ProductArgs {
     uint32_t rows, experts, n, k;  // k: stored, a multiple of 128
     uint32_t a_scale_stride, w_scale_stride;
     uint32_t out_dtype;
-    uint32_t wide;           // out and its rows start at 16-byte addresses
 };
 
 struct WeightGradArgs {
-    const uint8_t* y;        // [n, rows] bytes
-    const uint8_t* y_scale;
-    const uint8_t* x;        // [k, rows] bytes
+    const uint8_t* y;        // [rows / 128][n][128] bytes
+    const uint8_t* y_scale;  // [rows / 128][y_scale_stride]
+    const uint8_t* x;        // [rows / 128][k][128]
     const uint8_t* x_scale;
     const int32_t* offsets;
     void* dw;
     uint32_t rows;           // stored, a multiple of 128
-    uint32_t experts, n, k, scale_stride;
+    uint32_t experts, n, k;
+    uint32_t y_scale_stride, x_scale_stride;
     uint32_t out_dtype;
-    uint32_t wide;
 };
 
 // Each enqueues its kernels, or returns ZC_ERR_UNSUPPORTED and enqueues none

@@ -7,6 +7,8 @@
 // the scales cost no arithmetic and the sum over blocks stays in the unit's
 // 32-bit accumulators.  The weight side is the instruction's first operand:
 // a lane then has four neighbouring columns j of one row r.
+#include <stdlib.h>
+
 #include "zc_experts_kernels.h"
 
 namespace zc {
@@ -25,11 +27,12 @@ __device__ __forceinline__ i32x8 two(xu32x4 lo, xu32x4 hi) {
 struct Tile {
     const uint8_t* a;         // first row of the token side, at its first block
     const uint8_t* w;         // first row of the weight side, at its first block
-    const uint8_t* as;        // scale rows of the token side, from its first row
-    const uint8_t* ws;        // scale rows of the weight side, from its first row's
+    const uint8_t* as;        // their scales: by row (four blocks to a word), or
+    const uint8_t* ws;        // by block (four rows to a word)
     uint32_t a_rows, w_rows;  // rows that exist from there on
-    uint32_t a_stride, w_stride, as_stride, ws_stride;
-    uint32_t first_block;     // of the scale rows
+    uint32_t a_stride, w_stride;    // bytes between rows
+    uint64_t a_block, w_block;      // bytes between blocks
+    uint32_t as_stride, ws_stride;  // bytes between scale rows, or scale blocks
     uint32_t blocks;
 };
 
@@ -180,13 +183,14 @@ __device__ __forceinline__ Found find_tile(const ProductArgs& p, uint32_t index,
 }
 
 // The shape of a tile: 4 waves as WM x WN, each TM x TN instruction tiles of
-// 16 x 16; S stages of one block (128 bytes of every row, and a word of four
-// scale bytes for each) in LDS.  WROW: every row of the weight side has its
-// own scales (else one per 128 rows).
-template <int WM_, int TM_, int TN_, int S_, bool WROW_>
+// 16 x 16; S stages of one block (128 bytes of every row, and the scales) in
+// LDS.  BY_BLOCK: scales lie by block, a byte for every row of either side;
+// else by row, four blocks' bytes to a word, and 128 rows of the weight side
+// share one.
+template <int WM_, int TM_, int TN_, int S_, bool BY_BLOCK_>
 struct Shape {
     static constexpr int WM = WM_, WN = 4 / WM_, TM = TM_, TN = TN_, S = S_;
-    static constexpr bool WROW = WROW_;
+    static constexpr bool BY_BLOCK = BY_BLOCK_;
     static constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
     static constexpr int kScaleAt = (BM + BN) * 128;
     static constexpr int kStage = kScaleAt + 2048;
@@ -200,7 +204,6 @@ struct Out {
     T* out;              // row 0, column 0 of the tile
     uint64_t stride;     // elements
     uint32_t rows, cols; // of the tile that exist
-    uint32_t wide;       // rows start at 16-byte addresses
 };
 
 // From here to the kernels the code uses types and registers that only the
@@ -264,28 +267,33 @@ __device__ __forceinline__ void tile_product(const Tile& t, uint8_t* lds, f32x4 
         const uint32_t row = (wave * NW + i) * 8 + (lane >> 3);
         at_w[i] = (row < t.w_rows ? row : t.w_rows - 1) * t.w_stride + (((lane & 7) ^ turn_w(row)) << 4);
     }
-    const uint32_t srow = wave * 64 + lane;  // whose scales the lane brings
+    // scales: by row, a lane brings its row's word of four blocks; by block, a
+    // lane brings four rows' bytes, and every wave all of them for itself
+    const uint32_t srow = SH::BY_BLOCK ? lane * 4 : wave * 64 + lane;
     const uint32_t last_a = t.a_rows < SH::BM ? t.a_rows - 1 : SH::BM - 1;
-    const uint32_t at_as = (srow < last_a ? srow : last_a) * t.as_stride;
-    const uint32_t wrow = srow < t.w_rows ? srow : t.w_rows - 1;
-    const uint32_t at_ws = (SH::WROW ? wrow : wrow >> 7) * t.ws_stride;
-    const __amdgpu_buffer_rsrc_t ra = buffer(t.a), rw = buffer(t.w), ras = buffer(t.as), rws = buffer(t.ws);
+    const uint32_t last_w = t.w_rows < SH::BN ? t.w_rows - 1 : SH::BN - 1;
+    const uint32_t arow = srow < last_a ? srow : last_a, wrow = srow < last_w ? srow : last_w;
+    const uint32_t at_as = SH::BY_BLOCK ? arow & ~3u : arow * t.as_stride;
+    const uint32_t at_ws = SH::BY_BLOCK ? wrow & ~3u : (wrow >> 7) * t.ws_stride;
 
     // the n-th of a wave's loads of a block; blocks past the last are loaded
     // again, so that the loads in flight do not depend on where the loop stands
     auto load_one = [&](int n, uint32_t block, uint8_t* base) {
-        const uint32_t word = (t.first_block + block) & ~3u;
+        const uint64_t sa = SH::BY_BLOCK ? (uint64_t)block * t.as_stride : block & ~3u;
+        const uint64_t sw = SH::BY_BLOCK ? (uint64_t)block * t.ws_stride : block & ~3u;
         if (n < NA)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(base + (wave * NA + n) * 1024), 16, at_a[n],
-                                                     block * 128, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(t.a + block * t.a_block),
+                                                     (lds_void*)(base + (wave * NA + n) * 1024), 16, at_a[n], 0, 0, 0);
         else if (n < NA + NW)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(base + SH::BM * 128 + (wave * NW + n - NA) * 1024), 16,
-                                                     at_w[n - NA], block * 128, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(t.w + block * t.w_block),
+                                                     (lds_void*)(base + SH::BM * 128 + (wave * NW + n - NA) * 1024), 16,
+                                                     at_w[n - NA], 0, 0, 0);
         else if (n == NA + NW)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ras, (lds_void*)(base + SH::kScaleAt + wave * 256), 4, at_as, word, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(t.as + sa), (lds_void*)(base + SH::kScaleAt + wave * 256), 4,
+                                                     at_as, 0, 0, 0);
         else if (n == NA + NW + 1)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rws, (lds_void*)(base + SH::kScaleAt + 1024 + wave * 256), 4, at_ws,
-                                                     word, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(t.ws + sw), (lds_void*)(base + SH::kScaleAt + 1024 + wave * 256),
+                                                     4, at_ws, 0, 0, 0);
     };
     auto clamped = [&](uint32_t block) { return block < t.blocks ? block : t.blocks - 1; };
 
@@ -294,21 +302,22 @@ __device__ __forceinline__ void tile_product(const Tile& t, uint8_t* lds, f32x4 
     const uint32_t a_lo = (wave_a + r) * 128 + ((g ^ turn_a(r)) << 4), a_hi = a_lo ^ 64;
     const uint32_t w_lo = SH::BM * 128 + (wave_w + weight_row(0, r)) * 128 + ((g ^ turn_w(weight_row(0, r))) << 4);
     const uint32_t w_hi = w_lo ^ 64;
-    const uint32_t a_scale = SH::kScaleAt + (wave_a + r) * 4;
-    const uint32_t w_scale = SH::kScaleAt + 1024 + (SH::WROW ? wave_w + weight_row(0, r) : wave_w) * 4;
+    const uint32_t a_scale = SH::kScaleAt + (SH::BY_BLOCK ? wave * 256 + wave_a + r : (wave_a + r) * 4);
+    const uint32_t w_scale = SH::kScaleAt + 1024 + (SH::BY_BLOCK ? wave * 256 + wave_w + weight_row(0, r) : wave_w * 4);
 
     struct Side {     // 16 rows of one block
         i32x8 v;
-        uint32_t s;   // four blocks' scale bytes
+        uint32_t s;   // the block's scale, or four blocks' scales
     };
     auto read_a = [&](const uint8_t* base, int j) {
         return Side{two(*(const xu32x4*)(base + a_lo + j * 2048), *(const xu32x4*)(base + a_hi + j * 2048)),
-                    *(const uint32_t*)(base + a_scale + j * 64)};
+                    SH::BY_BLOCK ? base[a_scale + j * 16] : *(const uint32_t*)(base + a_scale + j * 64)};
     };
     auto read_w = [&](const uint8_t* base, int i, Side& x) {
         const uint32_t row = (i >> 1) * 32 + (i & 1) * 4;
         x.v = two(*(const xu32x4*)(base + w_lo + row * 128), *(const xu32x4*)(base + w_hi + row * 128));
-        if (SH::WROW || i == 0) x.s = *(const uint32_t*)(base + w_scale + row * 4);
+        if (SH::BY_BLOCK) x.s = base[w_scale + row];
+        else if (i == 0) x.s = *(const uint32_t*)(base + w_scale);
     };
 
     uint8_t* base = lds;
@@ -331,12 +340,12 @@ __device__ __forceinline__ void tile_product(const Tile& t, uint8_t* lds, f32x4 
     constexpr int HALF = SH::TM / 4 * 2, kEach = HALF ? (SH::TM - 2 + HALF) / HALF : 0;
     constexpr int kRest = (SH::TM - HALF) * SH::TN;
     for (uint32_t b = 0; b < t.blocks; ++b) {
-        const uint32_t shift = ((t.first_block + b) & 3) * 8;
+        const uint32_t shift = SH::BY_BLOCK ? 0 : (b & 3) * 8;
         uint32_t sw[SH::TN];
         Side a[SH::TM];
         a[0] = first;
 #pragma unroll
-        for (int i = 0; i < SH::TN; ++i) sw[i] = SH::WROW || i == 0 ? w[i].s >> shift : sw[0];
+        for (int i = 0; i < SH::TN; ++i) sw[i] = SH::BY_BLOCK || i == 0 ? w[i].s >> shift : sw[0];
 #pragma unroll
         for (int j = 0; j < HALF; ++j) {
 #pragma unroll
@@ -392,14 +401,16 @@ __device__ __forceinline__ f32x4 late(f32x4 v) {
     return v;
 }
 
-// A tile with all its columns, at aligned rows, leaves from the registers: 8
-// neighbouring columns per lane.  Any other goes over LDS, 16 rows at a time,
-// and leaves row by row, neighbouring lanes in neighbouring columns.
+// A tile with all its columns leaves from the registers, 8 neighbouring columns
+// per lane, in 16-byte words at whatever address a row starts.  One that ends
+// early goes over LDS, 16 rows at a time, and leaves row by row, neighbouring
+// lanes in neighbouring columns.
 template <typename T, typename SH>
 __device__ __forceinline__ void store_tile(const Out<T>& o, const f32x4 (&acc)[SH::TM][SH::TN], uint8_t* lds) {
     const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const uint32_t m0 = (wave / SH::WN) * SH::TM * 16, n0 = (wave % SH::WN) * SH::TN * 16;
-    if (o.wide && o.cols >= (uint32_t)SH::BN) {
+    if (o.cols >= (uint32_t)SH::BN) {
+        typedef xu32x4 __attribute__((aligned(2))) Word;
         T* p = o.out + (m0 + r) * o.stride + n0 + g * 8;
 #pragma unroll
         for (int j = 0; j < SH::TM; ++j) {
@@ -417,7 +428,7 @@ __device__ __forceinline__ void store_tile(const Out<T>& o, const f32x4 (&acc)[S
                         u.v[4 + q] = (T)hi[q];
                     }
 #pragma unroll
-                    for (int q = 0; q < (int)sizeof(T) / 2; ++q) reinterpret_cast<xu32x4*>(p + i * 16)[q] = u.w[q];
+                    for (int q = 0; q < (int)sizeof(T) / 2; ++q) reinterpret_cast<Word*>(p + i * 16)[q] = u.w[q];
                 }
             }
             p += 16 * o.stride;
@@ -437,9 +448,11 @@ __device__ __forceinline__ void store_tile(const Out<T>& o, const f32x4 (&acc)[S
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         const uint32_t m = m0 + j * 16, rows = m < o.rows ? (o.rows - m < 16 ? o.rows - m : 16) : 0;
 #pragma unroll 1
-        for (uint32_t q = 0; q < rows; ++q)
-#pragma unroll 1
-            for (uint32_t c = lane; c < cols; c += 64) o.out[(m + q) * o.stride + n0 + c] = (T)buf[q * kPitch + c];
+        for (uint32_t c = lane; c < cols; c += 64) {
+            T* p = o.out + m * o.stride + n0 + c;
+#pragma unroll 8
+            for (uint32_t q = 0; q < rows; ++q, p += o.stride) *p = (T)buf[q * kPitch + c];
+        }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -461,22 +474,6 @@ __device__ __forceinline__ void run_tile(const Tile& t, const Out<T>& o, uint8_t
 #endif
 }
 
-constexpr uint32_t kTileRows = 256, kTileCols = 256;
-
-// Workgroup -> (slot of token rows, tile of columns).  Neighbouring workgroup
-// indexes go to different XCDs; the eight XCDs take turns at runs of 32 tiles,
-// 4 slots by 8 columns, so that what an XCD's 32 CUs read at one time is 4 + 8
-// strips of 256 rows, shared through its L2.
-struct Place {
-    uint32_t slot, col;
-};
-__device__ __forceinline__ Place place_of(uint32_t index, uint32_t col_tiles) {
-    const uint32_t xcd = index & 7, l = index >> 3;
-    const uint32_t tile = ((l >> 5) * 8 + xcd) * 32 + (l & 31);
-    const uint32_t group = tile / (4 * col_tiles), in = tile % (4 * col_tiles);
-    return Place{group * 4 + (in & 3), in >> 2};
-}
-
 // Padding rows after the segment's last slot; cols of them from o.
 template <typename T>
 __device__ __forceinline__ void zero_padding(const Out<T>& o, const Found& f, uint32_t rows, uint32_t cols) {
@@ -496,13 +493,13 @@ __global__ __launch_bounds__(256, 1) void product(ProductArgs p, uint32_t col_ti
     if (!f.any) return;
     const uint32_t n0 = f.col * Cut::kCols;
     const uint32_t wrows = (p.n + 127) / 128;
-    const Out<T> o{static_cast<T*>(p.out) + (uint64_t)f.row * p.out_stride + n0, p.out_stride, f.count, p.n - n0, p.wide};
+    const Out<T> o{static_cast<T*>(p.out) + (uint64_t)f.row * p.out_stride + n0, p.out_stride, f.count, p.n - n0};
     if (f.count) {
         const Tile t{p.a + (uint64_t)f.row * p.k,
                      p.w + ((uint64_t)f.expert * p.n + n0) * p.k,
                      p.a_scale + (uint64_t)f.row * p.a_scale_stride,
                      p.w_scale + ((uint64_t)f.expert * wrows + n0 / 128) * p.w_scale_stride,
-                     f.count, p.n - n0, p.k, p.k, p.a_scale_stride, p.w_scale_stride, 0, p.k / 128};
+                     f.count, p.n - n0, p.k, p.k, 128, 128, p.a_scale_stride, p.w_scale_stride, p.k / 128};
         if constexpr (Cut::kRows == 256) {
             if (f.count > 128) run_tile<Shape<2, 8, 8, 2, false>>(t, o, lds);
             else if (f.count > 64) run_tile<Shape<2, 4, 8, 3, false>>(t, o, lds);
@@ -582,16 +579,11 @@ __device__ __forceinline__ void few_tile(const ProductArgs& p, const Found& f, u
             for (int h = 0; h < 2; ++h) v[h] += lds[(q * TM * 16 + row) * kPitch + c + h];
         if (row < f.count) {
             T* out = o.out + row * o.stride + c;
-            if (o.wide && c + 1 < o.cols) {
-                struct alignas(2 * sizeof(T)) Two {
-                    T v[2];
-                };
-                *reinterpret_cast<Two*>(out) = Two{{(T)v[0], (T)v[1]}};
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (c + h < o.cols) out[h] = (T)v[h];
-            }
+            struct Two {  // at any element's address
+                T v[2];
+            };
+            if (c + 1 < o.cols) *reinterpret_cast<Two*>(out) = Two{{(T)v[0], (T)v[1]}};
+            else if (c < o.cols) *out = (T)v[0];
         }
     }
 #endif
@@ -603,33 +595,63 @@ __global__ __launch_bounds__(256, 2) void product_few(ProductArgs p, uint32_t co
     const Found f = find_tile<FewCut>(p, blockIdx.x, col_tiles, kInOrder, reinterpret_cast<uint32_t*>(lds));
     if (!f.any) return;
     const uint32_t n0 = f.col * FewCut::kCols;
-    const Out<T> o{static_cast<T*>(p.out) + (uint64_t)f.row * p.out_stride + n0, p.out_stride, f.count, p.n - n0, p.wide};
+    const Out<T> o{static_cast<T*>(p.out) + (uint64_t)f.row * p.out_stride + n0, p.out_stride, f.count, p.n - n0};
     if (f.count > 32) few_tile<T, 4>(p, f, n0, o, lds);
     else if (f.count > 16) few_tile<T, 2>(p, f, n0, o, lds);
     else if (f.count) few_tile<T, 1>(p, f, n0, o, lds);
     zero_padding(o, f, FewCut::kRows, FewCut::kCols);
 }
 
-template <typename T>
-__global__ __launch_bounds__(256, 1) void weight_grad(WeightGradArgs p, uint32_t row_tiles, uint32_t col_tiles) {
+// Workgroup -> (slot of rows of Y, tile of columns) in runs of 32 tiles, 4 slots
+// by 8 columns, that the eight XCDs take in turn, so that what an XCD's 32 CUs
+// read at one time is 4 + 8 strips, shared through its L2.
+struct Place {
+    uint32_t slot, col;
+};
+__device__ __forceinline__ Place place_of(uint32_t index, uint32_t cols) {
+    const uint32_t xcd = index & 7, n = index >> 3;
+    const uint32_t tile = ((n >> 5) * 8 + xcd) * 32 + (n & 31);
+    const uint32_t group = tile / (4 * cols), in = tile % (4 * cols);
+    return Place{group * 4 + (in & 3), in >> 2};
+}
+
+template <typename T, typename SH>
+__global__ __launch_bounds__(256, 1) void weight_grad(WeightGradArgs p, uint32_t row_tiles, uint32_t col_tiles, Order order) {
     extern __shared__ __align__(16) uint8_t lds[];
-    const uint32_t padded = (row_tiles + 3) / 4 * 4;
-    const Place where = place_of(blockIdx.x, col_tiles);
-    const uint32_t e = where.slot / padded, i0 = where.slot % padded * kTileRows, j0 = where.col * kTileCols;
-    if (e >= p.experts || i0 >= p.n) return;
+    Place where;
+    uint32_t e, i0;
+    if (order == kRuns) {
+        const uint32_t padded = (row_tiles + 3) / 4 * 4;  // an expert's slots, in whole runs
+        where = place_of(blockIdx.x, col_tiles);
+        e = where.slot / padded;
+        i0 = where.slot % padded * SH::BM;
+        if (e >= p.experts || i0 >= p.n) return;
+    } else {
+        where.col = blockIdx.x % col_tiles;
+        where.slot = blockIdx.x / col_tiles;
+        e = where.slot / row_tiles;
+        i0 = where.slot % row_tiles * SH::BM;
+    }
+    const uint32_t j0 = where.col * SH::BN;
     uint32_t b0 = 0, b1 = p.rows / 128;
     if (p.offsets) {
         b0 = clamp_to(p.offsets[e], 0, p.rows) / 128;
         b1 = (clamp_to(p.offsets[e + 1], b0 * 128, p.rows) + 127) / 128;
     }
-    const Tile t{p.y + (uint64_t)i0 * p.rows + b0 * 128,
-                 p.x + (uint64_t)j0 * p.rows + b0 * 128,
-                 p.y_scale + (uint64_t)i0 * p.scale_stride,
-                 p.x_scale + (uint64_t)j0 * p.scale_stride,
-                 p.n - i0, p.k - j0, p.rows, p.rows, p.scale_stride, p.scale_stride, b0, b1 - b0};
-    const Out<T> o{static_cast<T*>(p.dw) + ((uint64_t)e * p.n + i0) * p.k + j0, p.k, p.n - i0, p.k - j0, p.wide};
-    run_tile<Shape<2, 8, 8, 2, true>>(t, o, lds);
+    // block b of Y: [n][128] bytes, and n scale bytes
+    const Tile t{p.y + ((uint64_t)b0 * p.n + i0) * 128,
+                 p.x + ((uint64_t)b0 * p.k + j0) * 128,
+                 p.y_scale + (uint64_t)b0 * p.y_scale_stride + i0,
+                 p.x_scale + (uint64_t)b0 * p.x_scale_stride + j0,
+                 p.n - i0, p.k - j0, 128, 128, (uint64_t)p.n * 128, (uint64_t)p.k * 128,
+                 p.y_scale_stride, p.x_scale_stride, b1 - b0};
+    const Out<T> o{static_cast<T*>(p.dw) + ((uint64_t)e * p.n + i0) * p.k + j0, p.k, p.n - i0, p.k - j0};
+    run_tile<SH>(t, o, lds);
 }
+
+typedef Shape<2, 8, 8, 2, true> GradWide;
+typedef Shape<2, 4, 4, 4, true> GradMid;
+typedef Shape<2, 2, 2, 7, true> GradSmall;
 
 constexpr int kLdsProduct = Shape<1, 2, 4, 4, false>::kLds > Shape<2, 4, 8, 3, false>::kLds ? Shape<1, 2, 4, 4, false>::kLds
                                                                                            : Shape<2, 4, 8, 3, false>::kLds;
@@ -639,15 +661,12 @@ static_assert(kLdsProduct <= 160 * 1024 && Shape<2, 8, 8, 2, false>::kLds <= kLd
 constexpr int kLdsMid = Shape<2, 4, 4, 4, false>::kLds;
 static_assert(Shape<1, 4, 2, 4, false>::kLds <= kLdsMid, "one LDS allocation serves every shape");
 constexpr int kLdsSmall = Shape<2, 2, 2, 8, false>::kLds;
-constexpr int kLdsGrad = Shape<2, 8, 8, 2, true>::kLds;
 
 // More LDS than the default limit has to be asked for, once per device.
 template <typename K>
 void allow_lds(K kernel, int bytes) {
     (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
-
-uint32_t runs_of_32(uint64_t tiles) { return (uint32_t)((tiles + 255) / 256 * 256); }
 
 }  // namespace
 
@@ -705,19 +724,35 @@ zc_status launch_product(const ProductArgs& a, hipStream_t stream) {
     return product_as<float>(a, stream);
 }
 
-zc_status launch_weight_grad(const WeightGradArgs& a, hipStream_t stream) {
-    const uint32_t rows = (a.n + kTileRows - 1) / kTileRows, cols = (a.k + kTileCols - 1) / kTileCols;
-    const uint64_t slots = (uint64_t)a.experts * ((rows + 3) / 4 * 4);
-    if (!fits(slots * cols + 256)) return ZC_ERR_UNSUPPORTED;
-    const dim3 grid(runs_of_32(slots * cols));
-    auto launch = [&](auto kernel) {
-        allow_lds(kernel, kLdsGrad);
-        hipLaunchKernelGGL(kernel, grid, dim3(256), kLdsGrad, stream, a, rows, cols);
+namespace {
+
+template <typename T>
+zc_status weight_grad_as(const WeightGradArgs& a, hipStream_t stream) {
+    auto launch = [&](auto shape) {
+        typedef decltype(shape) SH;
+        const uint32_t rows = (a.n + SH::BM - 1) / SH::BM, cols = (a.k + SH::BN - 1) / SH::BN;
+        const uint64_t tiles = (uint64_t)a.experts * rows * cols;
+        const Order order = tiles > 512 ? kRuns : kInOrder;
+        const uint64_t grid = order == kRuns ? ((uint64_t)a.experts * ((rows + 3) / 4 * 4) * cols + 255) / 256 * 256 : tiles;
+        if (!fits(grid)) return ZC_ERR_UNSUPPORTED;
+        allow_lds(weight_grad<T, SH>, SH::kLds);
+        hipLaunchKernelGGL((weight_grad<T, SH>), dim3((uint32_t)grid), dim3(256), SH::kLds, stream, a, rows, cols, order);
         return ZC_OK;
     };
-    if (a.out_dtype == ZC_BF16) return launch(weight_grad<__bf16>);
-    if (a.out_dtype == ZC_FP16) return launch(weight_grad<_Float16>);
-    return launch(weight_grad<float>);
+    auto tiles = [&](uint32_t side) { return (uint64_t)a.experts * ((a.n + side - 1) / side) * ((a.k + side - 1) / side); };
+    const char* force = getenv("ZC_FORCE");
+    const int kind = force ? atoi(force) : tiles(256) >= 192 ? 0 : tiles(128) >= 192 ? 1 : 2;
+    if (kind == 0) return launch(GradWide{});
+    if (kind == 1) return launch(GradMid{});
+    return launch(GradSmall{});
+}
+
+}  // namespace
+
+zc_status launch_weight_grad(const WeightGradArgs& a, hipStream_t stream) {
+    if (a.out_dtype == ZC_BF16) return weight_grad_as<__bf16>(a, stream);
+    if (a.out_dtype == ZC_FP16) return weight_grad_as<_Float16>(a, stream);
+    return weight_grad_as<float>(a, stream);
 }
 
 }  // namespace zc

@@ -170,9 +170,26 @@ def empty_fp8_weights(experts: int, n: int, k: int, device="cuda") -> Fp8Blocks:
     return _empty_blocks((experts, n), (experts, -(-n // BLOCK)), k, device)
 
 
-def empty_fp8_columns(rows: int, cols: int, device="cuda") -> Fp8Blocks:
-    """A blocked [cols, rows] for quantize_columns of a [rows, cols] matrix."""
-    return _empty_blocks((cols,), (cols,), rows, device)
+class Fp8Columns(NamedTuple):
+    """A [rows, cols] matrix in 8-bit blocks of 128 rows of a column: ``data``
+    E4M3 [ceil(rows / 128), cols, 128], ``scale`` E8M0 [ceil(rows / 128),
+    up(cols, 4)]."""
+    data: torch.Tensor
+    scale: torch.Tensor
+    rows: int
+    cols: int
+
+    def float(self) -> torch.Tensor:
+        """The values the blocks stand for, in 32 bits, as [rows, cols]."""
+        v = self.data.float() * self.scale.float()[:, :self.cols, None]
+        return v.transpose(1, 2).flatten(0, 1)[:self.rows]
+
+
+def empty_fp8_columns(rows: int, cols: int, device="cuda") -> Fp8Columns:
+    """Storage for quantize_columns of a [rows, cols] matrix."""
+    blocks = -(-rows // BLOCK)
+    return Fp8Columns(torch.zeros(blocks, cols, BLOCK, dtype=_FP8, device=device),
+                      torch.zeros(blocks, _up(cols, 4), dtype=torch.uint8, device=device).view(_E8M0), rows, cols)
 
 
 def _part(t, what: str, dtype, dims, width: int):
@@ -198,6 +215,15 @@ def _blocks(f: Fp8Blocks, what: str, cols: int, lead, scale_lead=None):
         _bad(what, f"{have} columns, {cols} expected")
     return (_part(data, what, _FP8, lead, (cols + 127) // 128 * 128),
             _part(scale, what, _E8M0, scale_lead or lead, (cols + 511) // 512 * 4))
+
+
+def _columns(f: Fp8Columns, what: str, rows: int, cols: int):
+    """Pointers of data and scale of the columns of a [rows, cols] matrix."""
+    data, scale, r, c = f
+    if r != rows or c != cols:
+        _bad(what, f"columns of {(r, c)}, {(rows, cols)} expected")
+    blocks = (rows + 127) // 128
+    return _part(data, what, _FP8, (blocks, cols), 128), _part(scale, what, _E8M0, (blocks,), (cols + 3) // 4 * 4)
 
 
 class Routing(NamedTuple):
@@ -354,11 +380,10 @@ def quantize_weights(w, out: Fp8Blocks, transpose: bool = False, stream=None):
         _failed(rc, "zc_quantize_weights")
 
 
-def quantize_columns(x, out: Fp8Blocks, used=None, stream=None):
-    """Enqueue the cast of x [rows, cols] in blocks of 128 rows of a column,
-    stored as the blocked [cols, rows]."""
+def quantize_columns(x, out: Fp8Columns, used=None, stream=None):
+    """Enqueue the cast of x [rows, cols] in blocks of 128 rows of a column."""
     p, stride, rows, cols = _matrix(x, "x", 0)
-    data, scale = _blocks(out, "out", rows, (cols,))
+    data, scale = _columns(out, "out", rows, cols)
     rc = _zc.zc_quantize_columns(p, stride, _DTYPES[x.dtype], rows, cols, _used(used), data, scale, _stream(stream))
     if rc:
         _failed(rc, "zc_quantize_columns")
@@ -383,17 +408,17 @@ def expert_product(a: Fp8Blocks, w: Fp8Blocks, out, offsets=None, counts=None, s
         _failed(rc, "zc_expert_product")
 
 
-def expert_weight_grad(y: Fp8Blocks, x: Fp8Blocks, dw, offsets=None, stream=None):
-    """Enqueue dw[e] = Y_e X_e^T over the rows of every expert's segment
-    (segments begin at multiples of 128); y: blocked [n, rows], x: blocked
-    [k, rows] from quantize_columns, dw [experts, n, k]."""
+def expert_weight_grad(y: Fp8Columns, x: Fp8Columns, dw, offsets=None, stream=None):
+    """Enqueue dw[e] = Y_e^T X_e over the rows of every expert's segment
+    (segments begin at multiples of 128); y: columns of [rows, n], x: columns
+    of [rows, k], dw [experts, n, k]."""
     if dw.dim() != 3 or dw.dtype not in _DTYPES:
         _bad("dw", f"shape {tuple(dw.shape)}, type {dw.dtype}")
     experts, n, k = dw.shape
     rows = x[2]
     p = _flat(dw, "dw", dw.dtype, 0)
-    yp, ysp = _blocks(y, "y", rows, (n,))
-    xp, xsp = _blocks(x, "x", rows, (k,))
+    yp, ysp = _columns(y, "y", rows, n)
+    xp, xsp = _columns(x, "x", rows, k)
     off = 0 if offsets is None else _flat(offsets, "offsets", _I32, experts + 1)
     rc = _zc.zc_expert_weight_grad(yp, ysp, xp, xsp, rows, experts, n, k, off, p, _DTYPES[dw.dtype], _stream(stream))
     if rc:
