@@ -7,8 +7,6 @@
 // the scales cost no arithmetic and the sum over blocks stays in the unit's
 // 32-bit accumulators.  The weight side is the instruction's first operand:
 // a lane then has four neighbouring columns j of one row r.
-#include <stdlib.h>
-
 #include "zc_experts_kernels.h"
 
 namespace zc {
@@ -740,10 +738,13 @@ zc_status weight_grad_as(const WeightGradArgs& a, hipStream_t stream) {
         return ZC_OK;
     };
     auto tiles = [&](uint32_t side) { return (uint64_t)a.experts * ((a.n + side - 1) / side) * ((a.k + side - 1) / side); };
-    const char* force = getenv("ZC_FORCE");
-    const int kind = force ? atoi(force) : tiles(256) >= 192 ? 0 : tiles(128) >= 192 ? 1 : 2;
-    if (kind == 0) return launch(GradWide{});
-    if (kind == 1) return launch(GradMid{});
+    // The widest tiles that still give most CUs one; in us, 256 / 128 / 64 wide:
+    //   448, 1792, 7168 tiles (1 expert 4096 x 7168, 2048 rows) 61/91/207
+    //   192, 704, 2816 (8 experts 1000 x 1401, 16384 rows)      76/51/91
+    //   128, 512, 2048 (16 experts 512 x 1024, 16384 rows)      59/35/43
+    //   35, 126, 378 (7 experts 178 x 1095, 16384 rows)         74/32/27
+    if (tiles(256) >= 256) return launch(GradWide{});
+    if (tiles(128) >= 192) return launch(GradMid{});
     return launch(GradSmall{});
 }
 
