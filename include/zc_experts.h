@@ -161,11 +161,17 @@ zc_status zc_expert_product(const void *d_a, const void *d_a_scale, uint64_t row
  * out_dtype; an expert without rows gets zeros.  Segments begin at multiples
  * of 128 (zc_route with such an align), padding rows are zeros.  d_offsets
  * NULL: one expert, all rows.
+ * Long segments of small weights are summed in parts, joined in their order,
+ * where d_ws holds them: zc_expert_weight_grad_workspace_bytes (0: none would
+ * be used).  d_ws NULL: every sum in one piece.  Which parts are taken goes by
+ * the arguments alone.
  */
+uint64_t zc_expert_weight_grad_workspace_bytes(uint64_t rows, uint32_t experts, uint32_t n, uint32_t k);
 zc_status zc_expert_weight_grad(const void *d_y, const void *d_y_scale, const void *d_x,
                                 const void *d_x_scale, uint64_t rows, uint32_t experts, uint32_t n,
                                 uint32_t k, const int32_t *d_offsets, void *d_dw,
-                                uint32_t out_dtype, hipStream_t stream);
+                                uint32_t out_dtype, void *d_ws, uint64_t ws_bytes,
+                                hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -12,10 +12,12 @@ from .binding import (EXPORTS, LIB_PATH, Plan, ZcError, check_buffer, lib, prefe
                       reduce_native)
 from .experts import (EXPERT_EXPORTS, ExpertPlan, Fp8Blocks, Fp8Columns, Routing,
                       empty_fp8_columns, empty_fp8_rows, empty_fp8_weights, expert_product, expert_weight_grad,
+                      expert_weight_grad_workspace_bytes,
                       quantize_columns, quantize_rows, quantize_weights)
 
 __all__ = ["EXPORTS", "LIB_PATH", "Plan", "ZcError", "check_buffer", "lib", "prefer_compressed",
            "reduce_native",
            "EXPERT_EXPORTS", "ExpertPlan", "Fp8Blocks", "Fp8Columns", "Routing", "empty_fp8_columns",
            "empty_fp8_rows", "empty_fp8_weights", "expert_product", "expert_weight_grad",
+           "expert_weight_grad_workspace_bytes",
            "quantize_columns", "quantize_rows", "quantize_weights"]

@@ -244,9 +244,15 @@ zc_status zc_expert_product(const void* d_a, const void* d_a_scale, uint64_t row
     return finished(launch_product(a, stream));
 }
 
+uint64_t zc_expert_weight_grad_workspace_bytes(uint64_t rows, uint32_t experts, uint32_t n, uint32_t k) {
+    if (!experts || !n || !k || experts > kMaxExperts || n >= kMaxWidth || k >= kMaxWidth || rows >= kMaxWidth) return 0;
+    const uint32_t parts = plan_weight_grad(stored((uint32_t)rows), experts, n, k, true).parts;
+    return parts == 1 ? 0 : up64((uint64_t)parts * experts * n * k * 4, 256);
+}
+
 zc_status zc_expert_weight_grad(const void* d_y, const void* d_y_scale, const void* d_x, const void* d_x_scale,
                                 uint64_t rows, uint32_t experts, uint32_t n, uint32_t k, const int32_t* d_offsets,
-                                void* d_dw, uint32_t out_dtype, hipStream_t stream) {
+                                void* d_dw, uint32_t out_dtype, void* d_ws, uint64_t ws_bytes, hipStream_t stream) {
     if (out_dtype > ZC_FP32 || !experts || !n || !k) return ZC_ERR_INVALID_ARG;
     if (!d_offsets && experts != 1) return ZC_ERR_INVALID_ARG;
     if (experts > kMaxExperts || n >= kMaxWidth || k >= kMaxWidth || rows >= kMaxWidth) return ZC_ERR_UNSUPPORTED;
@@ -254,10 +260,13 @@ zc_status zc_expert_weight_grad(const void* d_y, const void* d_y_scale, const vo
     if (rows && (!d_y || !aligned(d_y, 16) || !d_y_scale || !aligned(d_y_scale, 16) || !d_x || !aligned(d_x, 16) ||
                  !d_x_scale || !aligned(d_x_scale, 16)))
         return ZC_ERR_INVALID_ARG;
+    if (d_ws && !aligned(d_ws, 256)) return ZC_ERR_INVALID_ARG;
+    if (d_ws && ws_bytes < zc_expert_weight_grad_workspace_bytes(rows, experts, n, k)) return ZC_ERR_CAPACITY;
     const WeightGradArgs a{static_cast<const uint8_t*>(d_y), static_cast<const uint8_t*>(d_y_scale),
                            static_cast<const uint8_t*>(d_x), static_cast<const uint8_t*>(d_x_scale), d_offsets, d_dw,
                            stored((uint32_t)rows), experts, n, k, up_to(n, 4), up_to(k, 4), out_dtype};
-    return finished(launch_weight_grad(a, stream));
+    const WeightGradPlan plan = plan_weight_grad(a.rows, experts, n, k, d_ws != nullptr);
+    return finished(launch_weight_grad(a, plan, d_ws, stream));
 }
 
 }  // extern "C"

@@ -96,6 +96,14 @@ struct WeightGradArgs {
     uint32_t out_dtype;
 };
 
+// How a weight gradient is cut: tiles of side x side, each segment summed in up
+// to `parts` parts that are joined afterwards (parts > 1 needs a workspace of
+// parts * experts * n * k floats).  split: whether parts are allowed.
+struct WeightGradPlan {
+    uint32_t side, parts;
+};
+WeightGradPlan plan_weight_grad(uint32_t rows, uint32_t experts, uint32_t n, uint32_t k, bool split);
+
 // Each enqueues its kernels, or returns ZC_ERR_UNSUPPORTED and enqueues none
 // where the launch would have more workgroups than a launch may (2^32 threads).
 uint64_t route_tiles(uint64_t nslots);
@@ -107,7 +115,7 @@ zc_status launch_cast_rows(const CastRowsArgs& a, uint32_t dtype, hipStream_t st
 zc_status launch_cast_weights(const CastTileArgs& a, uint32_t dtype, hipStream_t stream);
 zc_status launch_cast_columns(const CastTileArgs& a, uint32_t dtype, hipStream_t stream);
 zc_status launch_product(const ProductArgs& a, hipStream_t stream);
-zc_status launch_weight_grad(const WeightGradArgs& a, hipStream_t stream);
+zc_status launch_weight_grad(const WeightGradArgs& a, const WeightGradPlan& plan, void* ws, hipStream_t stream);
 
 // Whether a launch may have this many workgroups of 256 threads.
 inline bool fits(uint64_t workgroups) { return workgroups < (1ull << 24); }

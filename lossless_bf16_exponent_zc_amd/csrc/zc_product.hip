@@ -613,28 +613,50 @@ __device__ __forceinline__ Place place_of(uint32_t index, uint32_t cols) {
     return Place{group * 4 + (in & 3), in >> 2};
 }
 
+// Blocks of an expert's segment.
+__device__ __forceinline__ void segment_blocks(const WeightGradArgs& p, uint32_t e, uint32_t& b0, uint32_t& n) {
+    b0 = 0;
+    n = p.rows / 128;
+    if (p.offsets) {
+        b0 = clamp_to(p.offsets[e], 0, p.rows) / 128;
+        n = (clamp_to(p.offsets[e + 1], b0 * 128, p.rows) + 127) / 128 - b0;
+    }
+}
+
+// In how many parts a segment of n blocks is summed, of at most `parts`.
+__device__ __forceinline__ uint32_t parts_of(uint32_t n, uint32_t parts) { return n < parts ? (n ? n : 1) : parts; }
+
+// One tile of one expert's gradient, or (parts > 1) of its sum over one part
+// of the segment, which goes to the part's own array of all gradients.
 template <typename T, typename SH>
-__global__ __launch_bounds__(256, 1) void weight_grad(WeightGradArgs p, uint32_t row_tiles, uint32_t col_tiles, Order order) {
+__global__ __launch_bounds__(256, 1) void weight_grad(WeightGradArgs p, T* out, uint32_t row_tiles, uint32_t col_tiles,
+                                                      Order order, uint32_t per_part, uint32_t parts) {
     extern __shared__ __align__(16) uint8_t lds[];
+    const uint32_t index = blockIdx.x % per_part, part = blockIdx.x / per_part;
     Place where;
     uint32_t e, i0;
     if (order == kRuns) {
         const uint32_t padded = (row_tiles + 3) / 4 * 4;  // an expert's slots, in whole runs
-        where = place_of(blockIdx.x, col_tiles);
+        where = place_of(index, col_tiles);
         e = where.slot / padded;
         i0 = where.slot % padded * SH::BM;
         if (e >= p.experts || i0 >= p.n) return;
     } else {
-        where.col = blockIdx.x % col_tiles;
-        where.slot = blockIdx.x / col_tiles;
+        where.col = index % col_tiles;
+        where.slot = index / col_tiles;
         e = where.slot / row_tiles;
         i0 = where.slot % row_tiles * SH::BM;
     }
     const uint32_t j0 = where.col * SH::BN;
-    uint32_t b0 = 0, b1 = p.rows / 128;
-    if (p.offsets) {
-        b0 = clamp_to(p.offsets[e], 0, p.rows) / 128;
-        b1 = (clamp_to(p.offsets[e + 1], b0 * 128, p.rows) + 127) / 128;
+    uint32_t b0, n;
+    segment_blocks(p, e, b0, n);
+    if (parts > 1) {
+        const uint32_t mine = parts_of(n, parts);
+        if (part >= mine) return;
+        const uint32_t lo = (uint32_t)((uint64_t)n * part / mine), hi = (uint32_t)((uint64_t)n * (part + 1) / mine);
+        b0 += lo;
+        n = hi - lo;
+        out += (uint64_t)part * p.experts * p.n * p.k;
     }
     // block b of Y: [n][128] bytes, and n scale bytes
     const Tile t{p.y + ((uint64_t)b0 * p.n + i0) * 128,
@@ -642,9 +664,38 @@ __global__ __launch_bounds__(256, 1) void weight_grad(WeightGradArgs p, uint32_t
                  p.y_scale + (uint64_t)b0 * p.y_scale_stride + i0,
                  p.x_scale + (uint64_t)b0 * p.x_scale_stride + j0,
                  p.n - i0, p.k - j0, 128, 128, (uint64_t)p.n * 128, (uint64_t)p.k * 128,
-                 p.y_scale_stride, p.x_scale_stride, b1 - b0};
-    const Out<T> o{static_cast<T*>(p.dw) + ((uint64_t)e * p.n + i0) * p.k + j0, p.k, p.n - i0, p.k - j0};
+                 p.y_scale_stride, p.x_scale_stride, n};
+    const Out<T> o{out + ((uint64_t)e * p.n + i0) * p.k + j0, p.k, p.n - i0, p.k - j0};
     run_tile<SH>(t, o, lds);
+}
+
+// The sum of an expert's parts, in their order.  grid: (pieces, experts).
+template <typename T>
+__global__ __launch_bounds__(256) void join_parts(WeightGradArgs p, const float* part, T* out, uint32_t parts) {
+    const uint32_t e = blockIdx.y;
+    uint32_t b0, n;
+    segment_blocks(p, e, b0, n);
+    const uint32_t mine = parts_of(n, parts);
+    const uint64_t size = (uint64_t)p.n * p.k, all = size * p.experts;
+    for (uint64_t i = (blockIdx.x * 256u + threadIdx.x) * 4ull; i < size; i += (uint64_t)gridDim.x * 1024) {
+        const float* src = part + e * size + i;
+        T* dst = out + e * size + i;
+        if (i + 4 <= size) {
+            typedef f32x4 __attribute__((aligned(4))) Word;
+            f32x4 v = *reinterpret_cast<const Word*>(src);
+            for (uint32_t q = 1; q < mine; ++q) v += *reinterpret_cast<const Word*>(src + q * all);
+            struct Four {
+                T v[4];
+            };
+            *reinterpret_cast<Four*>(dst) = Four{{(T)v[0], (T)v[1], (T)v[2], (T)v[3]}};
+        } else {
+            for (uint32_t j = 0; i + j < size; ++j) {
+                float v = src[j];
+                for (uint32_t q = 1; q < mine; ++q) v += src[q * all + j];
+                dst[j] = (T)v;
+            }
+        }
+    }
 }
 
 typedef Shape<2, 8, 8, 2, true> GradWide;
@@ -724,36 +775,66 @@ zc_status launch_product(const ProductArgs& a, hipStream_t stream) {
 
 namespace {
 
+template <typename T, typename SH>
+zc_status weight_grad_in(const WeightGradArgs& a, T* out, uint32_t parts, hipStream_t stream) {
+    const uint32_t rows = (a.n + SH::BM - 1) / SH::BM, cols = (a.k + SH::BN - 1) / SH::BN;
+    const uint64_t tiles = (uint64_t)a.experts * rows * cols;
+    const Order order = tiles > 512 ? kRuns : kInOrder;
+    const uint64_t each = order == kRuns ? ((uint64_t)a.experts * ((rows + 3) / 4 * 4) * cols + 255) / 256 * 256 : tiles;
+    if (!fits(each * parts)) return ZC_ERR_UNSUPPORTED;
+    allow_lds(weight_grad<T, SH>, SH::kLds);
+    hipLaunchKernelGGL((weight_grad<T, SH>), dim3((uint32_t)(each * parts)), dim3(256), SH::kLds, stream, a, out, rows, cols,
+                       order, (uint32_t)each, parts);
+    return ZC_OK;
+}
+
 template <typename T>
-zc_status weight_grad_as(const WeightGradArgs& a, hipStream_t stream) {
-    auto launch = [&](auto shape) {
-        typedef decltype(shape) SH;
-        const uint32_t rows = (a.n + SH::BM - 1) / SH::BM, cols = (a.k + SH::BN - 1) / SH::BN;
-        const uint64_t tiles = (uint64_t)a.experts * rows * cols;
-        const Order order = tiles > 512 ? kRuns : kInOrder;
-        const uint64_t grid = order == kRuns ? ((uint64_t)a.experts * ((rows + 3) / 4 * 4) * cols + 255) / 256 * 256 : tiles;
-        if (!fits(grid)) return ZC_ERR_UNSUPPORTED;
-        allow_lds(weight_grad<T, SH>, SH::kLds);
-        hipLaunchKernelGGL((weight_grad<T, SH>), dim3((uint32_t)grid), dim3(256), SH::kLds, stream, a, rows, cols, order);
-        return ZC_OK;
-    };
-    auto tiles = [&](uint32_t side) { return (uint64_t)a.experts * ((a.n + side - 1) / side) * ((a.k + side - 1) / side); };
-    // The widest tiles that still give most CUs one; in us, 256 / 128 / 64 wide:
-    //   448, 1792, 7168 tiles (1 expert 4096 x 7168, 2048 rows) 61/91/207
-    //   192, 704, 2816 (8 experts 1000 x 1401, 16384 rows)      76/51/91
-    //   128, 512, 2048 (16 experts 512 x 1024, 16384 rows)      59/35/43
-    //   35, 126, 378 (7 experts 178 x 1095, 16384 rows)         74/32/27
-    if (tiles(256) >= 256) return launch(GradWide{});
-    if (tiles(128) >= 192) return launch(GradMid{});
-    return launch(GradSmall{});
+zc_status weight_grad_shaped(const WeightGradArgs& a, T* out, const WeightGradPlan& plan, hipStream_t stream) {
+    if (plan.side == 256) return weight_grad_in<T, GradWide>(a, out, plan.parts, stream);
+    if (plan.side == 128) return weight_grad_in<T, GradMid>(a, out, plan.parts, stream);
+    return weight_grad_in<T, GradSmall>(a, out, plan.parts, stream);
+}
+
+template <typename T>
+zc_status weight_grad_as(const WeightGradArgs& a, const WeightGradPlan& plan, float* ws, hipStream_t stream) {
+    T* out = static_cast<T*>(a.dw);
+    if (plan.parts == 1) return weight_grad_shaped<T>(a, out, plan, stream);
+    if (zc_status e = weight_grad_shaped<float>(a, ws, plan, stream)) return e;
+    const uint64_t pieces = ((uint64_t)a.n * a.k + 1023) / 1024, most = 4096 / a.experts + 1;
+    hipLaunchKernelGGL(join_parts<T>, dim3((uint32_t)(pieces < most ? pieces : most), a.experts), dim3(256), 0, stream, a, ws,
+                       out, plan.parts);
+    return ZC_OK;
 }
 
 }  // namespace
 
-zc_status launch_weight_grad(const WeightGradArgs& a, hipStream_t stream) {
-    if (a.out_dtype == ZC_BF16) return weight_grad_as<__bf16>(a, stream);
-    if (a.out_dtype == ZC_FP16) return weight_grad_as<_Float16>(a, stream);
-    return weight_grad_as<float>(a, stream);
+WeightGradPlan plan_weight_grad(uint32_t rows, uint32_t experts, uint32_t n, uint32_t k, bool split) {
+    auto tiles = [&](uint32_t side) { return (uint64_t)experts * ((n + side - 1) / side) * ((k + side - 1) / side); };
+    // The widest tiles that still give most CUs one; in us, 256 / 128 / 64 wide:
+    //   448, 1792, 7168 tiles (1 expert 4096 x 7168, 4096 rows) 99/134/326
+    //   192, 704, 2816 (8 experts 1000 x 1401, 32768 rows)      137/87/153
+    //   128, 512, 2048 (16 experts 512 x 1024, 32768 rows)      109/60/67
+    //   16, 64, 256 (1 expert 1024 x 1024, 4096 rows)           42/20/15
+    if (tiles(256) >= 256) return WeightGradPlan{256, 1};
+    // Few tiles and long segments: a CU draws some 50 GB/s past its L2, so the
+    // segments go to more CUs, at the price of the join; whole / in parts:
+    //   1 expert 1024 x 1024, 32768 rows  87 (64 wide) / 53 (128 wide, 4 parts)
+    //   1 expert 60 x 300, 32768 rows     77 / 16 (64 wide, 16 parts)
+    //   but at 32 blocks of 128 rows an expert, 1024 x 1024   15 / 20
+    const uint32_t blocks = rows / 128 / experts;
+    if (split && blocks >= 64 && tiles(128) <= 128) {
+        const uint32_t side = tiles(64) <= 32 ? 64 : 128;
+        const uint64_t most = 256 / tiles(side);
+        return WeightGradPlan{side, most > 16 ? 16u : (uint32_t)most};
+    }
+    if (tiles(128) >= 192) return WeightGradPlan{128, 1};
+    return WeightGradPlan{64, 1};
+}
+
+zc_status launch_weight_grad(const WeightGradArgs& a, const WeightGradPlan& plan, void* ws, hipStream_t stream) {
+    if (a.out_dtype == ZC_BF16) return weight_grad_as<__bf16>(a, plan, static_cast<float*>(ws), stream);
+    if (a.out_dtype == ZC_FP16) return weight_grad_as<_Float16>(a, plan, static_cast<float*>(ws), stream);
+    return weight_grad_as<float>(a, plan, static_cast<float*>(ws), stream);
 }
 
 }  // namespace zc

@@ -25,6 +25,7 @@ EXPERT_EXPORTS = (
     "zc_route_rows", "zc_route_workspace_bytes", "zc_route", "zc_dispatch", "zc_dispatch_fp8",
     "zc_combine", "zc_combine_backward", "zc_quantize_rows", "zc_quantize_weights",
     "zc_quantize_columns", "zc_expert_product", "zc_expert_weight_grad",
+    "zc_expert_weight_grad_workspace_bytes",
 )
 
 BLOCK = 128  # values per scale
@@ -65,12 +66,13 @@ def lib() -> ctypes.CDLL:
         "zc_quantize_weights": [vp, u32, u32, u32, u32, i, vp, vp, vp],
         "zc_quantize_columns": [vp, u64, u32, u64, u32, vp, vp, vp, vp],
         "zc_expert_product": [vp, vp, u64, vp, vp, u32, u32, u32, vp, vp, vp, u64, u32, vp],
-        "zc_expert_weight_grad": [vp, vp, vp, vp, u64, u32, u32, u32, vp, vp, u32, vp],
+        "zc_expert_weight_grad": [vp, vp, vp, vp, u64, u32, u32, u32, vp, vp, u32, vp, u64, vp],
+        "zc_expert_weight_grad_workspace_bytes": [u64, u32, u32, u32],
     }
     for name in EXPERT_EXPORTS:
         f = getattr(L, name)
         f.argtypes = args[name]
-        f.restype = u64 if name in ("zc_route_rows", "zc_route_workspace_bytes") else i
+        f.restype = u64 if name.endswith(("_rows", "_bytes")) and not name.startswith("zc_quantize") else i
         setattr(_zc, name, f)
     _lib = L
     return L
@@ -408,18 +410,36 @@ def expert_product(a: Fp8Blocks, w: Fp8Blocks, out, offsets=None, counts=None, s
         _failed(rc, "zc_expert_product")
 
 
-def expert_weight_grad(y: Fp8Columns, x: Fp8Columns, dw, offsets=None, stream=None):
+def expert_weight_grad_workspace_bytes(rows: int, experts: int, n: int, k: int) -> int:
+    """Bytes expert_weight_grad uses to sum long segments in parts (or 0)."""
+    return _zc.zc_expert_weight_grad_workspace_bytes(rows, experts, n, k)
+
+
+def expert_weight_grad(y: Fp8Columns, x: Fp8Columns, dw, offsets=None, ws=None, stream=None):
     """Enqueue dw[e] = Y_e^T X_e over the rows of every expert's segment
     (segments begin at multiples of 128); y: columns of [rows, n], x: columns
-    of [rows, k], dw [experts, n, k]."""
-    if dw.dim() != 3 or dw.dtype not in _DTYPES:
-        _bad("dw", f"shape {tuple(dw.shape)}, type {dw.dtype}")
-    experts, n, k = dw.shape
+    of [rows, k], dw [experts, n, k].  ws: the workspace for long segments;
+    without one it is taken from torch's allocator, on the call's stream."""
+    shape = dw.shape
+    if len(shape) != 3 or dw.dtype not in _DTYPES:
+        _bad("dw", f"shape {tuple(shape)}, type {dw.dtype}")
+    experts, n, k = shape
     rows = x[2]
     p = _flat(dw, "dw", dw.dtype, 0)
     yp, ysp = _columns(y, "y", rows, n)
     xp, xsp = _columns(x, "x", rows, k)
     off = 0 if offsets is None else _flat(offsets, "offsets", _I32, experts + 1)
-    rc = _zc.zc_expert_weight_grad(yp, ysp, xp, xsp, rows, experts, n, k, off, p, _DTYPES[dw.dtype], _stream(stream))
+    need = _zc.zc_expert_weight_grad_workspace_bytes(rows, experts, n, k)
+    w = 0
+    if need:
+        if ws is None:
+            if stream is None:
+                ws = torch.empty(need, dtype=torch.uint8, device=dw.device)
+            else:
+                with torch.cuda.stream(stream):
+                    ws = torch.empty(need, dtype=torch.uint8, device=dw.device)
+        w = _flat(ws, "workspace", torch.uint8, need)
+    rc = _zc.zc_expert_weight_grad(yp, ysp, xp, xsp, rows, experts, n, k, off, p, _DTYPES[dw.dtype], w, need,
+                                   _stream(stream))
     if rc:
         _failed(rc, "zc_expert_weight_grad")

@@ -116,8 +116,9 @@ def test_cast_and_product_refusals(L):
                  (10, None), (11, 8), (12, 3)):
         assert rc(L.zc_expert_product, p, i, v) == BAD, (i, v)
     assert rc(L.zc_expert_product, p, 2, 1 << 31) == UNSUP and rc(L.zc_expert_product, p, 2, 0) == binding.ZC_OK
-    g = [P, P, P, P, 256, 4, 64, 64, P, P, 0, None]
-    for i, v in ((0, None), (1, P + 8), (2, P + 1), (3, None), (5, 0), (6, 0), (7, 0), (8, None), (9, None), (10, 3)):
+    g = [P, P, P, P, 256, 4, 64, 64, P, P, 0, None, 0, None]
+    for i, v in ((0, None), (1, P + 8), (2, P + 1), (3, None), (5, 0), (6, 0), (7, 0), (8, None), (9, None), (10, 3),
+                 (11, P + 64)):
         assert rc(L.zc_expert_weight_grad, g, i, v) == BAD, (i, v)
     assert rc(L.zc_expert_weight_grad, g, 4, 1 << 24) == UNSUP
 

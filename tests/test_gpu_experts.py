@@ -408,6 +408,42 @@ def test_weight_gradient_of_whole_numbers_is_exact(counts, align, n, k, out_dtyp
         assert torch.equal(dw[e].cpu(), (dy[a:b].T @ x[a:b]).to(DT[out_dtype])), e
 
 
+@pytest.mark.parametrize("counts,n,k", [([9000], 60, 130), ([17000, 0], 200, 70), ([40, 33000], 1, 129)])
+def test_weight_gradient_of_long_segments_in_parts(counts, n, k):
+    """Segments long enough to be summed in parts: with the caller's
+    workspace, with torch's, on another stream, and whole, all exact."""
+    E, off, g = len(counts), segments(counts, 128), gen(8)
+    rows = off[-1]
+    need = zc.expert_weight_grad_workspace_bytes(rows, E, n, k)
+    assert need >= 2 * E * n * k * 4
+    x, dy = torch.zeros(rows, k), torch.zeros(rows, n)
+    for e, c in enumerate(counts):
+        x[off[e]:off[e] + c], dy[off[e]:off[e] + c] = whole_numbers(g, c, k), whole_numbers(g, c, n)
+    fx, fy = zc.empty_fp8_columns(rows, k), zc.empty_fp8_columns(rows, n)
+    zc.quantize_columns(x.cuda(), fx)
+    zc.quantize_columns(dy.cuda(), fy)
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    want = torch.stack([dy[off[e]:off[e + 1]].double().T @ x[off[e]:off[e + 1]].double() for e in range(E)]).float()
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for kw in ({}, {"ws": ws[:need]}, {"stream": side}):
+        dw = torch.full((E, n, k), float("nan"), device="cuda")
+        torch.cuda.synchronize()
+        zc.expert_weight_grad(fy, fx, dw, offsets, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(dw.cpu(), want), kw
+    assert (ws[need:] == 0xFF).all()
+    dw = torch.full((E, n, k), float("nan"), device="cuda")
+    L = zc.lib()
+    rc = L.zc_expert_weight_grad(fy.data.data_ptr(), fy.scale.data_ptr(), fx.data.data_ptr(), fx.scale.data_ptr(), rows, E,
+                                 n, k, offsets.data_ptr(), dw.data_ptr(), 2, None, 0, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and torch.equal(dw.cpu(), want)
+    with pytest.raises(zc.ZcError) as e:
+        zc.expert_weight_grad(fy, fx, dw, offsets, ws=ws[:need - 1])
+    assert e.value.code == 2
+
+
 def test_weight_gradient_of_any_numbers():
     counts, n, k = [200, 0, 513], 300, 260
     off = segments(counts, 128)
