@@ -399,61 +399,60 @@ __device__ __forceinline__ f32x4 late(f32x4 v) {
     return v;
 }
 
-// A tile with all its columns leaves from the registers, 8 neighbouring columns
-// per lane, in 16-byte words at whatever address a row starts.  One that ends
-// early goes over LDS, 16 rows at a time, and leaves row by row, neighbouring
-// lanes in neighbouring columns.
-template <typename T, typename SH>
-__device__ __forceinline__ void store_tile(const Out<T>& o, const f32x4 (&acc)[SH::TM][SH::TN], uint8_t* lds) {
-    const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-    const uint32_t m0 = (wave / SH::WN) * SH::TM * 16, n0 = (wave % SH::WN) * SH::TN * 16;
-    if (o.cols >= (uint32_t)SH::BN) {
-        typedef xu32x4 __attribute__((aligned(2))) Word;
-        T* p = o.out + (m0 + r) * o.stride + n0 + g * 8;
-#pragma unroll
-        for (int j = 0; j < SH::TM; ++j) {
-            if (m0 + j * 16 + r < o.rows) {
-#pragma unroll
-                for (int i = 0; i < SH::TN; i += 2) {
-                    const f32x4 lo = late(acc[j][i]), hi = late(acc[j][i + 1]);
-                    union {
-                        T v[8];
-                        xu32x4 w[sizeof(T) / 2];
-                    } u;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        u.v[q] = (T)lo[q];
-                        u.v[4 + q] = (T)hi[q];
-                    }
-#pragma unroll
-                    for (int q = 0; q < (int)sizeof(T) / 2; ++q) reinterpret_cast<Word*>(p + i * 16)[q] = u.w[q];
-                }
-            }
-            p += 16 * o.stride;
-        }
-        return;
+// The first `left` (1..7) of 8 neighbouring results, as 4 + 2 + 1 of them.
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, const uint32_t* w, uint32_t left) {
+    typedef xu32x4 __attribute__((aligned(2))) Four;
+    typedef xu32x2 __attribute__((aligned(2))) Two;
+    typedef uint32_t __attribute__((aligned(2))) One;
+    if constexpr (sizeof(T) == 4) {
+        if (left & 4) *reinterpret_cast<Four*>(p) = xu32x4{w[0], w[1], w[2], w[3]};
+        if (left & 2) *reinterpret_cast<Two*>(p + (left & 4)) = left & 4 ? xu32x2{w[4], w[5]} : xu32x2{w[0], w[1]};
+        if (left & 1)
+            *reinterpret_cast<One*>(p + (left & 6)) = left & 4 ? (left & 2 ? w[6] : w[4]) : (left & 2 ? w[2] : w[0]);
+    } else {
+        if (left & 4) *reinterpret_cast<Two*>(p) = xu32x2{w[0], w[1]};
+        if (left & 2) *reinterpret_cast<One*>(p + (left & 4)) = left & 4 ? w[2] : w[0];
+        if (left & 1)
+            *reinterpret_cast<uint16_t*>(p + (left & 6)) =
+                (uint16_t)(left & 4 ? (left & 2 ? w[3] : w[2]) : (left & 2 ? w[1] : w[0]));
     }
-    constexpr uint32_t kCols = SH::TN * 16, kPitch = kCols + 4;  // floats
-    float* buf = reinterpret_cast<float*>(lds) + wave * 16 * kPitch;
-    const uint32_t cols = n0 < o.cols ? (o.cols - n0 < kCols ? o.cols - n0 : kCols) : 0;
+}
+
+// A tile leaves from the registers, 8 neighbouring columns per lane, in
+// 16-byte words at whatever address a row starts; ENDS: its columns end early.
+template <typename T, typename SH, bool ENDS>
+__device__ __forceinline__ void store_tile(const Out<T>& o, const f32x4 (&acc)[SH::TM][SH::TN]) {
+    typedef xu32x4 __attribute__((aligned(2))) Word;
+    const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    const uint32_t m0 = (wave / SH::WN) * SH::TM * 16, n0 = (wave % SH::WN) * SH::TN * 16 + g * 8;
+    T* p = o.out + (m0 + r) * o.stride + n0;
 #pragma unroll
     for (int j = 0; j < SH::TM; ++j) {
+        if (m0 + j * 16 + r < o.rows) {
 #pragma unroll
-        for (int i = 0; i < SH::TN; ++i)
-            *reinterpret_cast<f32x4*>(buf + r * kPitch + (i >> 1) * 32 + g * 8 + (i & 1) * 4) = late(acc[j][i]);
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        const uint32_t m = m0 + j * 16, rows = m < o.rows ? (o.rows - m < 16 ? o.rows - m : 16) : 0;
-#pragma unroll 1
-        for (uint32_t c = lane; c < cols; c += 64) {
-            T* p = o.out + m * o.stride + n0 + c;
-#pragma unroll 8
-            for (uint32_t q = 0; q < rows; ++q, p += o.stride) *p = (T)buf[q * kPitch + c];
+            for (int i = 0; i < SH::TN; i += 2) {
+                const f32x4 lo = late(acc[j][i]), hi = late(acc[j][i + 1]);
+                union {
+                    T v[8];
+                    uint32_t w[2 * sizeof(T)];
+                    xu32x4 q[sizeof(T) / 2];
+                } u;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    u.v[q] = (T)lo[q];
+                    u.v[4 + q] = (T)hi[q];
+                }
+                const uint32_t at = n0 + i * 16;
+                if (!ENDS || at + 8 <= o.cols) {
+#pragma unroll
+                    for (int q = 0; q < (int)sizeof(T) / 2; ++q) reinterpret_cast<Word*>(p + i * 16)[q] = u.q[q];
+                } else if (at < o.cols) {
+                    store_some(p + i * 16, u.w, o.cols - at);
+                }
+            }
         }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        p += 16 * o.stride;
     }
 }
 
@@ -468,7 +467,8 @@ __device__ __forceinline__ void run_tile(const Tile& t, const Out<T>& o, uint8_t
 #pragma unroll
         for (int i = 0; i < SH::TN; ++i) acc[j][i] = f32x4{0, 0, 0, 0};
     if (t.blocks) tile_product<SH>(t, lds, acc);
-    store_tile<T, SH>(o, acc, lds);
+    if (o.cols >= (uint32_t)SH::BN) store_tile<T, SH, false>(o, acc);
+    else store_tile<T, SH, true>(o, acc);
 #endif
 }
 
@@ -700,6 +700,7 @@ __global__ __launch_bounds__(256) void join_parts(WeightGradArgs p, const float*
 
 typedef Shape<2, 8, 8, 2, true> GradWide;
 typedef Shape<2, 4, 4, 4, true> GradMid;
+typedef Shape<2, 4, 4, 2, true> GradMidPair;  // two workgroups on a CU
 typedef Shape<2, 2, 2, 7, true> GradSmall;
 
 constexpr int kLdsProduct = Shape<1, 2, 4, 4, false>::kLds > Shape<2, 4, 8, 3, false>::kLds ? Shape<1, 2, 4, 4, false>::kLds
@@ -791,6 +792,11 @@ zc_status weight_grad_in(const WeightGradArgs& a, T* out, uint32_t parts, hipStr
 template <typename T>
 zc_status weight_grad_shaped(const WeightGradArgs& a, T* out, const WeightGradPlan& plan, hipStream_t stream) {
     if (plan.side == 256) return weight_grad_in<T, GradWide>(a, out, plan.parts, stream);
+    // with more tiles than CUs, a tile's stores beside the next one's loads are
+    // worth more than loads further ahead: 32 experts 2048 x 7168 of 128 rows
+    // 444 us one to a CU, 316 in pairs
+    const uint64_t tiles = (uint64_t)a.experts * ((a.n + 127) / 128) * ((a.k + 127) / 128) * plan.parts;
+    if (plan.side == 128 && tiles > 256) return weight_grad_in<T, GradMidPair>(a, out, plan.parts, stream);
     if (plan.side == 128) return weight_grad_in<T, GradMid>(a, out, plan.parts, stream);
     return weight_grad_in<T, GradSmall>(a, out, plan.parts, stream);
 }
@@ -815,7 +821,10 @@ WeightGradPlan plan_weight_grad(uint32_t rows, uint32_t experts, uint32_t n, uin
     //   192, 704, 2816 (8 experts 1000 x 1401, 32768 rows)      137/87/153
     //   128, 512, 2048 (16 experts 512 x 1024, 32768 rows)      109/60/67
     //   16, 64, 256 (1 expert 1024 x 1024, 4096 rows)           42/20/15
-    if (tiles(256) >= 256) return WeightGradPlan{256, 1};
+    // and do not go past n and k by more than half:
+    //   215 experts 24 x 1043, most without rows                61 (256 wide) / TODO
+    auto snug = [&](uint32_t side) { return tiles(side) * side * side * 2 <= (uint64_t)experts * n * k * 3; };
+    if (tiles(256) >= 256 && snug(256)) return WeightGradPlan{256, 1};
     // Few tiles and long segments: a CU draws some 50 GB/s past its L2, so the
     // segments go to more CUs, at the price of the join; whole / in parts:
     //   1 expert 1024 x 1024, 32768 rows  87 (64 wide) / 53 (128 wide, 4 parts)
@@ -827,7 +836,7 @@ WeightGradPlan plan_weight_grad(uint32_t rows, uint32_t experts, uint32_t n, uin
         const uint64_t most = 256 / tiles(side);
         return WeightGradPlan{side, most > 16 ? 16u : (uint32_t)most};
     }
-    if (tiles(128) >= 192) return WeightGradPlan{128, 1};
+    if (tiles(128) >= 192 && (snug(128) || tiles(64) > 2048)) return WeightGradPlan{128, 1};
     return WeightGradPlan{64, 1};
 }
 

@@ -32,6 +32,8 @@ BLOCK = 128  # values per scale
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _FP8, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 _I32, _F32 = torch.int32, torch.float32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent where torch has no GPU support
+_device = getattr(torch._C, "_cuda_getDevice", None)
 
 _lib = None
 
@@ -92,7 +94,7 @@ def _failed(rc: int, name: str):
 
 def _stream(stream):
     # current_stream() builds a Stream object, 3 us; its handle alone is 0.1
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+    return _raw_stream(_device()) if stream is None else stream.cuda_stream
 
 
 def _matrix(t, what: str, rows: int, dtype=None, width=None):
