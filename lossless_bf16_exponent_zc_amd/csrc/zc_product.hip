@@ -399,56 +399,95 @@ __device__ __forceinline__ f32x4 late(f32x4 v) {
     return v;
 }
 
-// The first `left` (1..7) of 8 neighbouring results, as 4 + 2 + 1 of them.
+// 8 neighbouring results of a lane, as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void store_some(T* p, const uint32_t* w, uint32_t left) {
+struct Eight {
+    xu32x4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Eight<T> eight(const f32x4& lo, const f32x4& hi) {
+    if constexpr (sizeof(T) == 4) {
+        return Eight<T>{{__builtin_bit_cast(xu32x4, lo), __builtin_bit_cast(xu32x4, hi)}};
+    } else {
+        typedef T Pair __attribute__((ext_vector_type(2)));
+        auto pair = [](float x, float y) { return __builtin_bit_cast(uint32_t, Pair{(T)x, (T)y}); };
+        return Eight<T>{{xu32x4{pair(lo[0], lo[1]), pair(lo[2], lo[3]), pair(hi[0], hi[1]), pair(hi[2], hi[3])}}};
+    }
+}
+
+// The first `left` (1..7) of them, as 4 + 2 + 1.
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, const Eight<T>& v, uint32_t left) {
     typedef xu32x4 __attribute__((aligned(2))) Four;
     typedef xu32x2 __attribute__((aligned(2))) Two;
     typedef uint32_t __attribute__((aligned(2))) One;
+    const bool past = left & 4;
     if constexpr (sizeof(T) == 4) {
-        if (left & 4) *reinterpret_cast<Four*>(p) = xu32x4{w[0], w[1], w[2], w[3]};
-        if (left & 2) *reinterpret_cast<Two*>(p + (left & 4)) = left & 4 ? xu32x2{w[4], w[5]} : xu32x2{w[0], w[1]};
-        if (left & 1)
-            *reinterpret_cast<One*>(p + (left & 6)) = left & 4 ? (left & 2 ? w[6] : w[4]) : (left & 2 ? w[2] : w[0]);
+        const xu32x4 a = v.w[0], b = v.w[1];
+        if (past) *reinterpret_cast<Four*>(p) = a;
+        const uint32_t x = past ? b[0] : a[0], y = past ? b[1] : a[1], z = past ? b[2] : a[2];
+        if (left & 2) *reinterpret_cast<Two*>(p + (left & 4)) = xu32x2{x, y};
+        if (left & 1) *reinterpret_cast<One*>(p + (left & 6)) = left & 2 ? z : x;
     } else {
-        if (left & 4) *reinterpret_cast<Two*>(p) = xu32x2{w[0], w[1]};
-        if (left & 2) *reinterpret_cast<One*>(p + (left & 4)) = left & 4 ? w[2] : w[0];
-        if (left & 1)
-            *reinterpret_cast<uint16_t*>(p + (left & 6)) =
-                (uint16_t)(left & 4 ? (left & 2 ? w[3] : w[2]) : (left & 2 ? w[1] : w[0]));
+        const xu32x4 a = v.w[0];
+        if (past) *reinterpret_cast<Two*>(p) = xu32x2{a[0], a[1]};
+        const uint32_t x = past ? a[2] : a[0], y = past ? a[3] : a[1];
+        if (left & 2) *reinterpret_cast<One*>(p + (left & 4)) = x;
+        if (left & 1) *reinterpret_cast<uint16_t*>(p + (left & 6)) = (uint16_t)(left & 2 ? y : x);
     }
 }
 
 // A tile leaves from the registers, 8 neighbouring columns per lane, in
-// 16-byte words at whatever address a row starts; ENDS: its columns end early.
-template <typename T, typename SH, bool ENDS>
+// 16-byte words.  Words that begin between multiples of 4 bytes cost twice
+// (weight gradient, 64 experts 2048 x 4096, 4097 wide: 295, 632 us; with all
+// words at multiples of 4: 373).  EDGES: the tile's columns end early,
+// or its rows are of 16-bit values and some begin there; words of such a row
+// begin one column before, with the column that the lane before holds.
+template <typename T, typename SH, bool EDGES>
 __device__ __forceinline__ void store_tile(const Out<T>& o, const f32x4 (&acc)[SH::TM][SH::TN]) {
     typedef xu32x4 __attribute__((aligned(2))) Word;
     const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const uint32_t m0 = (wave / SH::WN) * SH::TM * 16, n0 = (wave % SH::WN) * SH::TN * 16 + g * 8;
     T* p = o.out + (m0 + r) * o.stride + n0;
+    const uint32_t odd = EDGES && sizeof(T) == 2 ? ((uint32_t)(uintptr_t)p >> 1) & 1 : 0;  // in 16 rows the same again
 #pragma unroll
     for (int j = 0; j < SH::TM; ++j) {
         if (m0 + j * 16 + r < o.rows) {
+            uint32_t carry = 0;
 #pragma unroll
             for (int i = 0; i < SH::TN; i += 2) {
                 const f32x4 lo = late(acc[j][i]), hi = late(acc[j][i + 1]);
-                union {
-                    T v[8];
-                    uint32_t w[2 * sizeof(T)];
-                    xu32x4 q[sizeof(T) / 2];
-                } u;
+                Eight<T> v = eight<T>(lo, hi);
+                T* to = p + i * 16;
+                if constexpr (!EDGES) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    u.v[q] = (T)lo[q];
-                    u.v[4 + q] = (T)hi[q];
-                }
-                const uint32_t at = n0 + i * 16;
-                if (!ENDS || at + 8 <= o.cols) {
+                    for (int q = 0; q < (int)sizeof(T) / 2; ++q) reinterpret_cast<Word*>(to)[q] = v.w[q];
+                } else {
+                    const uint32_t at = n0 + i * 16;
+                    if constexpr (sizeof(T) == 2) {
+                        const xu32x4 w = v.w[0];
+                        const uint32_t behind = __shfl(w[3], (lane + 48) & 63), before = g ? behind : carry;
+                        carry = behind;
+                        if (odd) {
+                            v.w[0] = xu32x4{w[0] << 16 | before >> 16, w[1] << 16 | w[0] >> 16, w[2] << 16 | w[1] >> 16,
+                                            w[3] << 16 | w[2] >> 16};
+                            uint16_t* edge = reinterpret_cast<uint16_t*>(to);
+                            if (i == SH::TN - 2 && g == 3 && at + 7 < o.cols) edge[7] = (uint16_t)(w[3] >> 16);
+                            if (i == 0 && g == 0) {
+                                if (at < o.cols) edge[0] = (uint16_t)w[0];
+                                if (at + 1 < o.cols)
+                                    store_some(to + 1, Eight<T>{{xu32x4{v.w[0][1], v.w[0][2], v.w[0][3], 0}}},
+                                               o.cols - at < 7 ? o.cols - at - 1 : 6);
+                                continue;
+                            }
+                        }
+                    }
+                    if (at - odd + 8 <= o.cols) {
 #pragma unroll
-                    for (int q = 0; q < (int)sizeof(T) / 2; ++q) reinterpret_cast<Word*>(p + i * 16)[q] = u.q[q];
-                } else if (at < o.cols) {
-                    store_some(p + i * 16, u.w, o.cols - at);
+                        for (int q = 0; q < (int)sizeof(T) / 2; ++q) reinterpret_cast<Word*>(to - odd)[q] = v.w[q];
+                    } else if (at - odd < o.cols) {
+                        store_some(to - odd, v, o.cols - at + odd);
+                    }
                 }
             }
         }
@@ -467,7 +506,8 @@ __device__ __forceinline__ void run_tile(const Tile& t, const Out<T>& o, uint8_t
 #pragma unroll
         for (int i = 0; i < SH::TN; ++i) acc[j][i] = f32x4{0, 0, 0, 0};
     if (t.blocks) tile_product<SH>(t, lds, acc);
-    if (o.cols >= (uint32_t)SH::BN) store_tile<T, SH, false>(o, acc);
+    const bool odd = sizeof(T) == 2 && (((uintptr_t)o.out >> 1 | o.stride) & 1);
+    if (o.cols >= (uint32_t)SH::BN && !odd) store_tile<T, SH, false>(o, acc);
     else store_tile<T, SH, true>(o, acc);
 #endif
 }
@@ -822,7 +862,7 @@ WeightGradPlan plan_weight_grad(uint32_t rows, uint32_t experts, uint32_t n, uin
     //   128, 512, 2048 (16 experts 512 x 1024, 32768 rows)      109/60/67
     //   16, 64, 256 (1 expert 1024 x 1024, 4096 rows)           42/20/15
     // and do not go past n and k by more than half:
-    //   215 experts 24 x 1043, most without rows                61 (256 wide) / TODO
+    //   215 experts 24 x 1043, most without rows                whole step with casts 61 (256 wide) / 38 (64 wide)
     auto snug = [&](uint32_t side) { return tiles(side) * side * side * 2 <= (uint64_t)experts * n * k * 3; };
     if (tiles(256) >= 256 && snug(256)) return WeightGradPlan{256, 1};
     // Few tiles and long segments: a CU draws some 50 GB/s past its L2, so the
