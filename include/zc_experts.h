@@ -37,7 +37,8 @@
  * Conventions are zc.h's: device memory is the caller's; calls only enqueue
  * work on `stream` (no allocation, no synchronisation, no device memory read
  * on the host); argument errors are returned synchronously and enqueue
- * nothing; calls sharing a workspace must not overlap.  Strides are in
+ * nothing; calls sharing a workspace must not overlap, nor may what a call
+ * writes overlap what it reads.  Strides are in
  * elements between rows, the last dimension is contiguous.  Row-like buffers
  * need their element's alignment only (16-byte aligned pointers and strides
  * are faster); 8-bit data and scales need 16 bytes, workspaces 256.

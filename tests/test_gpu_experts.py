@@ -188,6 +188,37 @@ def test_combine_backward(tokens, topk, experts, align, hidden, dtype, pad, want
         assert (got[row < 0] == 0).all()
 
 
+@pytest.mark.parametrize("hidden,dtype,pad", [(2048, "bf16", 0), (2049, "bf16", 0), (2053, "fp16", 1), (1100, "fp32", 1),
+                                              (2056, "bf16", 64), (4120, "fp16", 0), (1024, "bf16", 9)])
+def test_rows_past_the_caches(hidden, dtype, pad):
+    """Row buffers past 256 MB, whose stores go around the caches, at every
+    kind of row start: multiples of 64 bytes, of 16, of 4 and of 2."""
+    topk, experts, align = 6, 19, 4
+    tokens = (256 << 20) // (topk * hidden * DT[dtype].itemsize) + 77
+    plan, ids, r = routed(tokens, topk, experts, align, seed=hidden, drop=0.1)
+    x, _ = strided(tokens, hidden, DT[dtype], 0)
+    g = torch.Generator("cuda").manual_seed(hidden)
+    x.normal_(generator=g)
+    weights = torch.rand(tokens, topk, device="cuda", generator=g)
+    rows, whole = strided(plan.rows, hidden, DT[dtype], pad)
+    plan.dispatch(x, r, rows)
+    used = int(r.offsets[-1])
+    slot = r.slot[:used].long()
+    token = slot.clamp(min=0) // topk
+    assert torch.equal(rows[:used], torch.where((slot >= 0)[:, None], x[token], 0))
+    assert torch.isnan(rows[used:]).all() and torch.isnan(whole[:, hidden:]).all()
+    live = rows.clone()  # dispatched rows, as an expert's outputs
+    want = torch.where((slot >= 0)[:, None], weights.reshape(-1)[slot.clamp(min=0)][:, None] * x[token].double(), 0)
+    for with_weights in (False, True):
+        whole.fill_(float("nan"))
+        dw = torch.full((tokens, topk), float("nan"), device="cuda") if with_weights else None
+        plan.combine_backward(x, live if with_weights else None, weights, r, rows, dw)
+        assert ((rows[:used].double() - want).abs() <= (plain.U[dtype] * 1.01 + 2.0 ** -24) * want.abs() + 2.0 ** -25).all()
+        assert torch.isnan(rows[used:]).all() and torch.isnan(whole[:, hidden:]).all()
+    size = x.double().square().sum(1)[:, None]  # <dy, R>: rows are the tokens' own
+    assert ((dw - torch.where(r.row >= 0, size, 0)).abs() <= size * (hidden * 2.0**-24)).all()
+
+
 def test_gradients_are_those_of_differences():
     """<dispatch(x), g> and combine are linear in each argument, so a
     difference of any step is the derivative up to 32-bit rounding."""
