@@ -134,6 +134,25 @@ __device__ __forceinline__ float to_float(float v) { return v; }
 // wave has it.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// 16 bytes of values at any element's address, zeros past the first n (n <= 0:
+// all): a short word comes in parts of 8, 4 and 2 bytes.
+template <typename T>
+__device__ __forceinline__ xu32x4 load_word(const T* p, int32_t n) {
+    typedef xu32x4 __attribute__((aligned(2))) Four;
+    typedef xu32x2 __attribute__((aligned(2))) Two;
+    typedef uint32_t __attribute__((aligned(2))) One;
+    if (n >= 16 / (int32_t)sizeof(T)) return *reinterpret_cast<const Four*>(p);
+    if (n <= 0) return xu32x4{};
+    const uint32_t bytes = (uint32_t)n * sizeof(T);
+    xu32x2 two = {0, 0};
+    uint32_t one = 0, half = 0;
+    if (bytes & 8) two = *reinterpret_cast<const Two*>(p);
+    if (bytes & 4) one = *reinterpret_cast<const One*>(p + (bytes & 8) / sizeof(T));
+    if (sizeof(T) == 2 && bytes & 2) half = *reinterpret_cast<const uint16_t*>(p + (bytes & 12) / sizeof(T));
+    const uint32_t next = bytes & 4 ? one : half, past = bytes & 4 ? half : 0;
+    return bytes & 8 ? xu32x4{two[0], two[1], next, past} : xu32x4{next, past, 0, 0};
+}
+
 // The byte of the least scale s = 2^(b-127) with top <= 448 s, top given as
 // the bits of a finite float >= 0: 448 = 1.75 * 2^8, so the exponent of top
 // less 8, one more where its mantissa passes 1.75; at least 2^-126 (so that
