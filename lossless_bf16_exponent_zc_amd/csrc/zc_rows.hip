@@ -141,6 +141,18 @@ __device__ __forceinline__ void zero_padding(const RowArgs& a) {
     }
 }
 
+// A row's last word moved to the row's end, over its neighbour, so that it is
+// whole (where the row has a word).
+struct Last {
+    uint32_t at, n;
+};
+template <typename T>
+__device__ __forceinline__ Last last_moved(uint32_t col, uint32_t width) {
+    constexpr uint32_t N = Pack<T>::N;
+    if (width < N) return Last{0, width};
+    return Last{col + N <= width ? col : width - N, N};
+}
+
 template <typename T, bool WAVE, Mode MODE>
 __global__ __launch_bounds__(256) void dispatch_rows(RowArgs a, Split s) {
     if (blockIdx.x < s.pad_blocks) {
@@ -162,10 +174,11 @@ __global__ __launch_bounds__(256) void dispatch_rows(RowArgs a, Split s) {
         }
     } else {
         if (at.col >= a.width) return;
-        const Pack<T> x = load<T, false>(in + at.col, a.width - at.col);
+        const Last c = last_moved<T>(at.col, a.width);
+        const Pack<T> x = load<T, false>(in + c.at, c.n);
         for (uint32_t k = 0; k < a.topk; ++k) {
             const uint32_t r = (uint32_t)row[k];
-            if (r < a.capacity) store<T, MODE == kPast>(row_of<T>(a.out, r, a.out_stride) + at.col, x, a.width - at.col);
+            if (r < a.capacity) store<T, MODE == kPast>(row_of<T>(a.out, r, a.out_stride) + c.at, x, c.n);
         }
     }
 }
@@ -175,32 +188,135 @@ __global__ __launch_bounds__(256) void combine_rows(RowArgs a, Split s) {
     typedef Pack<T> P;
     const Place at = place_of<T, WAVE>(s);
     if (at.token >= a.tokens || at.col >= a.width) return;
-    const uint32_t n = a.width - at.col;
+    const Last c = last_moved<T>(at.col, a.width);
     float acc[P::N] = {};
     const int32_t* row = a.row + (uint64_t)at.token * a.topk;
     const float* weight = a.weights ? a.weights + (uint64_t)at.token * a.topk : nullptr;
-#pragma unroll 4
-    for (uint32_t k = 0; k < a.topk; ++k) {
-        const uint32_t r = (uint32_t)row[k];
-        if (r >= a.capacity) continue;
-        const float w = weight ? weight[k] : 1.0f;
-        const P x = load<T, PAST>(row_of<const T>(a.x, r, a.x_stride) + at.col, n);
+    // GROUP rows at a time are asked for before any is used (a slot without a
+    // row reads row 0 and adds nothing): two where latency counts, as four or
+    // eight read more than few slots have (4096 tokens, 2 rows of 2048 values,
+    // by 1 / 2 / 4 / 8: 9.2 / 8.9 / 10.1 / 12.9 us; 64 tokens, 8 rows of 7168:
+    // 4.1 / 3.9 / 3.7 / 3.5); one for the largest (8192 tokens, 8 rows of
+    // 7168, by 1 / 2 / 4: 177 / 183 / 182)
+    constexpr uint32_t GROUP = PAST ? 1 : 2;
+    const uint32_t rows = a.capacity ? a.topk : 0;
+    for (uint32_t k0 = 0; k0 < rows; k0 += GROUP) {
+        P x[GROUP];
+        float w[GROUP];
+        bool any[GROUP];
 #pragma unroll
-        for (int i = 0; i < P::N; ++i) acc[i] = __builtin_fmaf(w, to_float(x.v[i]), acc[i]);
+        for (uint32_t g = 0; g < GROUP; ++g) {
+            const uint32_t k = k0 + g < rows ? k0 + g : rows - 1, r = (uint32_t)row[k];
+            any[g] = k0 + g < rows && r < a.capacity;
+            w[g] = weight ? weight[k] : 1.0f;
+            x[g] = load<T, PAST>(row_of<const T>(a.x, r < a.capacity ? r : 0, a.x_stride) + c.at, c.n);
+        }
+#pragma unroll
+        for (uint32_t g = 0; g < GROUP; ++g)
+#pragma unroll
+            for (int i = 0; i < P::N; ++i) acc[i] = any[g] ? __builtin_fmaf(w[g], to_float(x[g].v[i]), acc[i]) : acc[i];
     }
     P y;
 #pragma unroll
     for (int i = 0; i < P::N; ++i) y.v[i] = (T)acc[i];
-    store<T, PAST>(row_of<T>(a.out, at.token, a.out_stride) + at.col, y, n);
+    store<T, PAST>(row_of<T>(a.out, at.token, a.out_stride) + c.at, y, c.n);
 }
 
-// L threads per token (a workgroup or less); kGroup slots at a time (dy is
-// read again, from the cache, for every further group).
-constexpr int kGroup = 8;
+// The gradient for G slots of a token from k0 on, by L threads.  The rows of
+// all G are asked for before any is used: a load behind a branch waits for the
+// one before it (one token of 8 rows of 7168 values: 13.4 us; so 7.5).  So a
+// slot without a row reads dy, and its sum is dropped.
+template <typename T, int L, Mode MODE, int G>
+__device__ __forceinline__ void backward_group(const RowArgs& a, uint64_t t, uint32_t thread, uint32_t k0,
+                                               float (*part)[8]) {
+    typedef Pack<T> P;
+    const T* dy = row_of<const T>(a.x, t, a.x_stride);
+    const T* in[G];
+    T* out[G];
+    float w[G], acc[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const uint32_t k = k0 + g < a.topk ? k0 + g : a.topk - 1;
+        const uint32_t r = (uint32_t)a.row[t * a.topk + k];
+        const bool any = k0 + g < a.topk && r < a.capacity;
+        w[g] = a.weights ? a.weights[t * a.topk + k] : 1.0f;
+        acc[g] = 0.0f;
+        in[g] = any && a.dweights ? row_of<const T>(a.rows, r, a.rows_stride) : dy;
+        out[g] = any && a.out ? row_of<T>(a.out, r, a.out_stride) : nullptr;
+    }
+    if constexpr (MODE == kPastShifted) {  // no dweights
+        for (uint32_t c = thread * P::N; c < a.width + 63 / sizeof(T); c += L * P::N) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const Shifted s = shifted(out[g], c, a.width);
+                if (!out[g] || !s.any) continue;
+                const P d = load<T, false>(dy + s.at, P::N);
+                P o;
+#pragma unroll
+                for (int i = 0; i < P::N; ++i) o.v[i] = (T)(w[g] * to_float(d.v[i]));
+                store<T, true>(out[g] + s.at, o, P::N);
+            }
+        }
+        return;
+    }
+    // n values from c on, of which the first `skip` are another word's
+    auto word = [&](uint32_t c, uint32_t n, uint32_t skip) {
+        const P d = load<T, false>(dy + c, n);
+        P x[G];
+        if (a.dweights)
+#pragma unroll
+            for (int g = 0; g < G; ++g) x[g] = load<T, false>(in[g] + c, n);
+        if (a.out)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                P o;
+#pragma unroll
+                for (int i = 0; i < P::N; ++i) o.v[i] = (T)(w[g] * to_float(d.v[i]));
+                if (out[g]) store<T, MODE == kPast>(out[g] + c, o, n);
+            }
+        if (!a.dweights) return;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < P::N; ++i)
+                if (i >= (int)skip) acc[g] = __builtin_fmaf(to_float(d.v[i]), to_float(x[g].v[i]), acc[g]);
+    };
+    if (a.width < P::N) {
+        if (thread == 0) word(0, a.width, 0);
+    } else {
+        for (uint32_t c = thread * P::N; c < a.width; c += L * P::N) {
+            // the last word is moved to the row's end, over its neighbour,
+            // which stores the same there
+            const uint32_t at = c + P::N <= a.width ? c : a.width - P::N;
+            word(at, P::N, c - at);
+        }
+    }
+    if (!a.dweights) return;
+    float mine = 0.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        for (int m = L < 64 ? L / 2 : 32; m; m >>= 1) acc[g] += __shfl_xor(acc[g], m);
+        if ((int)thread == g) mine = acc[g];
+    }
+    if constexpr (L > 64) {
+        if (k0) __syncthreads();  // the last group's sums have been read
+        if (__lane_id() == 0)
+#pragma unroll
+            for (int g = 0; g < G; ++g) part[threadIdx.x >> 6][g] = acc[g];
+        __syncthreads();
+        if (thread < G) mine = (part[0][thread] + part[1][thread]) + (part[2][thread] + part[3][thread]);
+    }
+    if (thread < G && k0 + thread < a.topk) {
+        const uint64_t slot = t * a.topk + k0 + thread;
+        a.dweights[slot] = (uint32_t)a.row[slot] < a.capacity ? mine : 0.0f;
+    }
+}
 
+// L threads per token (a workgroup or less); 8, 4 or 2 slots at a time (dy is
+// read again, from the cache, for every further group).
 template <typename T, int L, Mode MODE>
 __global__ __launch_bounds__(256) void combine_rows_backward(RowArgs a, uint32_t pad_blocks) {
-    typedef Pack<T> P;
+    __shared__ float part[L > 64 ? 4 : 1][8];
     if (blockIdx.x < pad_blocks) {
         zero_padding<T>(a);
         return;
@@ -208,68 +324,14 @@ __global__ __launch_bounds__(256) void combine_rows_backward(RowArgs a, uint32_t
     const uint32_t thread = threadIdx.x % L, sub = threadIdx.x / L;
     const uint64_t t = (uint64_t)(blockIdx.x - pad_blocks) * (256 / L) + (L >= 64 ? uniform(sub) : sub);
     if (t >= a.tokens) return;  // L = 256: no workgroup
-    const T* dy = row_of<const T>(a.x, t, a.x_stride);
-    for (uint32_t k0 = 0; k0 < a.topk; k0 += kGroup) {
-        uint32_t r[kGroup];
-        float w[kGroup], acc[kGroup];
-#pragma unroll
-        for (int g = 0; g < kGroup; ++g) {
-            const uint32_t k = k0 + g;
-            r[g] = k < a.topk ? (uint32_t)a.row[t * a.topk + k] : ~0u;
-            w[g] = k < a.topk && a.weights ? a.weights[t * a.topk + k] : 1.0f;
-            acc[g] = 0.0f;
-        }
-        const uint32_t end = a.width + (MODE == kPastShifted ? 63 / sizeof(T) : 0);
-        for (uint32_t c = thread * P::N; c < end; c += L * P::N) {
-            const uint32_t n = a.width - c;
-            P d;
-            if (MODE != kPastShifted) d = load<T, false>(dy + c, n);
-#pragma unroll
-            for (int g = 0; g < kGroup; ++g) {
-                if (r[g] >= a.capacity) continue;
-                if constexpr (MODE == kPastShifted) {  // no dweights
-                    T* out = row_of<T>(a.out, r[g], a.out_stride);
-                    const Shifted s = shifted(out, c, a.width);
-                    if (!s.any) continue;
-                    d = load<T, false>(dy + s.at, P::N);
-                    P o;
-#pragma unroll
-                    for (int i = 0; i < P::N; ++i) o.v[i] = (T)(w[g] * to_float(d.v[i]));
-                    store<T, true>(out + s.at, o, P::N);
-                } else {
-                    if (a.dweights) {
-                        const P x = load<T, false>(row_of<const T>(a.rows, r[g], a.rows_stride) + c, n);
-#pragma unroll
-                        for (int i = 0; i < P::N; ++i)
-                            acc[g] = __builtin_fmaf(to_float(d.v[i]), to_float(x.v[i]), acc[g]);
-                    }
-                    if (a.out) {
-                        P o;
-#pragma unroll
-                        for (int i = 0; i < P::N; ++i) o.v[i] = (T)(w[g] * to_float(d.v[i]));
-                        store<T, MODE == kPast>(row_of<T>(a.out, r[g], a.out_stride) + c, o, n);
-                    }
-                }
-            }
-        }
-        if (MODE == kPastShifted || !a.dweights) continue;
-        float mine = 0.0f;
-#pragma unroll
-        for (int g = 0; g < kGroup; ++g) {
-            for (int m = L < 64 ? L / 2 : 32; m; m >>= 1) acc[g] += __shfl_xor(acc[g], m);
-            if ((int)thread == g) mine = acc[g];
-        }
-        if constexpr (L > 64) {
-            __shared__ float part[4][kGroup];
-            if (k0) __syncthreads();  // the last group's sums have been read
-            if (__lane_id() == 0)
-#pragma unroll
-                for (int g = 0; g < kGroup; ++g) part[threadIdx.x >> 6][g] = acc[g];
-            __syncthreads();
-            if (thread < kGroup) mine = (part[0][thread] + part[1][thread]) + (part[2][thread] + part[3][thread]);
-        }
-        if (thread < kGroup && k0 + thread < a.topk) a.dweights[t * a.topk + k0 + thread] = mine;
-    }
+    uint32_t k = 0;
+    // 16 threads a token keep the addresses of 8 slots in general registers,
+    // too many (20,000 tokens, 12 rows of 100 values, without dweights: 14.6 us
+    // by 8, 13.0 by 4)
+    constexpr uint32_t MOST = L < 64 ? 4 : 8;
+    for (; k + MOST / 2 < a.topk; k += MOST) backward_group<T, L, MODE, MOST>(a, t, thread, k, part);
+    if (MOST == 8 && k + 2 < a.topk) backward_group<T, L, MODE, 4>(a, t, thread, k, part);
+    else if (k < a.topk) backward_group<T, L, MODE, 2>(a, t, thread, k, part);
 }
 
 // The widest tx that leaves at most an eighth of the threads without a word,
@@ -348,16 +410,16 @@ zc_status backward_by(const RowArgs& a, hipStream_t stream) {
 
 // Threads per token, in us (4096 tokens, 4 rows each, unless stated):
 //            16 / 64 / 256 threads
-//    200 values    6.9 /  7.6 /  14
-//    400          11.8 /  8.8 /  16
-//   1001          23.5 / 16.4 /  24
-//   1500            32 /   23 /  27
-//   2048 (8192 tokens, 8 rows)  171 / 157 / 112
+//    200 values    5.0 /  6.0 / 12
+//   1001          16.1 / 15.8 / 20
+//   1500          22.8 / 22.3 / 26
+//   2048 (8192 tokens, 8 rows)  133 / 107 /  94
+//   1001 (512 tokens)           9.9 / 6.2 / 5.4
 template <typename T>
 zc_status backward_as(const RowArgs& a, hipStream_t stream) {
     const uint32_t words = (a.width + Pack<T>::N - 1) / Pack<T>::N;
     if (words <= 32) return backward_by<T, 16>(a, stream);
-    return words <= 192 ? backward_by<T, 64>(a, stream) : backward_by<T, 256>(a, stream);
+    return words <= 192 && a.tokens > 1024 ? backward_by<T, 64>(a, stream) : backward_by<T, 256>(a, stream);
 }
 
 }  // namespace
