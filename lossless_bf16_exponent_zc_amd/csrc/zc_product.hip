@@ -9,6 +9,8 @@
 // a lane then has four neighbouring columns j of one row r.
 #include "zc_experts_kernels.h"
 
+#include <algorithm>
+
 namespace zc {
 
 namespace {
@@ -41,6 +43,11 @@ struct WideCut {
 };
 struct MidCut {
     static constexpr uint32_t kRows = 128, kCols = 128, kShort = 0;
+    static constexpr int kStages = 4;
+};
+struct PairCut {  // MidCut's tiles, two workgroups on a CU
+    static constexpr uint32_t kRows = 128, kCols = 128, kShort = 0;
+    static constexpr int kStages = 2;
 };
 struct SmallCut {
     static constexpr uint32_t kRows = 64, kCols = 64, kShort = 0;
@@ -546,8 +553,8 @@ __global__ __launch_bounds__(256, 1) void product(ProductArgs p, uint32_t col_ti
         } else if constexpr (Cut::kRows == 64) {
             run_tile<Shape<2, 2, 2, 8, false>>(t, o, lds);
         } else {
-            if (f.count > 64) run_tile<Shape<2, 4, 4, 4, false>>(t, o, lds);
-            else run_tile<Shape<1, 4, 2, 4, false>>(t, o, lds);
+            if (f.count > 64) run_tile<Shape<2, 4, 4, Cut::kStages, false>>(t, o, lds);
+            else run_tile<Shape<1, 4, 2, Cut::kStages, false>>(t, o, lds);
         }
     }
     zero_padding(o, f, Cut::kRows, Cut::kCols);
@@ -750,6 +757,8 @@ static_assert(kLdsProduct <= 160 * 1024 && Shape<2, 8, 8, 2, false>::kLds <= kLd
               "one LDS allocation serves every shape");
 constexpr int kLdsMid = Shape<2, 4, 4, 4, false>::kLds;
 static_assert(Shape<1, 4, 2, 4, false>::kLds <= kLdsMid, "one LDS allocation serves every shape");
+constexpr int kLdsPair = Shape<2, 4, 4, 2, false>::kLds;
+static_assert(Shape<1, 4, 2, 2, false>::kLds <= kLdsPair && 2 * kLdsPair <= 160 * 1024, "two workgroups on a CU");
 constexpr int kLdsSmall = Shape<2, 2, 2, 8, false>::kLds;
 
 // More LDS than the default limit has to be asked for, once per device.
@@ -763,15 +772,21 @@ void allow_lds(K kernel, int bytes) {
 namespace {
 
 // Which cut, from what the host knows: rows, experts, n (not the counts).
-// Measured, in us, at n 4096, k 7168 where not said (wide / mid / small / few):
-//   few    up to 4 rows an expert and 32 more: 16 rows, 1 expert 28/24/20/13;
-//          64 rows, 8 experts, n 14336, k 4096 116/110/117/95; 128 rows, 32
-//          experts 164/163/181/164, but 512 rows there 234/174/201/217
-//   wide   from 128 tiles of 256 whole rows: 4096 rows, 1 expert 94/156/324/644;
-//          2048 rows 78/72; 16384 rows, 16 experts, n 512, k 1024 22/32
-//   small  where mid has at most 64 tiles: 128 rows, 1 expert 49/33/22/25; 256
-//          rows 70/33/24/46, but 512 rows 70/34/44/85
-//   mid    else: 1024 rows, 32 experts 241/180/230/290
+// Measured, in us, at n 4096, k 7168 where not said (wide / mid / pair):
+//   few    up to 4 rows an expert and 32 more, against mid / small: 16 rows, 1
+//          expert 13/24/20; 64 rows, 8 experts, n 14336, k 4096 95/110/117; 128
+//          rows, 32 experts 164/163/181, but 512 rows there 217/174/201
+//   wide   where its tiles fill most CUs, and an expert's rows most of a tile:
+//          4096 rows, 1 expert 92/149/127, but 2048 rows 79/76/62; 16384 rows,
+//          16 experts, n 512, k 1024 23/32/28; 2048 rows, 32 experts 254/206/211
+//   small  where mid has at most 64 tiles: 128 rows, 1 expert 22 (mid 33); 256
+//          rows 24 (33), but 512 rows 44 (34)
+//   pair   where mid has more tiles than CUs, so that one's stores run beside
+//          the other's loads, but not for many blocks of few rows, whose loads
+//          need mid's depth: 5947 rows, 201 experts, n 849, k 113 34/31/20; 8423
+//          rows, 1 expert, n 543, k 4297 51/49/41; but 1024 rows, 32 experts
+//          245/180/199, and 1024 rows, 1 expert (256 tiles) 72/39/47
+//   mid    else
 template <typename T>
 zc_status product_as(const ProductArgs& a, hipStream_t stream) {
     const uint64_t segments = a.offsets ? a.experts : 1;
@@ -791,7 +806,8 @@ zc_status product_as(const ProductArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL((product_few<T>), dim3((uint32_t)grid), dim3(256), 0, stream, a, cols(FewCut::kCols));
         return ZC_OK;
     }
-    if ((uint64_t)(a.rows / WideCut::kRows) * cols(WideCut::kCols) >= 128) {
+    const uint64_t whole = a.rows / WideCut::kRows, ends = std::min(used / 2, whole / 4);
+    if ((whole + ends) * cols(WideCut::kCols) >= 144 && a.rows >= 128 * used) {
         const uint64_t s = a.rows / WideCut::kRows + segments, c = cols(WideCut::kCols);
         if (s * c <= 512) return in_order(product<T, WideCut>, WideCut{}, kLdsProduct);
         // runs: each kind's slots rounded up to 4, its tiles to runs of 32, its
@@ -802,7 +818,10 @@ zc_status product_as(const ProductArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL((product<T, WideCut>), dim3((uint32_t)grid), dim3(256), kLdsProduct, stream, a, (uint32_t)c, kRuns);
         return ZC_OK;
     }
-    if ((a.rows / MidCut::kRows + used) * cols(MidCut::kCols) <= 64) return in_order(product<T, SmallCut>, SmallCut{}, kLdsSmall);
+    const uint64_t rest = a.experts > 1 ? used : a.rows % MidCut::kRows ? 1 : 0;
+    const uint64_t tiles = (a.rows / MidCut::kRows + rest) * cols(MidCut::kCols);
+    if (tiles <= 64) return in_order(product<T, SmallCut>, SmallCut{}, kLdsSmall);
+    if (tiles > 256 && (a.k <= 2048 || a.rows >= 64 * a.experts)) return in_order(product<T, PairCut>, PairCut{}, kLdsPair);
     return in_order(product<T, MidCut>, MidCut{}, kLdsMid);
 }
 
