@@ -10,6 +10,7 @@
 #include "zc_experts_kernels.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace zc {
 
@@ -281,8 +282,12 @@ __device__ __forceinline__ void tile_product(const Tile& t, uint8_t* lds, f32x4 
     const uint32_t at_as = SH::BY_BLOCK ? arow & ~3u : arow * t.as_stride;
     const uint32_t at_ws = SH::BY_BLOCK ? wrow & ~3u : (wrow >> 7) * t.ws_stride;
 
-    // the n-th of a wave's loads of a block; blocks past the last are loaded
-    // again, so that the loads in flight do not depend on where the loop stands
+    // the n-th of a wave's loads of a block.  PAST_END: blocks past the last are
+    // loaded again instead of none, so that the loop is one piece; short sums
+    // are faster without (256 experts 128 x 512 of 256 rows 43 -> 32 us), long
+    // ones of the widest product's with (8192 rows, n 4096, k 7168 177 -> 170)
+    constexpr bool PAST_END = SH::TM == 8 && !SH::BY_BLOCK;
+    auto clamped = [&](uint32_t block) { return PAST_END && block >= t.blocks ? t.blocks - 1 : block; };
     auto load_one = [&](int n, uint32_t block, uint8_t* base) {
         const uint64_t sa = SH::BY_BLOCK ? (uint64_t)block * t.as_stride : block & ~3u;
         const uint64_t sw = SH::BY_BLOCK ? (uint64_t)block * t.ws_stride : block & ~3u;
@@ -300,8 +305,6 @@ __device__ __forceinline__ void tile_product(const Tile& t, uint8_t* lds, f32x4 
             __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(t.ws + sw), (lds_void*)(base + SH::kScaleAt + 1024 + wave * 256),
                                                      4, at_ws, 0, 0, 0);
     };
-    auto clamped = [&](uint32_t block) { return block < t.blocks ? block : t.blocks - 1; };
-
     const uint32_t wave_a = (wave / SH::WN) * SH::TM * 16, wave_w = (wave % SH::WN) * SH::TN * 16;
     // where a lane's two pieces of a row lie (pieces g and g + 4)
     const uint32_t a_lo = (wave_a + r) * 128 + ((g ^ turn_a(r)) << 4), a_hi = a_lo ^ 64;
@@ -326,11 +329,12 @@ __device__ __forceinline__ void tile_product(const Tile& t, uint8_t* lds, f32x4 
     };
 
     uint8_t* base = lds;
-    for (int s = 0; s < SH::S; ++s) {
+    for (uint32_t s = 0; s < SH::S && (PAST_END || s < t.blocks); ++s) {
 #pragma unroll
         for (int n = 0; n < SH::kLoads; ++n) load_one(n, clamped(s), lds + s * SH::kStage);
     }
-    wait_loads_and_barrier<(SH::S - 1) * SH::kLoads>();
+    if (PAST_END || t.blocks >= SH::S) wait_loads_and_barrier<(SH::S - 1) * SH::kLoads>();
+    else wait_loads_and_barrier<0>();
     Side w[SH::TN], first = read_a(base, 0);
 #pragma unroll
     for (int i = 0; i < SH::TN; ++i) read_w(base, i, w[i]);
@@ -344,7 +348,9 @@ __device__ __forceinline__ void tile_product(const Tile& t, uint8_t* lds, f32x4 
     // two tiles the next block's weight side replaces this one's.
     constexpr int HALF = SH::TM / 4 * 2, kEach = HALF ? (SH::TM - 2 + HALF) / HALF : 0;
     constexpr int kRest = (SH::TM - HALF) * SH::TN;
-    for (uint32_t b = 0; b < t.blocks; ++b) {
+    // MORE: the block S later exists; without it all loads in flight are waited for.
+    auto one_block = [&](auto more, uint32_t b) {
+        constexpr bool MORE = decltype(more)::value;
         const uint32_t shift = SH::BY_BLOCK ? 0 : (b & 3) * 8;
         uint32_t sw[SH::TN];
         Side a[SH::TM];
@@ -362,15 +368,16 @@ __device__ __forceinline__ void tile_product(const Tile& t, uint8_t* lds, f32x4 
             __builtin_amdgcn_sched_barrier(0);
         }
         if (HALF == 0) a[1] = read_a(base, 1);
-        wait_loads_and_barrier<(SH::S - 2) * SH::kLoads>();
+        wait_loads_and_barrier<MORE ? (SH::S - 2) * SH::kLoads : 0>();
         __builtin_amdgcn_sched_barrier(0);
         uint8_t* const free = base;
         const uint32_t ahead = clamped(b + SH::S);
         base = base == lds + (SH::S - 1) * SH::kStage ? lds : base + SH::kStage;
         int done = 0;
         auto load_share = [&](int at) {  // the loads due by the at-th instruction
+            if (MORE)
 #pragma unroll
-            for (; done < SH::kLoads && done * kRest < at * SH::kLoads; ++done) load_one(done, ahead, free);
+                for (; done < SH::kLoads && done * kRest < at * SH::kLoads; ++done) load_one(done, ahead, free);
             __builtin_amdgcn_sched_barrier(0);
         };
 #pragma unroll
@@ -392,11 +399,15 @@ __device__ __forceinline__ void tile_product(const Tile& t, uint8_t* lds, f32x4 
             read_w(base, i, w[i]);
             load_share(kRest - 2 * (SH::TN - 1 - i));
         }
-    }
+    };
+    uint32_t b = 0;
+    for (; b + (PAST_END ? 0 : SH::S) < t.blocks; ++b) one_block(std::true_type{}, b);
+    if (!PAST_END)
+        for (; b < t.blocks; ++b) one_block(std::false_type{}, b);
     // the last results are written before anything reads them
     asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-    // no load may still write LDS when the next tile or another workgroup has it
-    wait_loads_and_barrier<0>();
+    // no load may still write LDS when another workgroup has it
+    if (PAST_END) wait_loads_and_barrier<0>();
 }
 
 // An accumulator read where it is written down and no earlier: read ahead of
