@@ -894,13 +894,19 @@ WeightGradPlan plan_weight_grad(uint32_t rows, uint32_t experts, uint32_t n, uin
     // and do not go past n and k by more than half:
     //   215 experts 24 x 1043, most without rows                whole step with casts 61 (256 wide) / 38 (64 wide)
     auto snug = [&](uint32_t side) { return tiles(side) * side * side * 2 <= (uint64_t)experts * n * k * 3; };
-    if (tiles(256) >= 256 && snug(256)) return WeightGradPlan{256, 1};
+    const uint32_t blocks = rows / 128 / experts;
+    // Short segments leave most of the time to the stores, which a pair on a CU
+    // hides; 256 wide / pairs of 128, by blocks of 128 rows an expert:
+    //   37 experts 1000 x 1401  1: 44/39  4: 58/55      16 experts 1408 x 2048  2: 38/27  8: 73/70
+    //   8 experts 4096 x 4096   1: 63/62  3: 94/103     128 experts 1024 x 1024  2: 90/111
+    const bool loose = tiles(256) * 65536 * 20 > (uint64_t)experts * n * k * 21;
+    const bool pairs = tiles(128) >= 512 && (blocks <= 1 || (loose && blocks <= 8));
+    if (tiles(256) >= 256 && snug(256) && !pairs) return WeightGradPlan{256, 1};
     // Few tiles and long segments: a CU draws some 50 GB/s past its L2, so the
     // segments go to more CUs, at the price of the join; whole / in parts:
     //   1 expert 1024 x 1024, 32768 rows  87 (64 wide) / 53 (128 wide, 4 parts)
     //   1 expert 60 x 300, 32768 rows     77 / 16 (64 wide, 16 parts)
     //   but at 32 blocks of 128 rows an expert, 1024 x 1024   15 / 20
-    const uint32_t blocks = rows / 128 / experts;
     if (split && blocks >= 64 && tiles(128) <= 128) {
         const uint32_t side = tiles(64) <= 32 ? 64 : 128;
         const uint64_t most = 256 / tiles(side);
