@@ -759,7 +759,8 @@ __global__ __launch_bounds__(256) void join_parts(WeightGradArgs p, const float*
 typedef Shape<2, 8, 8, 2, true> GradWide;
 typedef Shape<2, 4, 4, 4, true> GradMid;
 typedef Shape<2, 4, 4, 2, true> GradMidPair;  // two workgroups on a CU
-typedef Shape<2, 2, 2, 7, true> GradSmall;
+typedef Shape<2, 2, 2, 4, true> GradSmall;
+typedef Shape<2, 2, 2, 2, true> GradSmallMany;  // four workgroups on a CU
 
 constexpr int kLdsProduct = Shape<1, 2, 4, 4, false>::kLds > Shape<2, 4, 8, 3, false>::kLds ? Shape<1, 2, 4, 4, false>::kLds
                                                                                            : Shape<2, 4, 8, 3, false>::kLds;
@@ -868,6 +869,11 @@ zc_status weight_grad_shaped(const WeightGradArgs& a, T* out, const WeightGradPl
     const uint64_t tiles = (uint64_t)a.experts * ((a.n + 127) / 128) * ((a.k + 127) / 128) * plan.parts;
     if (plan.side == 128 && tiles > 256) return weight_grad_in<T, GradMidPair>(a, out, plan.parts, stream);
     if (plan.side == 128) return weight_grad_in<T, GradMid>(a, out, plan.parts, stream);
+    // likewise, where they outnumber what the CUs hold: 62 experts 62 x 526 of
+    // 896 rows 35 (one to a CU, 7 blocks ahead) / 22 (two, 4) / 18 (four, 2); but 1
+    // expert 1024 x 1024, 4096 rows 12.8 / 12.7 / 19.1
+    const uint64_t small = (uint64_t)a.experts * ((a.n + 63) / 64) * ((a.k + 63) / 64) * plan.parts;
+    if (small > 512) return weight_grad_in<T, GradSmallMany>(a, out, plan.parts, stream);
     return weight_grad_in<T, GradSmall>(a, out, plan.parts, stream);
 }
 
@@ -891,9 +897,10 @@ WeightGradPlan plan_weight_grad(uint32_t rows, uint32_t experts, uint32_t n, uin
     //   192, 704, 2816 (8 experts 1000 x 1401, 32768 rows)      137/87/153
     //   128, 512, 2048 (16 experts 512 x 1024, 32768 rows)      109/60/67
     //   16, 64, 256 (1 expert 1024 x 1024, 4096 rows)           42/20/15
-    // and do not go past n and k by more than half:
-    //   215 experts 24 x 1043, most without rows                whole step with casts 61 (256 wide) / 38 (64 wide)
-    auto snug = [&](uint32_t side) { return tiles(side) * side * side * 2 <= (uint64_t)experts * n * k * 3; };
+    // and do not go past n and k by more than two fifths; in us, 128 / 64 wide:
+    //   241 experts 44 x 1986, 128 rows each    89/70    50 experts 88 x 8791, 128 rows  117/79
+    //   but 100 experts 300 x 1000, 256 rows    30/39 (31% past)
+    auto snug = [&](uint32_t side) { return tiles(side) * side * side * 5 <= (uint64_t)experts * n * k * 7; };
     const uint32_t blocks = rows / 128 / experts;
     // Short segments leave most of the time to the stores, which a pair on a CU
     // hides; 256 wide / pairs of 128, by blocks of 128 rows an expert:
@@ -912,7 +919,7 @@ WeightGradPlan plan_weight_grad(uint32_t rows, uint32_t experts, uint32_t n, uin
         const uint64_t most = 256 / tiles(side);
         return WeightGradPlan{side, most > 16 ? 16u : (uint32_t)most};
     }
-    if (tiles(128) >= 192 && (snug(128) || tiles(64) > 2048)) return WeightGradPlan{128, 1};
+    if (tiles(128) >= 192 && snug(128)) return WeightGradPlan{128, 1};
     return WeightGradPlan{64, 1};
 }
 
