@@ -4,6 +4,12 @@
 //
 // Division by a power of two is exact, so each value is rounded once and the
 // result does not depend on how a block is split over lanes.
+//
+// Bound by memory: the input is read once, into registers, and every block's
+// maximum found there.  Measured, of bytes read and written: rows 16384 x 7168
+// 53 us (6.7 TB/s), weights 64 x 2048 x 1408 101 us (5.5), transposed 106 (5.2),
+// columns 16384 x 7168 66 us (5.3), dispatch of 8192 tokens to 8 rows of 7168 as
+// blocks 92 us (6.4).
 #include "zc_experts_kernels.h"
 
 namespace zc {

@@ -11,8 +11,12 @@
 //
 // Rows are moved in 16-byte words wherever they start (the memory takes words
 // at any element's address; a copy of odd rows of 7169 16-bit values runs at
-// 4.1 TB/s so and at 3.2 by elements); the last, shorter word of a row goes
-// by elements.
+// 4.1 TB/s so and at 3.2 by elements); the last, shorter word of a row is moved
+// to the row's end, over its neighbour.
+//
+// 8192 tokens, 8 rows each, 7168 16-bit values: dispatch 180 us (5.9 TB/s; 211
+// and 5.0, a copy's rate, where x is not in the Infinity Cache), combine 174
+// (6.1 TB/s), gradient 394 (5.1 TB/s).  8 tokens: 3.5 us each, the launch.
 #include "zc_experts_kernels.h"
 
 namespace zc {
