@@ -9,9 +9,8 @@
 // a lane then has four neighbouring columns j of one row r.
 //
 // Long sums are bound by the matrix unit and the chip's clock under it (16,384
-// rows, n 4096, k 7168: 370 us, 2.6 PFLOP/s, 65% of the unit's cycles; that is
-// what 256 x 256 tiles are for, as a CU then needs 64 bytes of operands for 1024
-// products); few rows an expert by the weights (64 rows on 32 experts, n 4096, k
+// rows, n 4096, k 7168: 370 us, 2.6 PFLOP/s, 65% of the unit's cycles; for
+// that the tiles are 256 x 256, a byte of operands for every 128 products); few rows an expert by the weights (64 rows on 32 experts, n 4096, k
 // 7168: 117 us, 5.8 TB/s); short sums by the results' stores (64 experts' weight
 // gradients 2048 x 4096 over 128 rows each: 285 us, 3.8 TB/s).
 #include "zc_experts_kernels.h"

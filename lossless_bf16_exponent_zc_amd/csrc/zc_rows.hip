@@ -19,6 +19,8 @@
 // (6.1 TB/s), gradient 394 (5.1 TB/s).  8 tokens: 3.5 us each, the launch.
 #include "zc_experts_kernels.h"
 
+#include <type_traits>
+
 namespace zc {
 
 namespace {
@@ -197,29 +199,32 @@ __global__ __launch_bounds__(256) void combine_rows(RowArgs a, Split s) {
     const int32_t* row = a.row + (uint64_t)at.token * a.topk;
     const float* weight = a.weights ? a.weights + (uint64_t)at.token * a.topk : nullptr;
     // GROUP rows at a time are asked for before any is used (a slot without a
-    // row reads row 0 and adds nothing): two where latency counts, as four or
-    // eight read more than few slots have (4096 tokens, 2 rows of 2048 values,
-    // by 1 / 2 / 4 / 8: 9.2 / 8.9 / 10.1 / 12.9 us; 64 tokens, 8 rows of 7168:
-    // 4.1 / 3.9 / 3.7 / 3.5); one for the largest (8192 tokens, 8 rows of
-    // 7168, by 1 / 2 / 4: 177 / 183 / 182)
-    constexpr uint32_t GROUP = PAST ? 1 : 2;
+    // row reads row 0 and adds nothing): two where latency counts (64 tokens, 8
+    // rows of 7168 values, by 1 / 2 / 4 / 8: 4.1 / 3.9 / 3.7 / 3.5 us; 4096 tokens,
+    // 2 rows of 2048: 9.2 / 8.9 / 10.1 / 12.9); one for the largest (8192 tokens,
+    // 8 rows of 7168, by 1 / 2 / 4: 177 / 183 / 182)
+    constexpr int GROUP = PAST ? 1 : 2;
     const uint32_t rows = a.capacity ? a.topk : 0;
-    for (uint32_t k0 = 0; k0 < rows; k0 += GROUP) {
-        P x[GROUP];
-        float w[GROUP];
-        bool any[GROUP];
+    auto add = [&](auto count, uint32_t k0) {
+        constexpr int G = decltype(count)::value;
+        P x[G];
+        float w[G];
+        bool any[G];
 #pragma unroll
-        for (uint32_t g = 0; g < GROUP; ++g) {
-            const uint32_t k = k0 + g < rows ? k0 + g : rows - 1, r = (uint32_t)row[k];
-            any[g] = k0 + g < rows && r < a.capacity;
-            w[g] = weight ? weight[k] : 1.0f;
-            x[g] = load<T, PAST>(row_of<const T>(a.x, r < a.capacity ? r : 0, a.x_stride) + c.at, c.n);
+        for (int g = 0; g < G; ++g) {
+            const uint32_t r = (uint32_t)row[k0 + g];
+            any[g] = r < a.capacity;
+            w[g] = weight ? weight[k0 + g] : 1.0f;
+            x[g] = load<T, PAST>(row_of<const T>(a.x, any[g] ? r : 0, a.x_stride) + c.at, c.n);
         }
 #pragma unroll
-        for (uint32_t g = 0; g < GROUP; ++g)
+        for (int g = 0; g < G; ++g)
 #pragma unroll
             for (int i = 0; i < P::N; ++i) acc[i] = any[g] ? __builtin_fmaf(w[g], to_float(x[g].v[i]), acc[i]) : acc[i];
-    }
+    };
+    uint32_t k = 0;
+    for (; k + GROUP <= rows; k += GROUP) add(std::integral_constant<int, GROUP>{}, k);
+    if (k < rows) add(std::integral_constant<int, 1>{}, k);
     P y;
 #pragma unroll
     for (int i = 0; i < P::N; ++i) y.v[i] = (T)acc[i];
