@@ -377,6 +377,34 @@ def test_product_of_whole_numbers_is_exact(counts, align, n, k, out_dtype):
     assert bool(torch.isnan(got[off[-1]:]).all()) and guard_intact(whole, n)
 
 
+SHAPES = [  # sizes that reach every shape of tile, in order and in runs, at ragged ends
+    ([3000, 1000, 257, 130, 100, 40, 20], 1, 2000, 300), ([3000, 1000, 257, 130, 100, 40, 20], 32, 6001, 140),
+    ([700, 1, 650], 8, 3001, 200), ([20] * 20, 1, 2000, 2100), ([500, 100, 60], 64, 2050, 2100), ([600], 1, 70, 2100),
+]
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("counts,align,n,k", SHAPES)
+def test_product_in_every_shape_of_tile_is_exact(counts, align, n, k, out_dtype):
+    """Sums of whole numbers below 2^24, against a product in 64 bits."""
+    g = torch.Generator("cuda").manual_seed(len(counts) + n)
+    E, off = len(counts), segments(counts, align)
+    a = torch.randint(-3, 4, (off[-1], k), generator=g, device="cuda").float()
+    w = torch.randint(-3, 4, (E, n, k), generator=g, device="cuda").float()
+    fa, fw = zc.empty_fp8_rows(off[-1], k), zc.empty_fp8_weights(E, n, k)
+    zc.quantize_rows(a, fa)
+    zc.quantize_weights(w, fw)
+    for pad in (0, 3):
+        out, whole = strided(off[-1], n, DT[out_dtype], pad)
+        zc.expert_product(fa, fw, out, torch.tensor(off, dtype=torch.int32, device="cuda"),
+                          torch.tensor(counts, dtype=torch.int32, device="cuda"))
+        for e, c in enumerate(counts):
+            want = a[off[e]:off[e] + c].double() @ w[e].double().T
+            assert torch.equal(out[off[e]:off[e] + c], want.to(DT[out_dtype])), e
+            assert (out[off[e] + c:off[e + 1]] == 0).all(), e
+        assert guard_intact(whole, n)
+
+
 @pytest.mark.parametrize("counts,align,n,k", PRODUCTS)
 def test_product_of_any_numbers(counts, align, n, k):
     g, E, off = gen(2), len(counts), segments(counts, align)
@@ -437,6 +465,27 @@ def test_weight_gradient_of_whole_numbers_is_exact(counts, align, n, k, out_dtyp
     for e, c in enumerate(counts):
         a, b = off[e], off[e] + c
         assert torch.equal(dw[e].cpu(), (dy[a:b].T @ x[a:b]).to(DT[out_dtype])), e
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("counts,n,k", [([300, 200], 3040, 3039), ([130] * 3, 1300, 1301), ([700, 0], 1200, 1401),
+                                        ([40] * 20, 60, 2000), ([300, 5000, 0, 60], 130, 71)])
+def test_weight_gradient_in_every_shape_of_tile_is_exact(counts, n, k, out_dtype):
+    g = torch.Generator("cuda").manual_seed(n + k)
+    E, off = len(counts), segments(counts, 128)
+    rows = off[-1]
+    x = torch.randint(-3, 4, (rows, k), generator=g, device="cuda").float()
+    dy = torch.randint(-3, 4, (rows, n), generator=g, device="cuda").float()
+    for e, c in enumerate(counts):
+        x[off[e] + c:off[e + 1]] = 0
+    fx, fy = zc.empty_fp8_columns(rows, k), zc.empty_fp8_columns(rows, n)
+    zc.quantize_columns(x, fx)
+    zc.quantize_columns(dy, fy)
+    dw = torch.full((E, n, k), float("nan"), dtype=DT[out_dtype], device="cuda")
+    zc.expert_weight_grad(fy, fx, dw, torch.tensor(off, dtype=torch.int32, device="cuda"))
+    for e in range(E):
+        y64, x64 = dy[off[e]:off[e + 1]].double().t().contiguous(), x[off[e]:off[e + 1]].double()
+        assert torch.equal(dw[e], (y64 @ x64).to(DT[out_dtype])), e
 
 
 @pytest.mark.parametrize("counts,n,k", [([9000], 60, 130), ([17000, 0], 200, 70), ([40, 33000], 1, 129)])
