@@ -273,7 +273,8 @@ def special(x):
 
 
 CASTS = [(1, 1, "bf16", 0), (3, 128, "fp16", 0), (130, 200, "bf16", 0), (5, 1024, "fp32", 0), (9, 2047, "fp16", 1),
-         (257, 1100, "bf16", 4), (64, 7168, "bf16", 0), (300, 130, "fp32", 2)]
+         (257, 1100, "bf16", 4), (64, 7168, "bf16", 0), (300, 130, "fp32", 2), (77, 400, "bf16", 3), (50, 512, "fp32", 0),
+         (1001, 98, "fp16", 0)]
 
 
 def as_bytes(f):
