@@ -251,15 +251,15 @@ __device__ __forceinline__ uint32_t turn_a(uint32_t row) { return (row >> 1) & 7
 __device__ __forceinline__ uint32_t turn_w(uint32_t row) { return ((row >> 1) & 1) + ((row >> 3) & 3) * 2; }
 
 // acc += the product of 16 weight rows and 16 token rows over one block, with
-// both scales (low bytes).  Written as the instruction itself, so that the
-// accumulator stays where it is: left to choose, the compiler moves the 256
-// accumulators of a wave around between blocks (50 moves a block).  s_nop
-// stands for the wait a scale just computed needs; results are read only
-// after the loop, which waits for them.
+// both scales (low bytes).  The compiler knows the instruction and keeps the
+// waits between it and whatever else touches its registers.  The empty asm
+// holds it where it stands between loads, reads and barriers (the compiler
+// takes it for arithmetic that may move: a wave's weight side then was copied,
+// 64 moves a block) and its accumulators in the unit's own registers.
+__device__ __forceinline__ void pin(f32x4& acc) { asm volatile("" : "+a"(acc)); }
 __device__ __forceinline__ void multiply(f32x4& acc, const i32x8& w, const i32x8& a, uint32_t sw, uint32_t sa) {
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
-                 : "+a"(acc)
-                 : "v"(w), "v"(a), "v"(sw), "v"(sa));
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, acc, 0, 0, 0, (int)sw, 0, (int)sa);
+    pin(acc);
 }
 
 template <typename SH>
@@ -406,12 +406,16 @@ __device__ __forceinline__ void tile_product(const Tile& t, uint8_t* lds, f32x4 
             load_share(kRest - 2 * (SH::TN - 1 - i));
         }
     };
+    // without this the first sums are known to be 0 + x, and the steady loop of
+    // the smaller tiles moves its accumulators around (64 moves a block)
+#pragma unroll
+    for (int j = 0; j < SH::TM; ++j)
+#pragma unroll
+        for (int i = 0; i < SH::TN; ++i) pin(acc[j][i]);
     uint32_t b = 0;
     for (; b + (PAST_END ? 0 : SH::S) < t.blocks; ++b) one_block(std::true_type{}, b);
     if (!PAST_END)
         for (; b < t.blocks; ++b) one_block(std::false_type{}, b);
-    // the last results are written before anything reads them
-    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
     // no load may still write LDS when another workgroup has it
     if (PAST_END) wait_loads_and_barrier<0>();
 }
@@ -419,7 +423,7 @@ __device__ __forceinline__ void tile_product(const Tile& t, uint8_t* lds, f32x4 
 // An accumulator read where it is written down and no earlier: read ahead of
 // the branches below, all of them would not fit the general registers.
 __device__ __forceinline__ f32x4 late(f32x4 v) {
-    asm volatile("" : "+a"(v));
+    pin(v);
     return v;
 }
 
