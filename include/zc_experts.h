@@ -160,8 +160,9 @@ zc_status zc_expert_product(const void *d_a, const void *d_a_scale, uint64_t row
  * sY[i,b] sX[j,b] <Y[b,i], X[b,j]>: Y and X as zc_quantize_columns makes them
  * from [rows, n] and [rows, k], dW contiguous [experts, n, k] of
  * out_dtype; an expert without rows gets zeros.  Segments begin at multiples
- * of 128 (zc_route with such an align), padding rows are zeros.  d_offsets
- * NULL: one expert, all rows.
+ * of 128 (zc_route with such an align), padding rows are zeros; a segment that
+ * shares a block of 128 rows with another one gets NaN.  d_offsets NULL: one
+ * expert, all rows.
  * Long segments of small weights are summed in parts, joined in their order,
  * where d_ws holds them: zc_expert_weight_grad_workspace_bytes (0: none would
  * be used).  d_ws NULL: every sum in one piece.  Which parts are taken goes by

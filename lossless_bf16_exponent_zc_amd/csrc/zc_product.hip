@@ -525,14 +525,15 @@ __device__ __forceinline__ void store_tile(const Out<T>& o, const f32x4 (&acc)[S
 
 #endif  // __HIP_DEVICE_COMPILE__
 
+// start: what the sums begin with.
 template <typename SH, typename T>
-__device__ __forceinline__ void run_tile(const Tile& t, const Out<T>& o, uint8_t* lds) {
+__device__ __forceinline__ void run_tile(const Tile& t, const Out<T>& o, uint8_t* lds, float start = 0.0f) {
 #if defined(__HIP_DEVICE_COMPILE__)
     f32x4 acc[SH::TM][SH::TN];
 #pragma unroll
     for (int j = 0; j < SH::TM; ++j)
 #pragma unroll
-        for (int i = 0; i < SH::TN; ++i) acc[j][i] = f32x4{0, 0, 0, 0};
+        for (int i = 0; i < SH::TN; ++i) acc[j][i] = f32x4{start, start, start, start};
     if (t.blocks) tile_product<SH>(t, lds, acc);
     const bool odd = sizeof(T) == 2 && (((uintptr_t)o.out >> 1 | o.stride) & 1);
     if (o.cols >= (uint32_t)SH::BN && !odd) store_tile<T, SH, false>(o, acc);
@@ -681,14 +682,18 @@ __device__ __forceinline__ Place place_of(uint32_t index, uint32_t cols) {
     return Place{group * 4 + (in & 3), in >> 2};
 }
 
-// Blocks of an expert's segment.
-__device__ __forceinline__ void segment_blocks(const WeightGradArgs& p, uint32_t e, uint32_t& b0, uint32_t& n) {
+// Blocks of an expert's segment.  False, and no blocks, where it shares one
+// with another segment: their rows cannot be told apart.
+__device__ __forceinline__ bool segment_blocks(const WeightGradArgs& p, uint32_t e, uint32_t& b0, uint32_t& n) {
     b0 = 0;
     n = p.rows / 128;
-    if (p.offsets) {
-        b0 = clamp_to(p.offsets[e], 0, p.rows) / 128;
-        n = (clamp_to(p.offsets[e + 1], b0 * 128, p.rows) + 127) / 128 - b0;
-    }
+    if (!p.offsets) return true;
+    const uint32_t lo = clamp_to(p.offsets[e], 0, p.rows), hi = clamp_to(p.offsets[e + 1], lo, p.rows);
+    const uint32_t last = clamp_to(p.offsets[p.experts], hi, p.rows);
+    const bool alone = lo == hi || (lo % 128 == 0 && (hi % 128 == 0 || hi == last));
+    b0 = lo / 128;
+    n = lo < hi && alone ? (hi + 127) / 128 - b0 : 0;
+    return alone;
 }
 
 // In how many parts a segment of n blocks is summed, of at most `parts`.
@@ -717,7 +722,7 @@ __global__ __launch_bounds__(256, 1) void weight_grad(WeightGradArgs p, T* out, 
     }
     const uint32_t j0 = where.col * SH::BN;
     uint32_t b0, n;
-    segment_blocks(p, e, b0, n);
+    const float start = segment_blocks(p, e, b0, n) ? 0.0f : __builtin_nanf("");
     if (parts > 1) {
         const uint32_t mine = parts_of(n, parts);
         if (part >= mine) return;
@@ -734,7 +739,7 @@ __global__ __launch_bounds__(256, 1) void weight_grad(WeightGradArgs p, T* out, 
                  p.n - i0, p.k - j0, 128, 128, (uint64_t)p.n * 128, (uint64_t)p.k * 128,
                  p.y_scale_stride, p.x_scale_stride, n};
     const Out<T> o{out + ((uint64_t)e * p.n + i0) * p.k + j0, p.k, p.n - i0, p.k - j0};
-    run_tile<SH>(t, o, lds);
+    run_tile<SH>(t, o, lds, start);
 }
 
 // The sum of an expert's parts, in their order.  grid: (pieces, experts).

@@ -249,7 +249,7 @@ def expert_weight_grad_workspace_bytes(rows: int, experts: int, n: int, k: int) 
 
 def expert_weight_grad(y: Fp8Columns, x: Fp8Columns, dw, offsets=None, ws=None, stream=None):
     """Enqueue dw[e] = Y_e^T X_e over the rows of every expert's segment
-    (segments begin at multiples of 128); y: columns of [rows, n], x: columns
+    (segments begin at multiples of 128, and get NaN where they do not); y: columns of [rows, n], x: columns
     of [rows, k], dw [experts, n, k].  ws: the workspace for long segments;
     without one it is taken from torch's allocator, on the call's stream."""
     if ws is None and stream is not None:

@@ -525,6 +525,28 @@ def test_weight_gradient_of_long_segments_in_parts(counts, n, k):
     assert e.value.code == 2
 
 
+@pytest.mark.parametrize("rows,parts", [(1024, False), (65536, True)])
+def test_weight_gradient_of_segments_that_share_a_block_is_nan(rows, parts):
+    """Rows of segments that begin inside a block of 128 cannot be told apart;
+    the segments around them, the last one's end, and empty ones wherever they
+    begin are as ever."""
+    n, k = 60, 130
+    off = [0, 128, 200, 200, 384, 512, rows - 60, rows - 60]
+    want = [128, None, 0, None, 128, rows - 60 - 512, 0]
+    assert (zc.expert_weight_grad_workspace_bytes(rows, len(want), n, k) > 0) == parts
+    x, y = torch.ones(rows, k, device="cuda"), torch.ones(rows, n, device="cuda")
+    x[rows - 60:] = 0
+    fx, fy = zc.empty_fp8_columns(rows, k), zc.empty_fp8_columns(rows, n)
+    zc.quantize_columns(x, fx)
+    zc.quantize_columns(y, fy)
+    for dt in DT.values():
+        dw = torch.zeros(len(want), n, k, dtype=dt, device="cuda")
+        zc.expert_weight_grad(fy, fx, dw, torch.tensor(off, dtype=torch.int32, device="cuda"))
+        for e, v in enumerate(want):
+            got = dw[e].cpu()
+            assert bool((torch.isnan(got) if v is None else got == torch.tensor(float(v)).to(dt)).all()), e
+
+
 def test_weight_gradient_of_any_numbers():
     counts, n, k = [200, 0, 513], 300, 260
     off = segments(counts, 128)
