@@ -138,10 +138,18 @@ public:
         return t.data_ptr();
     }
 
+    // The given stream, or the current one; a stream that names a GPU (torch's
+    // do) has to be the tensors' GPU's.
     hipStream_t stream(PyObject* o) {
-        if (o == Py_None) {
-            if (device >= 0 && device != c10::hip::current_device()) refuse("stream", "the tensors are not on the current GPU");
-            return c10::hip::getCurrentHIPStream().stream();
+        if (device >= 0 && device != c10::hip::current_device()) refuse("stream", "the tensors are not on the current GPU");
+        if (o == Py_None) return c10::hip::getCurrentHIPStream().stream();
+        if (PyObject* d = PyObject_GetAttrString(o, "device_index")) {
+            const long index = PyLong_AsLong(d);
+            Py_DECREF(d);
+            if (index == -1 && PyErr_Occurred()) throw PythonError{};
+            if (device >= 0 && index != device) refuse("stream", "not of the tensors' GPU");
+        } else {
+            PyErr_Clear();
         }
         PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
         if (!h) throw PythonError{};

@@ -9,6 +9,8 @@ Products of 8-bit blocks: exact where all partial sums are small whole
 numbers; else the bound that follows from how the matrix unit adds
 (experts_plain.unit_bound).
 """
+import types
+
 import numpy as np
 import pytest
 import torch
@@ -719,6 +721,20 @@ def test_refusals():
         with pytest.raises(zc.ZcError) as e:
             call()
         assert e.value.code == code
+
+
+def test_a_stream_of_another_gpu_is_refused():
+    plan = zc.ExpertPlan(8, 2, 4)
+    r, ws, ids = plan.empty_routing(), plan.empty_workspace(), torch.zeros(8, 2, dtype=torch.int32, device="cuda")
+    own = torch.cuda.Stream()
+    other = types.SimpleNamespace(cuda_stream=own.cuda_stream, device_index=own.device_index + 1)
+    with pytest.raises(zc.ZcError) as e:
+        plan.route(ids, r, ws, stream=other)
+    assert e.value.code == 1
+    torch.cuda.synchronize()
+    plan.route(ids, r, ws, stream=own)
+    own.synchronize()
+    assert r.counts.tolist() == [16, 0, 0, 0]
 
 
 def test_offsets_and_counts_out_of_range_are_clamped():
