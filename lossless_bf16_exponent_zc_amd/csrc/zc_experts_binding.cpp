@@ -62,9 +62,16 @@ int dtype_of(at::ScalarType t) {
 
 uint64_t up(uint64_t n, uint64_t m) { return (n + m - 1) / m * m; }
 
+// A size that the library takes in 32 bits.
+uint32_t size32(uint64_t v, const char* what) {
+    if (v >> 32) refuse(what, "size " + std::to_string(v), ZC_ERR_UNSUPPORTED);
+    return (uint32_t)v;
+}
+
 struct Matrix {
     void* p;
-    uint64_t stride, rows, width;
+    uint64_t stride, rows;
+    uint32_t width;
     int dtype;
 };
 
@@ -97,7 +104,7 @@ public:
         }
         if (t.stride(1) != 1 && w > 1) refuse(what, "strides " + shape_text(t.strides()) + ": columns must be contiguous");
         if ((uint64_t)n < rows) refuse(what, std::to_string(n) + " rows, " + std::to_string(rows) + " needed", ZC_ERR_CAPACITY);
-        return Matrix{t.data_ptr(), (uint64_t)s, (uint64_t)n, (uint64_t)w, have};
+        return Matrix{t.data_ptr(), (uint64_t)s, (uint64_t)n, size32(w, what), have};
     }
 
     // A contiguous tensor of `type` with at least `count` elements.
@@ -184,9 +191,9 @@ struct Sizes {
     explicit Sizes(PyObject* o) {
         PyObject* const* v = items(o, "plan", 6);
         tokens = number(v[0], "tokens");
-        topk = (uint32_t)number(v[1], "topk");
-        experts = (uint32_t)number(v[2], "experts");
-        align = (uint32_t)number(v[3], "align");
+        topk = size32(number(v[1], "topk"), "topk");
+        experts = size32(number(v[2], "experts"), "experts");
+        align = size32(number(v[3], "align"), "align");
         rows = number(v[4], "rows");
         ws_bytes = number(v[5], "workspace");
     }
@@ -277,7 +284,7 @@ void dispatch(Args a) {  // sizes, x, routing, rows, stream
     const Sizes z(a[0]);
     const Matrix x = c.matrix(a[1], "x", z.tokens), rows = c.matrix(a[3], "rows", z.rows, x.dtype, x.width);
     const Routing r(c, z, a[2]);
-    enqueue("zc_dispatch", zc.dispatch, x.p, x.stride, (uint32_t)x.dtype, z.tokens, z.topk, z.experts, (uint32_t)x.width,
+    enqueue("zc_dispatch", zc.dispatch, x.p, x.stride, (uint32_t)x.dtype, z.tokens, z.topk, z.experts, x.width,
             r.offsets, r.counts, r.row, rows.p, rows.stride, rows.rows, c.stream(a[4]));
 }
 
@@ -288,7 +295,7 @@ void dispatch_fp8(Args a) {  // sizes, x, routing, out, stream
     const Blocks out(c, a[3], "out", x.width, {z.rows}, {z.rows});
     const Routing r(c, z, a[2]);
     enqueue("zc_dispatch_fp8", zc.dispatch_fp8, x.p, x.stride, (uint32_t)x.dtype, z.tokens, z.topk, z.experts,
-            (uint32_t)x.width, r.offsets, r.counts, r.row, out.data, out.scale, std::min(out.data_rows, out.scale_rows),
+            x.width, r.offsets, r.counts, r.row, out.data, out.scale, std::min(out.data_rows, out.scale_rows),
             c.stream(a[4]));
 }
 
@@ -298,7 +305,7 @@ void combine(Args a) {  // sizes, rows, weights, routing, y, stream
     const Matrix y = c.matrix(a[4], "y", z.tokens), rows = c.matrix(a[1], "rows", z.rows, y.dtype, y.width);
     const int32_t* row = c.flat<int32_t>(items(a[3], "routing", 4)[2], "row", at::kInt, z.slots());
     const float* w = c.flat_or_null<float>(a[2], "weights", at::kFloat, z.slots());
-    enqueue("zc_combine", zc.combine, rows.p, rows.stride, w, (uint32_t)y.dtype, z.tokens, z.topk, (uint32_t)y.width, row,
+    enqueue("zc_combine", zc.combine, rows.p, rows.stride, w, (uint32_t)y.dtype, z.tokens, z.topk, y.width, row,
             rows.rows, y.p, y.stride, c.stream(a[5]));
 }
 
@@ -317,7 +324,7 @@ void combine_backward(Args a) {  // sizes, dy, rows, weights, routing, drows, dw
     const float* w = c.flat_or_null<float>(a[3], "weights", at::kFloat, z.slots());
     float* dw = c.flat_or_null<float>(a[6], "dweights", at::kFloat, z.slots());
     enqueue("zc_combine_backward", zc.combine_backward, dy.p, dy.stride, rows.p, rows.stride, w, (uint32_t)dy.dtype, z.tokens,
-            z.topk, z.experts, (uint32_t)dy.width, r.offsets, r.counts, r.row, std::min(drows.rows, rows.rows), drows.p,
+            z.topk, z.experts, dy.width, r.offsets, r.counts, r.row, std::min(drows.rows, rows.rows), drows.p,
             drows.stride, dw, c.stream(a[7]));
 }
 
@@ -326,7 +333,7 @@ void quantize_rows(Args a) {  // x, out, used, stream
     const Matrix x = c.matrix(a[0], "x", 0);
     const Blocks out(c, a[1], "out", x.width, {x.rows}, {x.rows});
     const int32_t* used = c.flat_or_null<int32_t>(a[2], "used", at::kInt, 1);
-    enqueue("zc_quantize_rows", zc.quantize_rows, x.p, x.stride, (uint32_t)x.dtype, x.rows, (uint32_t)x.width, used, out.data,
+    enqueue("zc_quantize_rows", zc.quantize_rows, x.p, x.stride, (uint32_t)x.dtype, x.rows, x.width, used, out.data,
             out.scale, c.stream(a[3]));
 }
 
@@ -335,10 +342,10 @@ void quantize_weights(Args a) {  // w, out, transpose, stream
     const at::Tensor& w = stack(c, a[0], "w");
     const int transpose = PyObject_IsTrue(a[2]);
     if (transpose < 0) throw PythonError{};
-    const uint64_t e = w.size(0), n = w.size(transpose ? 2 : 1), k = w.size(transpose ? 1 : 2);
-    const Blocks out(c, a[1], "out", k, {e, n}, {e, (n + 127) / 128});
-    enqueue("zc_quantize_weights", zc.quantize_weights, w.data_ptr(), (uint32_t)dtype_of(w.scalar_type()), (uint32_t)e,
-            (uint32_t)n, (uint32_t)k, transpose, out.data, out.scale, c.stream(a[3]));
+    const uint32_t e = size32(w.size(0), "w"), n = size32(w.size(transpose ? 2 : 1), "w");
+    const uint32_t k = size32(w.size(transpose ? 1 : 2), "w");
+    const Blocks out(c, a[1], "out", k, {e, n}, {e, (n + 127ull) / 128});
+    enqueue("zc_quantize_weights", zc.quantize_weights, w.data_ptr(), (uint32_t)dtype_of(w.scalar_type()), e, n, k, transpose, out.data, out.scale, c.stream(a[3]));
 }
 
 void quantize_columns(Args a) {  // x, out, used, stream
@@ -346,7 +353,7 @@ void quantize_columns(Args a) {  // x, out, used, stream
     const Matrix x = c.matrix(a[0], "x", 0);
     const Columns out(c, a[1], "out", x.rows, x.width);
     const int32_t* used = c.flat_or_null<int32_t>(a[2], "used", at::kInt, 1);
-    enqueue("zc_quantize_columns", zc.quantize_columns, x.p, x.stride, (uint32_t)x.dtype, x.rows, (uint32_t)x.width, used,
+    enqueue("zc_quantize_columns", zc.quantize_columns, x.p, x.stride, (uint32_t)x.dtype, x.rows, x.width, used,
             out.data, out.scale, c.stream(a[3]));
 }
 
@@ -355,19 +362,20 @@ void expert_product(Args a) {  // a, w, out, offsets, counts, stream
     PyObject* const* wt = items(a[1], "w", 3);
     const at::Tensor& w = c.tensor(wt[0], "w");
     if (w.dim() != 3) refuse("expert_product", "a is [rows, k], w is [experts, n, k]");
-    const uint64_t experts = w.size(0), n = w.size(1), k = number(wt[2], "w");
+    const uint32_t experts = size32(w.size(0), "w"), n = size32(w.size(1), "w"), k = size32(number(wt[2], "w"), "w");
     const Matrix out = c.matrix(a[2], "out", 0, -1, n);
-    const Blocks ab(c, a[0], "a", k, {out.rows}, {out.rows}), wb(c, a[1], "w", k, {experts, n}, {experts, (n + 127) / 128});
-    const int32_t* offsets = c.flat_or_null<int32_t>(a[3], "offsets", at::kInt, experts + 1);
+    const Blocks ab(c, a[0], "a", k, {out.rows}, {out.rows}), wb(c, a[1], "w", k, {experts, n},
+        {experts, (n + 127ull) / 128});
+    const int32_t* offsets = c.flat_or_null<int32_t>(a[3], "offsets", at::kInt, experts + 1ull);
     const int32_t* counts = c.flat_or_null<int32_t>(a[4], "counts", at::kInt, experts);
-    enqueue("zc_expert_product", zc.expert_product, ab.data, ab.scale, out.rows, wb.data, wb.scale, (uint32_t)experts,
-            (uint32_t)n, (uint32_t)k, offsets, counts, out.p, out.stride, (uint32_t)out.dtype, c.stream(a[5]));
+    enqueue("zc_expert_product", zc.expert_product, ab.data, ab.scale, out.rows, wb.data, wb.scale, experts,
+            n, k, offsets, counts, out.p, out.stride, (uint32_t)out.dtype, c.stream(a[5]));
 }
 
 void expert_weight_grad(Args a) {  // y, x, dw, offsets, ws, stream
     Call c;
     const at::Tensor& dw = stack(c, a[2], "dw");
-    const uint32_t experts = (uint32_t)dw.size(0), n = (uint32_t)dw.size(1), k = (uint32_t)dw.size(2);
+    const uint32_t experts = size32(dw.size(0), "dw"), n = size32(dw.size(1), "dw"), k = size32(dw.size(2), "dw");
     const uint64_t rows = number(items(a[1], "x", 4)[2], "x");
     const Columns y(c, a[0], "y", rows, n), x(c, a[1], "x", rows, k);
     const int32_t* offsets = c.flat_or_null<int32_t>(a[3], "offsets", at::kInt, (uint64_t)experts + 1);

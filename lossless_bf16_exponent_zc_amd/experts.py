@@ -169,6 +169,8 @@ class ExpertPlan:
         self.tokens, self.topk, self.experts, self.align = int(tokens), int(topk), int(experts), int(align)
         if min(self.tokens, self.topk, self.experts, self.align) < 0:
             _bad("ExpertPlan", "negative size")
+        if self.tokens >> 64 or max(self.topk, self.experts, self.align) >> 32:  # ctypes would cut them short
+            _bad("ExpertPlan", "size past the library's types", ZC_ERR_UNSUPPORTED)
         self.rows = lib().zc_route_rows(self.tokens, self.topk, self.experts, self.align)
         self.workspace_bytes = lib().zc_route_workspace_bytes(self.tokens, self.topk, self.experts)
         if self.workspace_bytes == 0 or (self.rows == 0 and self.tokens):
@@ -244,6 +246,8 @@ def expert_product(a: Fp8Blocks, w: Fp8Blocks, out, offsets=None, counts=None, s
 
 def expert_weight_grad_workspace_bytes(rows: int, experts: int, n: int, k: int) -> int:
     """Bytes expert_weight_grad uses to sum long segments in parts (or 0)."""
+    if any(v < 0 or v >> 32 for v in (rows, experts, n, k)):  # past every limit; ctypes would cut them short
+        return 0
     return lib().zc_expert_weight_grad_workspace_bytes(rows, experts, n, k)
 
 

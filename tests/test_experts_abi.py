@@ -48,6 +48,20 @@ def test_plan_limits(L, args):
     assert e.value.code == UNSUP
 
 
+@pytest.mark.parametrize("args", [(8, 2**32 + 2, 4, 1), (8, 2, 2**32 + 4, 1), (8, 2, 4, 2**32 + 1), (2**64 + 8, 2, 4, 1)])
+def test_sizes_past_the_librarys_types_are_refused(args):
+    with pytest.raises(zc.ZcError) as e:
+        zc.ExpertPlan(*args)
+    assert e.value.code == UNSUP
+
+
+def test_weight_gradient_workspace_of_sizes_past_the_librarys_types():
+    assert zc.expert_weight_grad_workspace_bytes(32768, 1, 60, 300) > 0
+    for args in ((32768, 2**32 + 1, 60, 300), (32768, 1, 2**32 + 60, 300), (32768, 1, 60, 2**32 + 300),
+                 (2**64 + 32768, 1, 60, 300), (-1, 1, 60, 300)):
+        assert zc.expert_weight_grad_workspace_bytes(*args) == 0
+
+
 def test_route_refusals(L):
     ok = [P, 8, 2, 4, 1, P, P, P, P, 16, P, 256, None]
 

@@ -737,6 +737,18 @@ def test_a_stream_of_another_gpu_is_refused():
     assert r.counts.tolist() == [16, 0, 0, 0]
 
 
+def test_widths_past_32_bits_are_refused():
+    """8.6 GB that no call may take for rows of 64 values."""
+    plan = zc.ExpertPlan(1, 1, 1)
+    r, wide = plan.empty_routing(), torch.empty(1, 2**32 + 64, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: plan.dispatch(wide, r, wide), lambda: plan.combine(wide, None, r, wide),
+                 lambda: plan.combine_backward(wide, wide, None, r, wide, None),
+                 lambda: zc.quantize_weights(wide[None], zc.empty_fp8_weights(1, 1, 64))):
+        with pytest.raises(zc.ZcError) as e:
+            call()
+        assert e.value.code == 3
+
+
 def test_offsets_and_counts_out_of_range_are_clamped():
     """Segments that leave the buffers are cut to them; nothing is read or
     written outside."""
