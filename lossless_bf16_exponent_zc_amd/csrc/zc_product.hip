@@ -788,10 +788,15 @@ constexpr int kLdsPair = Shape<2, 4, 4, 2, false>::kLds;
 static_assert(Shape<1, 4, 2, 2, false>::kLds <= kLdsPair && 2 * kLdsPair <= 160 * 1024, "two workgroups on a CU");
 constexpr int kLdsSmall = Shape<2, 2, 2, 8, false>::kLds;
 
-// More LDS than the default limit has to be asked for, once per device.
+// More LDS than the default limit has to be asked for.  Every launch does (a
+// call of 3.6 us of host time, 3.3 without), so nothing has to be kept of
+// which GPU has been asked.
 template <typename K>
-void allow_lds(K kernel, int bytes) {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+zc_status allow_lds(K kernel, int bytes) {
+    const auto f = reinterpret_cast<const void*>(kernel);
+    if (hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess) return ZC_OK;
+    (void)hipGetLastError();  // reported here, not by the next launch
+    return ZC_ERR_HIP;
 }
 
 }  // namespace
@@ -823,7 +828,7 @@ zc_status product_as(const ProductArgs& a, hipStream_t stream) {
         typedef decltype(cut) Cut;
         const uint64_t grid = (a.rows / Cut::kRows + segments) * cols(Cut::kCols);
         if (!fits(grid)) return ZC_ERR_UNSUPPORTED;
-        allow_lds(kernel, lds);
+        if (zc_status e = allow_lds(kernel, lds)) return e;
         hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(256), lds, stream, a, cols(Cut::kCols), kInOrder);
         return ZC_OK;
     };
@@ -841,7 +846,7 @@ zc_status product_as(const ProductArgs& a, hipStream_t stream) {
         // runs to the 8 XCDs
         const uint64_t grid = (((s + 6) / 4 * c + 14) / 8 + 14) / 8 * 256;
         if (!fits(grid)) return ZC_ERR_UNSUPPORTED;
-        allow_lds(product<T, WideCut>, kLdsProduct);
+        if (zc_status e = allow_lds(product<T, WideCut>, kLdsProduct)) return e;
         hipLaunchKernelGGL((product<T, WideCut>), dim3((uint32_t)grid), dim3(256), kLdsProduct, stream, a, (uint32_t)c, kRuns);
         return ZC_OK;
     }
@@ -869,7 +874,7 @@ zc_status weight_grad_in(const WeightGradArgs& a, T* out, uint32_t parts, hipStr
     const Order order = tiles > 512 ? kRuns : kInOrder;
     const uint64_t each = order == kRuns ? ((uint64_t)a.experts * ((rows + 3) / 4 * 4) * cols + 255) / 256 * 256 : tiles;
     if (!fits(each * parts)) return ZC_ERR_UNSUPPORTED;
-    allow_lds(weight_grad<T, SH>, SH::kLds);
+    if (zc_status e = allow_lds(weight_grad<T, SH>, SH::kLds)) return e;
     hipLaunchKernelGGL((weight_grad<T, SH>), dim3((uint32_t)(each * parts)), dim3(256), SH::kLds, stream, a, out, rows, cols,
                        order, (uint32_t)each, parts);
     return ZC_OK;
