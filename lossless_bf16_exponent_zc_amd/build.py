@@ -7,6 +7,8 @@ Flags:
                                  separately rounded adds/multiplies
   -fno-gpu-flush-denormals-to-zero   subnormal BF16 values are data
   -Xclang -target-feature -Xclang -packed-fp32-ops   no packed fp32 ops
+  -Wall -Werror                  also what the optimizer says it could not do
+                                 (a loop that a pragma asks it to unroll)
 """
 import os
 import subprocess
@@ -27,7 +29,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["-std=c++17", "-O3", "-fPIC", "--offload-arch=gfx950",
          "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-         "-Wall", "-Wno-unused-result", "-I" + INCLUDE]
+         "-Wall", "-Werror", "-Wno-unused-result", "-I" + INCLUDE]
 
 
 def _compile(src: str, extra) -> str:
@@ -43,7 +45,7 @@ def _build_binding() -> None:
     import torch
 
     at = os.path.dirname(torch.__file__)
-    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-Werror", "-D__HIP_PLATFORM_AMD__",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
            "-I" + os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"), "-isystem", os.path.join(at, "include"),
            "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "zc_experts_binding.cpp"), "-o", BINDING + ".tmp",

@@ -118,7 +118,6 @@ zc_status zc_dispatch_fp8(const void* d_x, uint64_t x_stride, uint32_t dtype, ui
     if (bad_matrix(d_x, x_stride, hidden, dtype) || !d_data || !aligned(d_data, 16) || !d_scale ||
         !aligned(d_scale, 16) || bad_words(d_row) || bad_segments(d_offsets, d_counts))
         return ZC_ERR_INVALID_ARG;
-    const uint32_t eb = elem_bytes(dtype);
     const CastRowsArgs a{d_x, x_stride, static_cast<uint8_t*>(d_data), static_cast<uint8_t*>(d_scale), d_row,
                          d_offsets, d_counts, nullptr, (uint32_t)tokens, topk, experts, hidden, stored(hidden),
                          scales(hidden), (uint32_t)row_capacity};
@@ -193,7 +192,6 @@ zc_status zc_quantize_rows(const void* d_x, uint64_t x_stride, uint32_t dtype, u
     if (bad_matrix(d_x, x_stride, cols, dtype) || !d_data || !aligned(d_data, 16) || !d_scale ||
         !aligned(d_scale, 16) || !aligned(d_used, 4))
         return ZC_ERR_INVALID_ARG;
-    const uint32_t eb = elem_bytes(dtype);
     const CastRowsArgs a{d_x, x_stride, static_cast<uint8_t*>(d_data), static_cast<uint8_t*>(d_scale), nullptr,
                          nullptr, nullptr, d_used, (uint32_t)rows, 1, 0, cols, stored(cols), scales(cols),
                          (uint32_t)rows};
@@ -220,7 +218,6 @@ zc_status zc_quantize_columns(const void* d_x, uint64_t x_stride, uint32_t dtype
     if (bad_matrix(d_x, x_stride, cols, dtype) || !d_data || !aligned(d_data, 16) || !d_scale ||
         !aligned(d_scale, 16) || !aligned(d_used, 4))
         return ZC_ERR_INVALID_ARG;
-    const uint32_t eb = elem_bytes(dtype);
     const CastTileArgs a{d_x, x_stride, static_cast<uint8_t*>(d_data), static_cast<uint8_t*>(d_scale), d_used,
                          (uint32_t)rows, cols, 1, 128, up_to(cols, 4), 0};
     return finished(launch_cast_columns(a, dtype, stream));

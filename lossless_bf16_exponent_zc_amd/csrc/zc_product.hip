@@ -25,7 +25,7 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ i32x8 two(xu32x4 lo, xu32x4 hi) {
+[[maybe_unused]] __device__ __forceinline__ i32x8 two(xu32x4 lo, xu32x4 hi) {
     return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
@@ -586,8 +586,8 @@ __global__ __launch_bounds__(256, 1) void product(ProductArgs p, uint32_t col_ti
 // four waves taking every fourth block, straight from memory to the unit, and
 // adding up in LDS in their order.  Nothing here is used twice but the rows,
 // so staging would only hold loads back; narrow tiles put the weights of a few
-// experts on all CUs (one CU draws about 50 GB/s from memory, however many
-// loads it has in flight).
+// experts on all CUs (one CU draws about 50 GB/s from memory so, each wave
+// with one block's loads in flight).
 template <typename T, int TM>
 __device__ __forceinline__ void few_tile(const ProductArgs& p, const Found& f, uint32_t n0, const Out<T>& o, float* lds) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -613,8 +613,6 @@ __device__ __forceinline__ void few_tile(const ProductArgs& p, const Found& f, u
 #pragma unroll
     for (int j = 0; j < TM; ++j) acc[j][0] = acc[j][1] = f32x4{0, 0, 0, 0};
     auto piece = [](const uint8_t* q) { return two(*(const xu32x4*)q, *(const xu32x4*)(q + 64)); };
-    constexpr int U = TM == 1 ? 8 : TM == 2 ? 4 : 2;
-#pragma unroll U
     for (uint32_t b = wave; b < blocks; b += 4) {
         const uint32_t at = (b >> 2) * 512, sat = b & ~3u;
         const i32x8 w0 = piece(w[0] + at), w1 = piece(w[1] + at);
