@@ -20,7 +20,8 @@ __global__ void k(const i32x8* a, f32x4* out, unsigned n) {
 UNUSED = "int f(int x) { int y = x; return x; }"
 
 
-@pytest.mark.parametrize("source,said", [(NOT_UNROLLED, "not unrolled"), (UNUSED, "unused variable")])
+@pytest.mark.parametrize("source,said", [(NOT_UNROLLED, "not unrolled"), (UNUSED, "unused variable")],
+                         ids=["unroll", "unused"])
 def test_a_warning_fails_the_build(tmp_path, monkeypatch, source, said):
     (tmp_path / "k.hip").write_text(source)
     monkeypatch.setattr(build, "CSRC", str(tmp_path))

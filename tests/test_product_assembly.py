@@ -23,7 +23,7 @@ WAITS = 12
 @pytest.fixture(scope="module")
 def kernels(tmp_path_factory):
     out = str(tmp_path_factory.mktemp("asm") / "zc_product.s")
-    cmd = [build.HIPCC, *build.FLAGS, "-S", "--cuda-device-only", SOURCE, "-o", out]
+    cmd = [build.HIPCC, *build.FLAGS, "-Wno-unused-command-line-argument", "-S", "--cuda-device-only", SOURCE, "-o", out]
     r = subprocess.run(cmd, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     found, lines = {}, None
