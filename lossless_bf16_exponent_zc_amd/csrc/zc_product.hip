@@ -98,15 +98,10 @@ __device__ __forceinline__ Slots slot_of(uint32_t index, uint32_t cols, uint32_t
     const uint32_t runs_l = ((nlong + 3) / 4 * cols + 7) / 8, runs_s = ((nshort + 3) / 4 * cols + 7) / 8;
     const uint32_t mine_l = (runs_l + 7 - xcd) / 8, mine_s = (runs_s + 7 - xcd) / 8, mine = mine_l + mine_s;
     if (run >= mine) return Slots{0, 0, false, false};
-    uint32_t before, upto;  // long runs before this one, and with it
-    if (mine < 65536) {
-        const uint32_t phase = xcd * mine / 8;
-        before = (run * mine_l + phase) / mine;
-        upto = ((run + 1) * mine_l + phase) / mine;
-    } else {
-        before = run < mine_l ? run : mine_l;
-        upto = run < mine_l ? run + 1 : mine_l;
-    }
+    // long runs before this one, and with it (a launch has below 2^24
+    // workgroups, so an XCD below 2^16 runs and the products below 2^32)
+    const uint32_t phase = xcd * mine / 8;
+    const uint32_t before = (run * mine_l + phase) / mine, upto = ((run + 1) * mine_l + phase) / mine;
     const bool l = upto > before;
     const uint32_t tile = ((l ? before : run - before) * 8 + xcd) * 32 + (n & 31);
     const uint32_t group = tile / (4 * cols), in = tile % (4 * cols), slot = group * 4 + (in & 3);
