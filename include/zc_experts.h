@@ -58,7 +58,9 @@ extern "C" {
 typedef enum zc_dtype { ZC_BF16 = 0, ZC_FP16 = 1, ZC_FP32 = 2 } zc_dtype;
 
 /* Limits: experts 1..1024, topk 1..64, align a power of two 1..1024, rows
- * below 2^31, row widths below 2^24.  zc_route_rows gives the rows that hold
+ * below 2^31 (below 2^24 in blocks of 128 rows of one column:
+ * zc_quantize_columns, zc_expert_weight_grad), row widths below 2^24.
+ * zc_route_rows gives the rows that hold
  * every possible routing, up(slots + min(experts, slots) * (align - 1), align),
  * or 0 where a limit is passed.  A call whose launch would pass 2^32 threads is
  * refused with ZC_ERR_UNSUPPORTED. */
@@ -165,7 +167,7 @@ zc_status zc_expert_product(const void *d_a, const void *d_a_scale, uint64_t row
  * expert, all rows.
  * Long segments of small weights are summed in parts, joined in their order,
  * where d_ws holds them: zc_expert_weight_grad_workspace_bytes (0: none would
- * be used).  d_ws NULL: every sum in one piece.  Which parts are taken goes by
+ * be used, or a limit is passed).  d_ws NULL: every sum in one piece.  Which parts are taken goes by
  * the arguments alone.
  */
 uint64_t zc_expert_weight_grad_workspace_bytes(uint64_t rows, uint32_t experts, uint32_t n, uint32_t k);

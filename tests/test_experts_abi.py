@@ -62,6 +62,16 @@ def test_weight_gradient_workspace_of_sizes_past_the_librarys_types():
         assert zc.expert_weight_grad_workspace_bytes(*args) == 0
 
 
+def test_rows_of_columns_blocks_stay_below_their_limit(L):
+    """2^24, where rows of every other call go to 2^31."""
+    q = [P, 64, 0, 1 << 24, 64, None, P, P, None]
+    assert L.zc_quantize_columns(*q) == UNSUP
+    assert L.zc_expert_weight_grad_workspace_bytes((1 << 24) - 1, 1, 60, 300) > 0
+    assert L.zc_expert_weight_grad_workspace_bytes(1 << 24, 1, 60, 300) == 0
+    header = open(os.path.join(ROOT, "include", "zc_experts.h")).read()
+    assert "below 2^24 in blocks of 128 rows" in header
+
+
 def test_route_refusals(L):
     ok = [P, 8, 2, 4, 1, P, P, P, P, 16, P, 256, None]
 
