@@ -147,7 +147,9 @@ zc_status zc_quantize_columns(const void *d_x, uint64_t x_stride, uint32_t dtype
  * zero to a multiple of 2^-13 of the group's largest power of two, and all
  * groups and blocks in 32 bits: about 2e-5 of the sum's root mean square off
  * on Gaussian data, whatever k, and at most 7 * 2^-13 of each group's
- * largest product.
+ * largest product.  Results in 16 bits hardly show it beside their own
+ * rounding (1.7e-3 in bf16, 2e-4 in fp16); results in 32 bits are that far from
+ * a product in 32-bit arithmetic.  zc_expert_weight_grad adds in the same way.
  * d_offsets NULL: one expert, all rows (experts must be 1, d_counts NULL).
  * d_counts NULL: segments are whole, offset_e to offset_(e+1).  Padding rows
  * are written as zeros.  Offsets and counts that leave [0, rows] are clamped.
