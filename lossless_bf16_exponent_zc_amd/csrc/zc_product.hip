@@ -694,9 +694,13 @@ __device__ __forceinline__ bool segment_blocks(const WeightGradArgs& p, uint32_t
     b0 = 0;
     n = p.rows / 128;
     if (!p.offsets) return true;
-    const uint32_t lo = clamp_to(p.offsets[e], 0, p.rows), hi = clamp_to(p.offsets[e + 1], lo, p.rows);
-    const uint32_t last = clamp_to(p.offsets[p.experts], hi, p.rows);
-    const bool alone = lo == hi || (lo % 128 == 0 && (hi % 128 == 0 || hi == last));
+    const int32_t begin = p.offsets[e], end = p.offsets[e + 1];
+    const uint32_t lo = clamp_to(begin, 0, p.rows), hi = clamp_to(end, lo, p.rows);
+    bool alone = (lo == hi) | ((lo | hi) % 128 == 0);
+    // the last segment may end anywhere; its end is read only then (241 experts
+    // 44 x 1986 of 128 rows, the shortest tiles: 85.4 us without a check, 87.5
+    // so, 88.5 where every tile reads it; 37 experts 1000 x 1401 36.5 each way)
+    if (!alone && lo % 128 == 0) alone = clamp_to(p.offsets[p.experts], hi, p.rows) == hi;
     b0 = lo / 128;
     n = lo < hi && alone ? (hi + 127) / 128 - b0 : 0;
     return alone;
