@@ -22,10 +22,11 @@
 // bits.
 //
 // Long sums are bound by the matrix unit and the chip's clock under it (16,384
-// rows, n 4096, k 7168: 370 us, 2.6 PFLOP/s, 65% of the unit's cycles; for
-// that the tiles are 256 x 256, a byte of operands for every 128 products); few rows an expert by the weights (64 rows on 32 experts, n 4096, k
-// 7168: 117 us, 5.8 TB/s); short sums by the results' stores (64 experts' weight
-// gradients 2048 x 4096 over 128 rows each: 285 us, 3.8 TB/s).
+// rows, n 4096, k 7168: 360 us, 2.7 PFLOP/s, 67% of the unit's cycles; for that
+// the tiles are 256 x 256, a byte of operands for every 128 products); few rows
+// an expert by the weights (64 rows on 32 experts, n 4096, k 7168: 117 us, 5.8
+// TB/s); short sums by the results' stores (64 experts' weight gradients 2048 x
+// 4096 over 128 rows each: 271 us, 4.0 TB/s).
 #include "zc_experts_kernels.h"
 
 #include <algorithm>
@@ -799,7 +800,7 @@ static_assert(Shape<1, 4, 2, 2, false>::kLds <= kLdsPair && 2 * kLdsPair <= 160 
 constexpr int kLdsSmall = Shape<2, 2, 2, 8, false>::kLds;
 
 // More LDS than the default limit has to be asked for.  Every launch does (a
-// call of 3.6 us of host time, 3.3 without), so nothing has to be kept of
+// call of 3.5 us of host time, 3.4 without), so nothing has to be kept of
 // which GPU has been asked.
 template <typename K>
 zc_status allow_lds(K kernel, int bytes) {

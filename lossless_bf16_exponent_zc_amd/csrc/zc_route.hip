@@ -13,8 +13,9 @@
 // before its own; from kMostSummed tiles on a launch between them scans the
 // tiles once for all.
 //
-// Bound by latency: 64 slots on 256 experts 3.6 us, 65,536 slots 8.6 us (0.8 MB,
-// 0.2 us at the memory's rate), 524,288 slots 14.7 us.  Tiles of 2048 put 65,536
+// Bound by latency: 64 slots on 256 experts 3.7 us, 65,536 slots 8.8 us in a row
+// of such calls and 10.6 behind other kernels (4.7 + 5.9; 0.8 MB, 0.2 us at the
+// memory's rate), 524,288 slots 15 us.  Tiles of 2048 put 65,536
 // slots on 32 CUs and leave few counts to add up (tiles of 1024 in three
 // launches: 16.3 us); one launch for 8192 slots took 12.5 us, two take 8.
 #include "zc_experts_kernels.h"
