@@ -4,8 +4,6 @@ import os
 import subprocess
 import sys
 
-import pytest
-
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 SHIM = r"""
@@ -43,7 +41,8 @@ def run(tmp_path, fails):
     src, lib = tmp_path / "shim.c", tmp_path / "shim.so"
     src.write_text(SHIM)
     subprocess.run(["gcc", "-shared", "-fPIC", str(src), "-o", str(lib)], check=True)
-    env = dict(os.environ, LD_PRELOAD=str(lib), FAILS=fails)
+    before = os.environ.get("LD_PRELOAD")
+    env = dict(os.environ, LD_PRELOAD=str(lib) + (":" + before if before else ""), FAILS=fails)
     r = subprocess.run([sys.executable, "-c", CHILD, ROOT, str(lib)], env=env, capture_output=True, text=True, timeout=110)
     assert r.returncode == 0, r.stderr
     return [tuple(map(int, line.split())) for line in r.stdout.splitlines()]
