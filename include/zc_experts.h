@@ -1,13 +1,14 @@
 /*
  * zc_experts.h -- rows of a mixture of experts on AMD MI355X (gfx950): C ABI.
  *
- * What happens around the compressed all-to-all of zc.h: tokens are sorted by
+ * What happens around the compressed all-to-all of zc.h: tokens choose their
+ * experts (zc_choose, with the loss that balances them), are sorted by
  * expert (zc_route, zc_dispatch), optionally as 8-bit blocks, the experts'
  * matrix products run on the sorted rows (zc_expert_product), rows go back to
  * their tokens with the router's weights applied (zc_combine), and the
  * gradients of all of these (zc_combine with no weights is the gradient of
  * zc_dispatch; zc_combine_backward; zc_expert_product on transposed weights;
- * zc_expert_weight_grad).
+ * zc_expert_weight_grad; zc_choose_backward).
  *
  * Rows.  A slot is one (token, choice) pair, i = token * topk + choice, with
  * an expert id.  An id outside [0, experts) has no row here (another GPU's
@@ -178,6 +179,54 @@ zc_status zc_expert_weight_grad(const void *d_y, const void *d_y_scale, const vo
                                 uint32_t k, const int32_t *d_offsets, void *d_dw,
                                 uint32_t out_dtype, void *d_ws, uint64_t ws_bytes,
                                 hipStream_t stream);
+
+typedef enum zc_score { ZC_SOFTMAX = 0, ZC_SIGMOID = 1 } zc_score;
+
+/*
+ * The router's choice.  From logits l [tokens, experts] of one of the three
+ * row types: scores s = softmax(l) or sigmoid(l) of each token, in 32 bits.
+ * Every token chooses the topk experts of largest l, or with d_bias (float
+ * [experts], part of the choice only) of largest s + bias, compared in 64 bits;
+ * in that order, ties to the lower index.  A logit or a bias of -Inf closes an
+ * expert: it is never chosen, nor is one whose logit is NaN; where fewer than
+ * topk are left, the other ids are -1, which zc_route gives no row, and their
+ * weights 0.  d_ids int32 and d_weights float [tokens, topk]: a weight is
+ * scale * s, or with normalize scale * s / (sum of the token's chosen s), which
+ * does not underflow where every s does.  NaN, and softmax's +Inf, make the
+ * token's scores NaN, and with them its weights, the sums and the loss.
+ *
+ * d_mask (bytes [tokens], or NULL): tokens where it is 0 choose -1 throughout
+ * and are counted nowhere; their logits are not read.
+ *
+ * The balance loss is made of p = s / (sum of the token's s) and the T counted
+ * tokens: d_counts[e] (int32) choices of e, d_sums[e] (float) = sum of p[t,e]
+ * over the tokens, *d_counted (int32) = T, and
+ *   *d_loss = balance * experts / (topk * T^2) * sum over e of counts[e] * sums[e],
+ * 1 * balance for even choices and shares; 0 without a counted token.  Counts,
+ * sums and T of several GPUs add up to those of all.
+ */
+uint64_t zc_choose_workspace_bytes(uint64_t tokens, uint32_t topk, uint32_t experts);
+zc_status zc_choose(const void *d_logits, uint64_t stride, uint32_t dtype, uint64_t tokens,
+                    uint32_t topk, uint32_t experts, uint32_t score, int normalize, float scale,
+                    float balance, const float *d_bias, const uint8_t *d_mask, int32_t *d_ids,
+                    float *d_weights, int32_t *d_counts, float *d_sums, int32_t *d_counted,
+                    float *d_loss, void *d_ws, uint64_t ws_bytes, hipStream_t stream);
+
+/*
+ * The gradient of zc_choose for the logits (of their type, d_dlogits [tokens,
+ * experts]), given that of the weights (d_dweights float [tokens, topk], as
+ * zc_combine_backward writes it; NULL: none) and that of the loss (*d_dloss;
+ * NULL: 1).  d_ids, d_counts, d_counted as zc_choose wrote them, or counts and
+ * T added up over GPUs; they, and which experts are chosen, count as constants.
+ * The ids of one token differ from each other, apart from those without an
+ * expert, which have no gradient.  Masked tokens get zeros.
+ */
+zc_status zc_choose_backward(const void *d_logits, uint64_t stride, uint32_t dtype, uint64_t tokens,
+                             uint32_t topk, uint32_t experts, uint32_t score, int normalize,
+                             float scale, float balance, const uint8_t *d_mask, const int32_t *d_ids,
+                             const int32_t *d_counts, const int32_t *d_counted,
+                             const float *d_dweights, const float *d_dloss, void *d_dlogits,
+                             uint64_t dlogits_stride, hipStream_t stream);
 
 #ifdef __cplusplus
 }

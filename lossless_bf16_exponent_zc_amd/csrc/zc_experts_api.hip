@@ -8,6 +8,8 @@ namespace {
 
 constexpr uint64_t kMaxRows = 0x7FFFFFFFull;
 constexpr uint32_t kMaxWidth = 1u << 24;
+constexpr uint64_t kDotsAt = 256, kDots = 64;  // in a choice's workspace: one double per 16 experts
+static_assert(kMaxExperts <= 16 * kDots, "one double per 16 experts");
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 uint64_t up64(uint64_t n, uint64_t m) { return (n + m - 1) / m * m; }
@@ -264,6 +266,54 @@ zc_status zc_expert_weight_grad(const void* d_y, const void* d_y_scale, const vo
                            stored((uint32_t)rows), experts, n, k, up_to(n, 4), up_to(k, 4), out_dtype};
     const WeightGradPlan plan = plan_weight_grad(a.rows, experts, n, k, d_ws != nullptr);
     return finished(launch_weight_grad(a, plan, d_ws, stream));
+}
+
+uint64_t zc_choose_workspace_bytes(uint64_t tokens, uint32_t topk, uint32_t experts) {
+    if (!route_limits(tokens, topk, experts, 1)) return 0;
+    // the count of finished workgroups, their dots, the first kernel's parts
+    const uint64_t parts = choose_parts(tokens, experts);
+    return up64(kDotsAt + kDots * 8 + parts * 4 + parts * experts * 8, 256);
+}
+
+zc_status zc_choose(const void* d_logits, uint64_t stride, uint32_t dtype, uint64_t tokens, uint32_t topk,
+                    uint32_t experts, uint32_t score, int normalize, float scale, float balance, const float* d_bias,
+                    const uint8_t* d_mask, int32_t* d_ids, float* d_weights, int32_t* d_counts, float* d_sums,
+                    int32_t* d_counted, float* d_loss, void* d_ws, uint64_t ws_bytes, hipStream_t stream) {
+    if (dtype > ZC_FP32 || score > ZC_SIGMOID) return ZC_ERR_INVALID_ARG;
+    if (!route_limits(tokens, topk, experts, 1)) return ZC_ERR_UNSUPPORTED;
+    if (bad_words(d_counts) || bad_words(d_sums) || bad_words(d_counted) || bad_words(d_loss) || !aligned(d_bias, 4) ||
+        !d_ws || !aligned(d_ws, 256))
+        return ZC_ERR_INVALID_ARG;
+    if (tokens && (bad_matrix(d_logits, stride, experts, dtype) || bad_words(d_ids) || bad_words(d_weights)))
+        return ZC_ERR_INVALID_ARG;
+    if (ws_bytes < zc_choose_workspace_bytes(tokens, topk, experts)) return ZC_ERR_CAPACITY;
+    const uint64_t parts = choose_parts(tokens, experts);
+    uint8_t* ws = static_cast<uint8_t*>(d_ws);
+    ChooseArgs a{d_logits, stride, d_bias, d_mask, (uint32_t)tokens, topk, experts, normalize ? 1u : 0u, scale, balance,
+                 d_ids, d_weights, d_counts, d_sums, d_counted, d_loss};
+    a.arrived = reinterpret_cast<uint32_t*>(ws);
+    a.dots = reinterpret_cast<double*>(ws + kDotsAt);
+    a.part_live = reinterpret_cast<uint32_t*>(ws + kDotsAt + kDots * 8);
+    a.part_sums = reinterpret_cast<float*>(a.part_live + parts);
+    a.part_counts = reinterpret_cast<uint32_t*>(a.part_sums + parts * experts);
+    return finished(launch_choose(a, dtype, score == ZC_SIGMOID, stream));
+}
+
+zc_status zc_choose_backward(const void* d_logits, uint64_t stride, uint32_t dtype, uint64_t tokens, uint32_t topk,
+                             uint32_t experts, uint32_t score, int normalize, float scale, float balance,
+                             const uint8_t* d_mask, const int32_t* d_ids, const int32_t* d_counts,
+                             const int32_t* d_counted, const float* d_dweights, const float* d_dloss, void* d_dlogits,
+                             uint64_t dlogits_stride, hipStream_t stream) {
+    if (dtype > ZC_FP32 || score > ZC_SIGMOID) return ZC_ERR_INVALID_ARG;
+    if (!route_limits(tokens, topk, experts, 1)) return ZC_ERR_UNSUPPORTED;
+    if (bad_words(d_counts) || bad_words(d_counted) || !aligned(d_dloss, 4)) return ZC_ERR_INVALID_ARG;
+    if (!tokens) return ZC_OK;
+    if (bad_matrix(d_logits, stride, experts, dtype) || bad_matrix(d_dlogits, dlogits_stride, experts, dtype) ||
+        !aligned(d_dweights, 4) || (d_dweights && bad_words(d_ids)))
+        return ZC_ERR_INVALID_ARG;
+    const ChooseGradArgs a{d_logits, stride, d_mask, (uint32_t)tokens, topk, experts, normalize ? 1u : 0u, scale, balance,
+                           d_ids, d_counts, d_counted, d_dweights, d_dloss, d_dlogits, dlogits_stride};
+    return finished(launch_choose_backward(a, dtype, score == ZC_SIGMOID, stream));
 }
 
 }  // extern "C"

@@ -32,6 +32,8 @@ struct Library {
     decltype(&zc_expert_product) expert_product;
     decltype(&zc_expert_weight_grad) expert_weight_grad;
     decltype(&zc_expert_weight_grad_workspace_bytes) expert_weight_grad_workspace_bytes;
+    decltype(&zc_choose) choose;
+    decltype(&zc_choose_backward) choose_backward;
 } zc;
 PyObject* error_type = nullptr;  // binding.ZcError
 
@@ -388,6 +390,72 @@ void expert_weight_grad(Args a) {  // y, x, dw, offsets, ws, stream
             dw.data_ptr(), (uint32_t)dtype_of(dw.scalar_type()), ws, need, c.stream(a[5]));
 }
 
+float real(PyObject* o, const char* what) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse(what, "a number expected");
+    }
+    return (float)v;
+}
+
+// What a Router passes: (tokens, topk, experts, workspace bytes, score,
+// normalize, scale, balance).
+struct RouterSizes {
+    uint64_t tokens, ws_bytes;
+    uint32_t topk, experts, score;
+    int normalize;
+    float scale, balance;
+    explicit RouterSizes(PyObject* o) {
+        PyObject* const* v = items(o, "router", 8);
+        tokens = number(v[0], "tokens");
+        topk = size32(number(v[1], "topk"), "topk");
+        experts = size32(number(v[2], "experts"), "experts");
+        ws_bytes = number(v[3], "workspace");
+        score = size32(number(v[4], "score"), "score");
+        normalize = number(v[5], "normalize") != 0;
+        scale = real(v[6], "scale");
+        balance = real(v[7], "balance");
+    }
+    uint64_t slots() const { return tokens * topk; }
+};
+
+void choose(Args a) {  // sizes, logits, choice, ws, bias, mask, stream
+    Call c;
+    const RouterSizes z(a[0]);
+    const Matrix x = c.matrix(a[1], "logits", z.tokens, -1, z.experts);
+    PyObject* const* o = items(a[2], "choice", 6);
+    int32_t* ids = c.flat<int32_t>(o[0], "ids", at::kInt, z.slots());
+    float* weights = c.flat<float>(o[1], "weights", at::kFloat, z.slots());
+    int32_t* counts = c.flat<int32_t>(o[2], "counts", at::kInt, z.experts);
+    float* sums = c.flat<float>(o[3], "sums", at::kFloat, z.experts);
+    int32_t* counted = c.flat<int32_t>(o[4], "counted", at::kInt, 1);
+    float* loss = c.flat<float>(o[5], "loss", at::kFloat, 1);
+    uint64_t bytes = 0;
+    void* ws = c.flat(a[3], "workspace", at::kByte, z.ws_bytes, &bytes);
+    const float* bias = c.flat_or_null<float>(a[4], "bias", at::kFloat, z.experts);
+    const uint8_t* mask = c.flat_or_null<uint8_t>(a[5], "mask", at::kBool, z.tokens);
+    enqueue("zc_choose", zc.choose, x.p, x.stride, (uint32_t)x.dtype, z.tokens, z.topk, z.experts, z.score, z.normalize,
+            z.scale, z.balance, bias, mask, ids, weights, counts, sums, counted, loss, ws, bytes, c.stream(a[6]));
+}
+
+void choose_backward(Args a) {  // sizes, logits, choice, dweights, dloss, dlogits, mask, stream
+    Call c;
+    const RouterSizes z(a[0]);
+    const Matrix x = c.matrix(a[1], "logits", z.tokens, -1, z.experts);
+    const Matrix dx = c.matrix(a[5], "dlogits", z.tokens, x.dtype, z.experts);
+    PyObject* const* o = items(a[2], "choice", 6);
+    const int32_t* ids = c.flat<int32_t>(o[0], "ids", at::kInt, z.slots());
+    const int32_t* counts = c.flat<int32_t>(o[2], "counts", at::kInt, z.experts);
+    const int32_t* counted = c.flat<int32_t>(o[4], "counted", at::kInt, 1);
+    const float* dweights = c.flat_or_null<float>(a[3], "dweights", at::kFloat, z.slots());
+    const float* dloss = c.flat_or_null<float>(a[4], "dloss", at::kFloat, 1);
+    const uint8_t* mask = c.flat_or_null<uint8_t>(a[6], "mask", at::kBool, z.tokens);
+    enqueue("zc_choose_backward", zc.choose_backward, x.p, x.stride, (uint32_t)x.dtype, z.tokens, z.topk, z.experts,
+            z.score, z.normalize, z.scale, z.balance, mask, ids, counts, counted, dweights, dloss, dx.p, dx.stride,
+            c.stream(a[7]));
+}
+
 // A call as Python makes it: exactly N positional arguments, every C++
 // exception turned into Python's.
 template <void (*F)(Args), int N>
@@ -428,7 +496,8 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
                      get("zc_combine_backward", zc.combine_backward) && get("zc_quantize_rows", zc.quantize_rows) &&
                      get("zc_quantize_weights", zc.quantize_weights) && get("zc_quantize_columns", zc.quantize_columns) &&
                      get("zc_expert_product", zc.expert_product) && get("zc_expert_weight_grad", zc.expert_weight_grad) &&
-                     get("zc_expert_weight_grad_workspace_bytes", zc.expert_weight_grad_workspace_bytes);
+                     get("zc_expert_weight_grad_workspace_bytes", zc.expert_weight_grad_workspace_bytes) &&
+                     get("zc_choose", zc.choose) && get("zc_choose_backward", zc.choose_backward);
     if (!all) return nullptr;
     Py_INCREF(args[0]);
     Py_XDECREF(error_type);
@@ -441,7 +510,7 @@ PyMethodDef methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&bind)), METH_FASTCALL, nullptr},
     CALL(route, 5), CALL(dispatch, 5), CALL(dispatch_fp8, 5), CALL(combine, 6), CALL(combine_backward, 8),
     CALL(quantize_rows, 4), CALL(quantize_weights, 4), CALL(quantize_columns, 4), CALL(expert_product, 6),
-    CALL(expert_weight_grad, 6), {nullptr, nullptr, 0, nullptr}};
+    CALL(expert_weight_grad, 6), CALL(choose, 7), CALL(choose_backward, 8), {nullptr, nullptr, 0, nullptr}};
 #undef CALL
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "zc_experts_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

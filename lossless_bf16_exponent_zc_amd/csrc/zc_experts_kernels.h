@@ -96,6 +96,44 @@ struct WeightGradArgs {
     uint32_t out_dtype;
 };
 
+struct ChooseArgs {
+    const void* logits;
+    uint64_t stride;         // elements
+    const float* bias;       // or null
+    const uint8_t* mask;     // or null: every token counts
+    uint32_t tokens, topk, experts;
+    uint32_t normalize;
+    float scale, balance;
+    int32_t* ids;
+    float* weights;
+    int32_t* counts;
+    float* sums;
+    int32_t* counted;
+    float* loss;
+    // workspace
+    uint32_t* arrived;       // workgroups of the second kernel that are done
+    double* dots;            // one per workgroup of the second kernel
+    uint32_t* part_live;     // per workgroup of the first kernel: tokens counted,
+    float* part_sums;        // shares and
+    uint32_t* part_counts;   // choices by expert
+};
+
+struct ChooseGradArgs {
+    const void* logits;
+    uint64_t stride;         // elements
+    const uint8_t* mask;     // or null
+    uint32_t tokens, topk, experts;
+    uint32_t normalize;
+    float scale, balance;
+    const int32_t* ids;
+    const int32_t* counts;
+    const int32_t* counted;
+    const float* dweights;   // or null: none
+    const float* dloss;      // or null: 1
+    void* dlogits;
+    uint64_t out_stride;     // elements
+};
+
 // How a weight gradient is cut: tiles of side x side, each segment summed in up
 // to `parts` parts that are joined afterwards (parts > 1 needs a workspace of
 // parts * experts * n * k floats).  split: whether parts are allowed.
@@ -116,6 +154,10 @@ zc_status launch_cast_weights(const CastTileArgs& a, uint32_t dtype, hipStream_t
 zc_status launch_cast_columns(const CastTileArgs& a, uint32_t dtype, hipStream_t stream);
 zc_status launch_product(const ProductArgs& a, hipStream_t stream);
 zc_status launch_weight_grad(const WeightGradArgs& a, const WeightGradPlan& plan, void* ws, hipStream_t stream);
+
+uint32_t choose_parts(uint64_t tokens, uint32_t experts);  // workgroups of the first kernel
+zc_status launch_choose(const ChooseArgs& a, uint32_t dtype, bool sigmoid, hipStream_t stream);
+zc_status launch_choose_backward(const ChooseGradArgs& a, uint32_t dtype, bool sigmoid, hipStream_t stream);
 
 // Whether a launch may have this many workgroups of 256 threads.
 inline bool fits(uint64_t workgroups) { return workgroups < (1ull << 24); }

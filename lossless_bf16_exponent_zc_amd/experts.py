@@ -1,6 +1,7 @@
 """Binding of the expert operators (the C ABI in include/zc_experts.h).
 
-Around the compressed all-to-all: ``ExpertPlan`` sorts tokens by expert
+Around the compressed all-to-all: ``Router`` chooses each token's experts and
+takes the balance loss and both gradients; ``ExpertPlan`` sorts tokens by expert
 (route, dispatch, dispatch_fp8), brings rows back with the router's weights
 (combine) and takes the gradients of both (combine_backward; the gradient of
 dispatch is combine without weights).  ``quantize_rows`` / ``_weights`` /
@@ -28,7 +29,7 @@ EXPERT_EXPORTS = (
     "zc_route_rows", "zc_route_workspace_bytes", "zc_route", "zc_dispatch", "zc_dispatch_fp8",
     "zc_combine", "zc_combine_backward", "zc_quantize_rows", "zc_quantize_weights",
     "zc_quantize_columns", "zc_expert_product", "zc_expert_weight_grad",
-    "zc_expert_weight_grad_workspace_bytes",
+    "zc_expert_weight_grad_workspace_bytes", "zc_choose_workspace_bytes", "zc_choose", "zc_choose_backward",
 )
 
 BLOCK = 128  # values per scale
@@ -54,7 +55,7 @@ def lib() -> ctypes.CDLL:
     if _lib is not None:
         return _lib
     L = binding.lib()
-    vp, u32, u64, i = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int
+    vp, u32, u64, i, f32 = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int, ctypes.c_float
     args = {
         "zc_route_rows": [u64, u32, u32, u32],
         "zc_route_workspace_bytes": [u64, u32, u32],
@@ -69,6 +70,9 @@ def lib() -> ctypes.CDLL:
         "zc_expert_product": [vp, vp, u64, vp, vp, u32, u32, u32, vp, vp, vp, u64, u32, vp],
         "zc_expert_weight_grad": [vp, vp, vp, vp, u64, u32, u32, u32, vp, vp, u32, vp, u64, vp],
         "zc_expert_weight_grad_workspace_bytes": [u64, u32, u32, u32],
+        "zc_choose_workspace_bytes": [u64, u32, u32],
+        "zc_choose": [vp, u64, u32, u64, u32, u32, u32, i, f32, f32] + [vp] * 9 + [u64, vp],
+        "zc_choose_backward": [vp, u64, u32, u64, u32, u32, u32, i, f32, f32] + [vp] * 7 + [u64, vp],
     }
     for name in EXPERT_EXPORTS:
         f = getattr(L, name)
@@ -80,7 +84,7 @@ def lib() -> ctypes.CDLL:
         raise ImportError(f"{e}: build the package with `python -c 'import __graft_entry__ as g; g.build()'`") from e
     calls.bind(ZcError, {name: ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in EXPERT_EXPORTS})
     for name in ("route", "dispatch", "dispatch_fp8", "combine", "combine_backward", "quantize_rows", "quantize_weights",
-                 "quantize_columns", "expert_product", "expert_weight_grad"):
+                 "quantize_columns", "expert_product", "expert_weight_grad", "choose", "choose_backward"):
         setattr(_zc, name, getattr(calls, name))
     _lib = L
     return L
@@ -158,6 +162,69 @@ class Routing(NamedTuple):
     counts: torch.Tensor
     row: torch.Tensor
     slot: torch.Tensor
+
+
+class Choice(NamedTuple):
+    """What tokens chose: ``ids`` int32 and ``weights`` float32 [tokens, topk]
+    (-1 and 0 without an expert), ``counts`` int32 [experts] (choices of each),
+    ``sums`` float32 [experts] (each one's shares of the scores, summed over
+    tokens), ``counted`` int32 [1] (tokens that are not masked), ``loss``
+    float32 [1].  ``counts``, ``sums`` and ``counted`` of several GPUs add up."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+    counts: torch.Tensor
+    sums: torch.Tensor
+    counted: torch.Tensor
+    loss: torch.Tensor
+
+
+class Router:
+    """How tokens choose their experts: ``score`` "softmax" or "sigmoid" of the
+    logits, weights divided by their sum over a token's choices (``normalize``)
+    and times ``scale``, and ``balance``, the factor of the balance loss.
+    Its ids and weights are what ``ExpertPlan.route`` and ``combine`` take."""
+
+    SCORES = ("softmax", "sigmoid")
+
+    def __init__(self, tokens: int, topk: int, experts: int, score: str = "softmax", normalize: bool = False,
+                 scale: float = 1.0, balance: float = 0.0):
+        self.tokens, self.topk, self.experts = int(tokens), int(topk), int(experts)
+        if min(self.tokens, self.topk, self.experts) < 0:
+            _bad("Router", "negative size")
+        if self.tokens >> 64 or max(self.topk, self.experts) >> 32:  # ctypes would cut them short
+            _bad("Router", "size past the library's types", ZC_ERR_UNSUPPORTED)
+        if score not in self.SCORES:
+            _bad("Router", f"score {score!r}")
+        self.score, self.normalize, self.scale, self.balance = score, bool(normalize), float(scale), float(balance)
+        self.workspace_bytes = lib().zc_choose_workspace_bytes(self.tokens, self.topk, self.experts)
+        if self.workspace_bytes == 0:
+            _bad("Router", f"{tokens} tokens, {topk} choices, {experts} experts", ZC_ERR_UNSUPPORTED)
+        self._sizes = (self.tokens, self.topk, self.experts, self.workspace_bytes, self.SCORES.index(score),
+                       int(self.normalize), self.scale, self.balance)
+
+    # buffers (torch allocation only) -------------------------------------
+    def empty_choice(self, device="cuda") -> Choice:
+        z = lambda *s, dtype=torch.int32: torch.zeros(*s, dtype=dtype, device=device)
+        f = torch.float32
+        return Choice(z(self.tokens, self.topk), z(self.tokens, self.topk, dtype=f), z(self.experts),
+                      z(self.experts, dtype=f), z(1), z(1, dtype=f))
+
+    def empty_workspace(self, device="cuda"):
+        return torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
+
+    # calls ----------------------------------------------------------------
+    def choose(self, logits, choice: Choice, ws, bias=None, mask=None, stream=None):
+        """Enqueue the choice by logits [tokens, experts].  bias: float32
+        [experts], added to the scores that are compared, not to the weights;
+        mask: bool [tokens], tokens where it is False choose no expert and are
+        counted nowhere."""
+        _zc.choose(self._sizes, logits, choice, ws, bias, mask, stream)
+
+    def choose_backward(self, logits, choice: Choice, dweights, dloss, dlogits, mask=None, stream=None):
+        """Enqueue the gradient for the logits: dweights float32 [tokens, topk]
+        (``combine_backward``'s) or None, dloss float32 [1] or None for 1.
+        choice.counts and .counted may have been added up over GPUs."""
+        _zc.choose_backward(self._sizes, logits, choice, dweights, dloss, dlogits, mask, stream)
 
 
 class ExpertPlan:
