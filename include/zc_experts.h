@@ -8,7 +8,8 @@
  * their tokens with the router's weights applied (zc_combine), and the
  * gradients of all of these (zc_combine with no weights is the gradient of
  * zc_dispatch; zc_combine_backward; zc_expert_product on transposed weights;
- * zc_expert_weight_grad; zc_choose_backward).
+ * zc_expert_weight_grad; zc_choose_backward).  zc_orthogonalize makes an update
+ * of the experts' weights from their gradients.
  *
  * Rows.  A slot is one (token, choice) pair, i = token * topk + choice, with
  * an expert id.  An id outside [0, experts) has no row here (another GPU's
@@ -227,6 +228,26 @@ zc_status zc_choose_backward(const void *d_logits, uint64_t stride, uint32_t dty
                              const int32_t *d_counts, const int32_t *d_counted,
                              const float *d_dweights, const float *d_dloss, void *d_dlogits,
                              uint64_t dlogits_stride, hipStream_t stream);
+
+/*
+ * Orthogonalised updates, each matrix x [n, k] of the batch by itself:
+ *   X = x / (|x| + eps),  |x| the root of the sum of squares (0 / 0 is 0), then
+ *   steps times  X <- a X + (b A + c A^2) X,  A = X X^T
+ * (X <- a X + X (b A + c A^2), A = X^T X, which is the same, where n > k).
+ * d_x contiguous [batch, n, k] of one of the three row types, d_out the result,
+ * bf16, contiguous; they may be the same memory.  Products take fp16 factors
+ * into 32-bit sums and X is kept in 22 bits (a pair of fp16): results are off
+ * by 2e-4 to 2e-3 of their root mean square, besides their rounding to bf16 of
+ * 1.7e-3, whatever the singular values.  That holds where X and A stay in
+ * fp16's range, as they do where no singular value passes about 5.  A matrix
+ * with a value that is not finite comes out as NaN, the others as they are.
+ * Limits: batch 0..65535, n and k 1..65536, steps 1..64.
+ * zc_orthogonalize_workspace_bytes is 0 past a limit.
+ */
+uint64_t zc_orthogonalize_workspace_bytes(uint32_t batch, uint32_t n, uint32_t k);
+zc_status zc_orthogonalize(const void *d_x, uint32_t dtype, uint32_t batch, uint32_t n, uint32_t k,
+                           uint32_t steps, float a, float b, float c, float eps, void *d_out,
+                           void *d_ws, uint64_t ws_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

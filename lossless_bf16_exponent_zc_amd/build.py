@@ -22,7 +22,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libzc.so")
 BINDING = os.path.join(HERE, "zc_experts_binding.so")
 SOURCES = ["zc_api.hip", "zc_sigma.hip", "zc_encode.hip", "zc_decode.hip", "zc_finish.hip",
-           "zc_experts_api.hip", "zc_route.hip", "zc_rows.hip", "zc_blocks.hip", "zc_product.hip", "zc_choose.hip"]
+           "zc_experts_api.hip", "zc_route.hip", "zc_rows.hip", "zc_blocks.hip", "zc_product.hip", "zc_choose.hip", "zc_orthogonalize.hip"]
 
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

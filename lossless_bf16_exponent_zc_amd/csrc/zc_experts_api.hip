@@ -8,6 +8,7 @@ namespace {
 
 constexpr uint64_t kMaxRows = 0x7FFFFFFFull;
 constexpr uint32_t kMaxWidth = 1u << 24;
+constexpr uint32_t kMaxBatch = 65535, kMaxSide = 1u << 16, kMaxSteps = 64;  // of an update
 constexpr uint64_t kDotsAt = 256, kDots = 64;  // in a choice's workspace: one double per 16 experts
 static_assert(kMaxExperts <= 16 * kDots, "one double per 16 experts");
 
@@ -26,6 +27,38 @@ bool route_limits(uint64_t tokens, uint32_t topk, uint32_t experts, uint32_t ali
 uint64_t route_rows(uint64_t tokens, uint32_t topk, uint32_t experts, uint32_t align) {
     const uint64_t slots = tokens * topk, used = slots < experts ? slots : experts;
     return up64(slots + used * (align - 1), align);
+}
+
+// Where the parts of an update's workspace lie; bytes 0 past a limit.
+struct OrthLayout {
+    uint64_t rows, cols, side, parts, hi_a, hi_b, lo, gram, poly, gram_rest, poly_rest, bytes;
+};
+
+OrthLayout orth_layout(uint32_t batch, uint32_t n, uint32_t k) {
+    OrthLayout l{};
+    if (!batch || batch > kMaxBatch || !n || !k || n > kMaxSide || k > kMaxSide) return l;
+    l.rows = up64(n, 64);
+    l.cols = up64(k, 64);
+    l.side = l.rows < l.cols ? l.rows : l.cols;
+    const uint64_t groups = ((uint64_t)n * k + 16383) / 16384;  // of 64 values a thread
+    l.parts = groups < 64 ? groups : 64;
+    uint64_t at = 0;
+    auto take = [&](uint64_t bytes) {
+        const uint64_t here = at;
+        at += up64(bytes, 256);
+        return here;
+    };
+    take(l.parts * batch * 8);
+    const uint64_t x = l.rows * l.cols * batch * 2, s = l.side * l.side * batch * 2;
+    l.hi_a = take(x);
+    l.hi_b = take(x);
+    l.lo = take(x);
+    l.gram = take(s);
+    l.poly = take(s);
+    l.gram_rest = take(l.side * batch * 4);
+    l.poly_rest = take(l.side * batch * 4);
+    l.bytes = at;
+    return l;
 }
 
 zc_status finished(zc_status launched) {
@@ -314,6 +347,32 @@ zc_status zc_choose_backward(const void* d_logits, uint64_t stride, uint32_t dty
     const ChooseGradArgs a{d_logits, stride, d_mask, (uint32_t)tokens, topk, experts, normalize ? 1u : 0u, scale, balance,
                            d_ids, d_counts, d_counted, d_dweights, d_dloss, d_dlogits, dlogits_stride};
     return finished(launch_choose_backward(a, dtype, score == ZC_SIGMOID, stream));
+}
+
+uint64_t zc_orthogonalize_workspace_bytes(uint32_t batch, uint32_t n, uint32_t k) { return orth_layout(batch, n, k).bytes; }
+
+zc_status zc_orthogonalize(const void* d_x, uint32_t dtype, uint32_t batch, uint32_t n, uint32_t k, uint32_t steps,
+                           float a, float b, float c, float eps, void* d_out, void* d_ws, uint64_t ws_bytes,
+                           hipStream_t stream) {
+    if (dtype > ZC_FP32 || !n || !k || !steps) return ZC_ERR_INVALID_ARG;
+    if (batch > kMaxBatch || n > kMaxSide || k > kMaxSide || steps > kMaxSteps) return ZC_ERR_UNSUPPORTED;
+    if (!batch) return ZC_OK;
+    if (bad_matrix(d_x, k, k, dtype) || bad_matrix(d_out, k, k, ZC_BF16) || !d_ws || !aligned(d_ws, 256))
+        return ZC_ERR_INVALID_ARG;
+    const OrthLayout l = orth_layout(batch, n, k);
+    if (ws_bytes < l.bytes) return ZC_ERR_CAPACITY;
+    uint8_t* ws = static_cast<uint8_t*>(d_ws);
+    auto half = [&](uint64_t at) { return reinterpret_cast<_Float16*>(ws + at); };
+    auto word = [&](uint64_t at) { return reinterpret_cast<float*>(ws + at); };
+    // a power of two about the square root of the longer side
+    uint32_t shift = 0;
+    while ((4ull << (2 * shift)) <= (n > k ? n : k)) ++shift;
+    const float scale = (float)(1u << shift);
+    const OrthArgs args{d_x, static_cast<__bf16*>(d_out), batch, n, k, (uint32_t)l.rows, (uint32_t)l.cols, (uint32_t)l.side,
+                        a, b, c, eps, scale, 1.0f / scale, 1.0f / (scale * scale), reinterpret_cast<double*>(ws),
+                        (uint32_t)l.parts, half(l.hi_a), half(l.hi_b), nullptr, nullptr, half(l.lo), half(l.gram),
+                        half(l.poly), word(l.gram_rest), word(l.poly_rest)};
+    return finished(launch_orthogonalize(args, dtype, steps, stream));
 }
 
 }  // extern "C"

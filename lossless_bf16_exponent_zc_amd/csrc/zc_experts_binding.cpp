@@ -34,6 +34,8 @@ struct Library {
     decltype(&zc_expert_weight_grad_workspace_bytes) expert_weight_grad_workspace_bytes;
     decltype(&zc_choose) choose;
     decltype(&zc_choose_backward) choose_backward;
+    decltype(&zc_orthogonalize) orthogonalize;
+    decltype(&zc_orthogonalize_workspace_bytes) orthogonalize_workspace_bytes;
 } zc;
 PyObject* error_type = nullptr;  // binding.ZcError
 
@@ -456,6 +458,27 @@ void choose_backward(Args a) {  // sizes, logits, choice, dweights, dloss, dlogi
             c.stream(a[7]));
 }
 
+void orthogonalize(Args a) {  // x, out, ws, steps, coefficients, eps, stream
+    Call c;
+    const at::Tensor& x = stack(c, a[0], "x");
+    const at::Tensor& out = stack(c, a[1], "out");
+    if (out.scalar_type() != at::kBFloat16) refuse("out", std::string("type ") + c10::toString(out.scalar_type()) + ", BFloat16 expected");
+    if (x.sizes() != out.sizes()) refuse("out", "shape " + shape_text(out.sizes()) + ", " + shape_text(x.sizes()) + " expected");
+    const uint32_t batch = size32(x.size(0), "x"), n = size32(x.size(1), "x"), k = size32(x.size(2), "x");
+    const uint32_t steps = size32(number(a[3], "steps"), "steps");
+    PyObject* const* f = items(a[4], "coefficients", 3);
+    const float fa = real(f[0], "coefficients"), fb = real(f[1], "coefficients"), fc = real(f[2], "coefficients");
+    const float eps = real(a[5], "eps");
+    const uint64_t need = zc.orthogonalize_workspace_bytes(batch, n, k);
+    at::Tensor own;  // from torch's allocator, on the current stream, which is the call's
+    uint64_t bytes = need;
+    void* ws = nullptr;
+    if (a[2] != Py_None) ws = c.flat(a[2], "workspace", at::kByte, need, &bytes);
+    else if (need) ws = (own = at::empty({(int64_t)need}, x.options().dtype(at::kByte))).data_ptr();
+    enqueue("zc_orthogonalize", zc.orthogonalize, x.data_ptr(), (uint32_t)dtype_of(x.scalar_type()), batch, n, k, steps, fa,
+            fb, fc, eps, out.data_ptr(), ws, bytes, c.stream(a[6]));
+}
+
 // A call as Python makes it: exactly N positional arguments, every C++
 // exception turned into Python's.
 template <void (*F)(Args), int N>
@@ -497,7 +520,9 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
                      get("zc_quantize_weights", zc.quantize_weights) && get("zc_quantize_columns", zc.quantize_columns) &&
                      get("zc_expert_product", zc.expert_product) && get("zc_expert_weight_grad", zc.expert_weight_grad) &&
                      get("zc_expert_weight_grad_workspace_bytes", zc.expert_weight_grad_workspace_bytes) &&
-                     get("zc_choose", zc.choose) && get("zc_choose_backward", zc.choose_backward);
+                     get("zc_choose", zc.choose) && get("zc_choose_backward", zc.choose_backward) &&
+                     get("zc_orthogonalize", zc.orthogonalize) &&
+                     get("zc_orthogonalize_workspace_bytes", zc.orthogonalize_workspace_bytes);
     if (!all) return nullptr;
     Py_INCREF(args[0]);
     Py_XDECREF(error_type);
@@ -510,7 +535,8 @@ PyMethodDef methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&bind)), METH_FASTCALL, nullptr},
     CALL(route, 5), CALL(dispatch, 5), CALL(dispatch_fp8, 5), CALL(combine, 6), CALL(combine_backward, 8),
     CALL(quantize_rows, 4), CALL(quantize_weights, 4), CALL(quantize_columns, 4), CALL(expert_product, 6),
-    CALL(expert_weight_grad, 6), CALL(choose, 7), CALL(choose_backward, 8), {nullptr, nullptr, 0, nullptr}};
+    CALL(expert_weight_grad, 6), CALL(choose, 7), CALL(choose_backward, 8),
+    CALL(orthogonalize, 7), {nullptr, nullptr, 0, nullptr}};
 #undef CALL
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "zc_experts_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -134,6 +134,25 @@ struct ChooseGradArgs {
     uint64_t out_stride;     // elements
 };
 
+struct OrthArgs {
+    const void* x;           // [batch][n][k]
+    __bf16* out;             // [batch][n][k]
+    uint32_t batch, n, k;
+    uint32_t rows, cols;     // n, k in multiples of 64
+    uint32_t side;           // the smaller of the two
+    float a, b, c, eps;
+    float scale, inverse, inverse_square;  // X is held times scale, a power of two
+    // workspace
+    double* part;            // [batch][parts] sums of squares
+    uint32_t parts;          // at most 64
+    _Float16 *hi_a, *hi_b;   // [batch][rows][cols], one step's X and the next one's
+    const _Float16* hi;      // the present one
+    _Float16* next;          // the other
+    _Float16* lo;            // [batch][rows][cols]
+    _Float16 *gram, *poly;   // [batch][side][side]
+    float *gram_rest, *poly_rest;  // [batch][side] what their diagonals were rounded by
+};
+
 // How a weight gradient is cut: tiles of side x side, each segment summed in up
 // to `parts` parts that are joined afterwards (parts > 1 needs a workspace of
 // parts * experts * n * k floats).  split: whether parts are allowed.
@@ -158,6 +177,8 @@ zc_status launch_weight_grad(const WeightGradArgs& a, const WeightGradPlan& plan
 uint32_t choose_parts(uint64_t tokens, uint32_t experts);  // workgroups of the first kernel
 zc_status launch_choose(const ChooseArgs& a, uint32_t dtype, bool sigmoid, hipStream_t stream);
 zc_status launch_choose_backward(const ChooseGradArgs& a, uint32_t dtype, bool sigmoid, hipStream_t stream);
+
+zc_status launch_orthogonalize(OrthArgs a, uint32_t dtype, uint32_t steps, hipStream_t stream);
 
 // Whether a launch may have this many workgroups of 256 threads.
 inline bool fits(uint64_t workgroups) { return workgroups < (1ull << 24); }

@@ -6,7 +6,8 @@ takes the balance loss and both gradients; ``ExpertPlan`` sorts tokens by expert
 (combine) and takes the gradients of both (combine_backward; the gradient of
 dispatch is combine without weights).  ``quantize_rows`` / ``_weights`` /
 ``_columns`` cast to 8-bit blocks of 128; ``expert_product`` and
-``expert_weight_grad`` multiply such blocks, expert by expert.
+``expert_weight_grad`` multiply such blocks, expert by expert;
+``orthogonalize`` makes updates of the experts' weights from their gradients.
 
 Argument marshalling and checks only, as in ``binding``: every buffer is the
 caller's, every call enqueues on the current (or the given) stream.  The
@@ -30,6 +31,7 @@ EXPERT_EXPORTS = (
     "zc_combine", "zc_combine_backward", "zc_quantize_rows", "zc_quantize_weights",
     "zc_quantize_columns", "zc_expert_product", "zc_expert_weight_grad",
     "zc_expert_weight_grad_workspace_bytes", "zc_choose_workspace_bytes", "zc_choose", "zc_choose_backward",
+    "zc_orthogonalize_workspace_bytes", "zc_orthogonalize",
 )
 
 BLOCK = 128  # values per scale
@@ -73,6 +75,8 @@ def lib() -> ctypes.CDLL:
         "zc_choose_workspace_bytes": [u64, u32, u32],
         "zc_choose": [vp, u64, u32, u64, u32, u32, u32, i, f32, f32] + [vp] * 9 + [u64, vp],
         "zc_choose_backward": [vp, u64, u32, u64, u32, u32, u32, i, f32, f32] + [vp] * 7 + [u64, vp],
+        "zc_orthogonalize_workspace_bytes": [u32, u32, u32],
+        "zc_orthogonalize": [vp, u32, u32, u32, u32, u32, f32, f32, f32, f32, vp, vp, u64, vp],
     }
     for name in EXPERT_EXPORTS:
         f = getattr(L, name)
@@ -84,7 +88,8 @@ def lib() -> ctypes.CDLL:
         raise ImportError(f"{e}: build the package with `python -c 'import __graft_entry__ as g; g.build()'`") from e
     calls.bind(ZcError, {name: ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in EXPERT_EXPORTS})
     for name in ("route", "dispatch", "dispatch_fp8", "combine", "combine_backward", "quantize_rows", "quantize_weights",
-                 "quantize_columns", "expert_product", "expert_weight_grad", "choose", "choose_backward"):
+                 "quantize_columns", "expert_product", "expert_weight_grad", "choose", "choose_backward",
+                 "orthogonalize"):
         setattr(_zc, name, getattr(calls, name))
     _lib = L
     return L
@@ -331,3 +336,25 @@ def expert_weight_grad(y: Fp8Columns, x: Fp8Columns, dw, offsets=None, ws=None, 
             _zc.expert_weight_grad(y, x, dw, offsets, None, None)
     else:
         _zc.expert_weight_grad(y, x, dw, offsets, ws, stream)
+
+
+def orthogonalize_workspace_bytes(batch: int, n: int, k: int) -> int:
+    """Bytes orthogonalize uses for x [batch, n, k] (0 past a limit)."""
+    if any(v < 0 or v >> 32 for v in (batch, n, k)):  # past every limit; ctypes would cut them short
+        return 0
+    return lib().zc_orthogonalize_workspace_bytes(batch, n, k)
+
+
+def orthogonalize(x, out, ws=None, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, stream=None):
+    """Enqueue the orthogonalised updates of x [batch, n, k] (momentum of
+    ``expert_weight_grad``'s results, say): X = x / (|x| + eps) of every matrix,
+    then ``steps`` times X <- a X + (b A + c A^2) X with A = X X^T and a, b, c the
+    coefficients.  out: bfloat16 [batch, n, k], which may be x.  Off by 2e-4 to
+    2e-3 of the results' root mean square besides their rounding.  ws: a workspace
+    of orthogonalize_workspace_bytes; without one it is taken from torch's
+    allocator, on the call's stream."""
+    if ws is None and stream is not None:
+        with torch.cuda.stream(stream):
+            _zc.orthogonalize(x, out, None, steps, tuple(coefficients), eps, None)
+    else:
+        _zc.orthogonalize(x, out, ws, steps, tuple(coefficients), eps, stream)

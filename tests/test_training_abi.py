@@ -1,7 +1,6 @@
-"""The router's part of include/zc_experts.h without a GPU: sizes, refusals
-before any HIP call, and the 64-bit definitions that the GPU is held to."""
-import ctypes
-
+"""The router and the orthogonalised updates of include/zc_experts.h without a
+GPU: sizes, refusals before any HIP call, and the 64-bit definitions that the
+GPU is held to."""
 import pytest
 import torch
 
@@ -74,3 +73,16 @@ def test_definitions_by_hand():
     assert abs(float(loss) - 3 * (0.5 * (1 / 3 + e) / 2 + 0.5 * (1 / 3 + 1 - e) / 2)) < 1e-15
     even = torch.zeros(6, 3, dtype=torch.float64)
     assert abs(float(plain.loss_of(torch.tensor([4, 4, 4]), plain.shares(even + 1).sum(0), 6, 2, 1.0)) - 1) < 1e-15
+
+
+def test_orthogonalize_refusals(L):
+    good = [P, 2, 2, 8, 12, 5, 3.0, -4.0, 2.0, 0.0, P, P, 1 << 24, None]
+    for i, v in ((0, None), (0, P + 2), (1, 3), (3, 0), (4, 0), (5, 0), (10, None), (10, P + 1), (11, None), (11, P + 64)):
+        assert rc(L.zc_orthogonalize, good, i, v) == BAD, (i, v)
+    for i, v in ((2, 65536), (3, 65537), (4, 65537), (5, 65)):
+        assert rc(L.zc_orthogonalize, good, i, v) == UNSUP, (i, v)
+    need = zc.orthogonalize_workspace_bytes(2, 8, 12)
+    assert need > 0 and rc(L.zc_orthogonalize, good, 12, need - 1) == CAP
+    assert rc(L.zc_orthogonalize, good, 2, 0) == binding.ZC_OK
+    for args in ((0, 8, 8), (1, 0, 8), (1, 8, 65537), (65536, 8, 8), (2**32 + 1, 8, 8), (1, 2**32 + 8, 8), (-1, 8, 8)):
+        assert zc.orthogonalize_workspace_bytes(*args) == 0
