@@ -31,17 +31,17 @@ uint64_t route_rows(uint64_t tokens, uint32_t topk, uint32_t experts, uint32_t a
 
 // Where the parts of an update's workspace lie; bytes 0 past a limit.
 struct OrthLayout {
-    uint64_t rows, cols, side, parts, hi_a, hi_b, lo, gram, poly, gram_rest, poly_rest, bytes;
+    uint64_t length, side, parts, hi_a, hi_b, lo, across, gram, poly, gram_rest, poly_rest, bytes;
 };
 
 OrthLayout orth_layout(uint32_t batch, uint32_t n, uint32_t k) {
     OrthLayout l{};
     if (!batch || batch > kMaxBatch || !n || !k || n > kMaxSide || k > kMaxSide) return l;
-    l.rows = up64(n, 64);
-    l.cols = up64(k, 64);
-    l.side = l.rows < l.cols ? l.rows : l.cols;
-    const uint64_t groups = ((uint64_t)n * k + 16383) / 16384;  // of 64 values a thread
-    l.parts = groups < 64 ? groups : 64;
+    l.length = up64(n > k ? n : k, 64);
+    l.side = up64(n > k ? k : n, 64);
+    // parts of at least 32 values a thread, enough for eight workgroups a CU
+    const uint64_t groups = ((uint64_t)n * k + 8191) / 8192, most = 2048 / batch + 1;
+    l.parts = groups < most ? groups : most;
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t here = at;
@@ -49,10 +49,11 @@ OrthLayout orth_layout(uint32_t batch, uint32_t n, uint32_t k) {
         return here;
     };
     take(l.parts * batch * 8);
-    const uint64_t x = l.rows * l.cols * batch * 2, s = l.side * l.side * batch * 2;
-    l.hi_a = take(x);
-    l.hi_b = take(x);
-    l.lo = take(x);
+    const uint64_t y = l.length * l.side * batch * 2, s = l.side * l.side * batch * 2;
+    l.hi_a = take(y);
+    l.hi_b = take(y);
+    l.lo = take(y);
+    l.across = take(y);
     l.gram = take(s);
     l.poly = take(s);
     l.gram_rest = take(l.side * batch * 4);
@@ -368,9 +369,9 @@ zc_status zc_orthogonalize(const void* d_x, uint32_t dtype, uint32_t batch, uint
     uint32_t shift = 0;
     while ((4ull << (2 * shift)) <= (n > k ? n : k)) ++shift;
     const float scale = (float)(1u << shift);
-    const OrthArgs args{d_x, static_cast<__bf16*>(d_out), batch, n, k, (uint32_t)l.rows, (uint32_t)l.cols, (uint32_t)l.side,
-                        a, b, c, eps, scale, 1.0f / scale, 1.0f / (scale * scale), reinterpret_cast<double*>(ws),
-                        (uint32_t)l.parts, half(l.hi_a), half(l.hi_b), nullptr, nullptr, half(l.lo), half(l.gram),
+    const OrthArgs args{d_x, static_cast<__bf16*>(d_out), batch, n, k, (uint32_t)l.length, (uint32_t)l.side, a, b, c, eps,
+                        scale, 1.0f / scale, 1.0f / (scale * scale), reinterpret_cast<double*>(ws), (uint32_t)l.parts,
+                        half(l.hi_a), half(l.hi_b), nullptr, nullptr, half(l.lo), half(l.across), half(l.gram),
                         half(l.poly), word(l.gram_rest), word(l.poly_rest)};
     return finished(launch_orthogonalize(args, dtype, steps, stream));
 }

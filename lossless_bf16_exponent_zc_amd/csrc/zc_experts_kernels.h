@@ -138,17 +138,17 @@ struct OrthArgs {
     const void* x;           // [batch][n][k]
     __bf16* out;             // [batch][n][k]
     uint32_t batch, n, k;
-    uint32_t rows, cols;     // n, k in multiples of 64
-    uint32_t side;           // the smaller of the two
+    uint32_t length, side;   // the larger and the smaller of n and k, in multiples of 64
     float a, b, c, eps;
-    float scale, inverse, inverse_square;  // X is held times scale, a power of two
+    float scale, inverse, inverse_square;  // Y is held times scale, a power of two
     // workspace
     double* part;            // [batch][parts] sums of squares
-    uint32_t parts;          // at most 64
-    _Float16 *hi_a, *hi_b;   // [batch][rows][cols], one step's X and the next one's
+    uint32_t parts;
+    _Float16 *hi_a, *hi_b;   // [batch][length][side], one step's Y and the next one's
     const _Float16* hi;      // the present one
     _Float16* next;          // the other
-    _Float16* lo;            // [batch][rows][cols]
+    _Float16* lo;            // [batch][length][side]
+    _Float16* across;        // [batch][side][length], the present hi turned over
     _Float16 *gram, *poly;   // [batch][side][side]
     float *gram_rest, *poly_rest;  // [batch][side] what their diagonals were rounded by
 };
