@@ -31,7 +31,7 @@ uint64_t route_rows(uint64_t tokens, uint32_t topk, uint32_t experts, uint32_t a
 
 // Where the parts of an update's workspace lie; bytes 0 past a limit.
 struct OrthLayout {
-    uint64_t length, side, parts, hi_a, hi_b, lo, across, gram, poly, gram_rest, poly_rest, bytes;
+    uint64_t length, side, parts, hi_a, hi_b, lo, across, square[3], rest[3], bytes;
 };
 
 OrthLayout orth_layout(uint32_t batch, uint32_t n, uint32_t k) {
@@ -54,10 +54,8 @@ OrthLayout orth_layout(uint32_t batch, uint32_t n, uint32_t k) {
     l.hi_b = take(y);
     l.lo = take(y);
     l.across = take(y);
-    l.gram = take(s);
-    l.poly = take(s);
-    l.gram_rest = take(l.side * batch * 4);
-    l.poly_rest = take(l.side * batch * 4);
+    for (uint64_t& at_square : l.square) at_square = take(s);
+    for (uint64_t& at_rest : l.rest) at_rest = take(l.side * batch * 4);
     l.bytes = at;
     return l;
 }
@@ -364,15 +362,20 @@ zc_status zc_orthogonalize(const void* d_x, uint32_t dtype, uint32_t batch, uint
     if (ws_bytes < l.bytes) return ZC_ERR_CAPACITY;
     uint8_t* ws = static_cast<uint8_t*>(d_ws);
     auto half = [&](uint64_t at) { return reinterpret_cast<_Float16*>(ws + at); };
-    auto word = [&](uint64_t at) { return reinterpret_cast<float*>(ws + at); };
     // a power of two about the square root of the longer side
     uint32_t shift = 0;
     while ((4ull << (2 * shift)) <= (n > k ? n : k)) ++shift;
     const float scale = (float)(1u << shift);
-    const OrthArgs args{d_x, static_cast<__bf16*>(d_out), batch, n, k, (uint32_t)l.length, (uint32_t)l.side, a, b, c, eps,
-                        scale, 1.0f / scale, 1.0f / (scale * scale), reinterpret_cast<double*>(ws), (uint32_t)l.parts,
-                        half(l.hi_a), half(l.hi_b), nullptr, nullptr, half(l.lo), half(l.across), half(l.gram),
-                        half(l.poly), word(l.gram_rest), word(l.poly_rest)};
+    OrthArgs args{d_x, static_cast<__bf16*>(d_out), batch, n, k, (uint32_t)l.length, (uint32_t)l.side, a, b, c, eps, scale,
+                  1.0f / scale, 1.0f / (scale * scale), reinterpret_cast<double*>(ws), (uint32_t)l.parts};
+    args.hi_a = half(l.hi_a);
+    args.hi_b = half(l.hi_b);
+    args.lo = half(l.lo);
+    args.across = half(l.across);
+    for (int i = 0; i < 3; ++i) {
+        args.square[i] = half(l.square[i]);
+        args.rest[i] = reinterpret_cast<float*>(ws + l.rest[i]);
+    }
     return finished(launch_orthogonalize(args, dtype, steps, stream));
 }
 

@@ -34,20 +34,26 @@ namespace {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-enum Product { kGram, kSquare, kApply, kLast };
+// Of matrices of side x side: A = Y^T Y (kGram), gamma M^2 + alpha M (kSquare),
+// gamma M N + alpha M + beta N (kMix).  Of Y: factor Y + Y M, in the making
+// (kApply) or as the result (kLast).
+enum Product { kGram, kSquare, kMix, kApply, kLast };
 
 // Tiles of kSide x kSide by four waves, 2 x 2, each T x T instruction tiles of
-// 16 x 16; S stages of 64 of the summed dimension in LDS.
+// 16 x 16; S stages in LDS, each of 64 of the summed dimension.
 template <int T_, int S_>
 struct Shape {
     static constexpr int T = T_, S = S_;
     static constexpr int kSide = 32 * T;
-    static constexpr int kOperand = kSide * 128;   // bytes of one operand's stage
+    static constexpr int kOperand = kSide * 128;  // bytes of one operand's stage
     static constexpr int kStage = 2 * kOperand;
-    static constexpr int kEach = kSide / 32;       // loads per wave, operand and stage
+    static constexpr int kEach = kSide / 32;      // loads per wave, operand and stage
     static constexpr int kLoads = 2 * kEach;
     static constexpr int kLds = S * kStage;
+    static constexpr int kOnCu = 2 * kLds <= 160 * 1024 ? 2 : 1;
 };
 
 // One operand of a product, result[i][j] = sum over c of left[i][c] right[j][c].
@@ -85,14 +91,24 @@ __device__ __forceinline__ void multiply(f32x4& acc, const Part& right, const Pa
     pin(acc);
 }
 
-// Piece c (16 bytes) of a row lies at place c ^ turn(row) of its 128 bytes, so
-// that the 16 lanes that a 16-byte read takes at a time find 16 places of the
-// 64 banks.
-__device__ __forceinline__ uint32_t turn(uint32_t row) { return (row >> 1) & 7; }
+// Row that lane row m (0..15) of part t holds: two neighbouring parts interleave
+// in fours, so that a lane's results of two by two parts are 8 neighbouring
+// columns of two rows, and 8 neighbouring rows where they leave turned over:
+// 16-byte words either way.
+__device__ __forceinline__ constexpr uint32_t part_row(uint32_t t, uint32_t m) {
+    return (t >> 1) * 32 + (m >> 2) * 8 + (t & 1) * 4 + (m & 3);
+}
+
+// Piece c (16 bytes) of a row lies at place c ^ turn(row) of its 128 bytes.  LDS
+// has 16 places side by side, two rows, and a 16-byte read takes 16 lanes at a
+// time, of which 8 have pieces one further than the other 8 (lanes 0-3, 12-15
+// with 20-27, and so on); with the rows in the order above these turns give
+// them 16 different places.
+__device__ __forceinline__ uint32_t turn(uint32_t row) { return ((row >> 1) & 1) + ((row >> 3) & 3) * 2; }
 
 // acc[ti][tj] += the products of a tile, over `blocks` blocks of 64.  A lane
-// then has, of part (ti, tj), row ti * 16 + (lane & 15) and the four columns
-// from tj * 16 + (lane >> 4) * 4 on.
+// then has, of part (ti, tj), row part_row(ti, lane & 15) and the four columns
+// from part_row(tj, (lane >> 4) * 4) on.
 template <typename SH>
 __device__ __forceinline__ void tile_product(const Operand& left, const Operand& right, uint32_t blocks, uint8_t* lds,
                                              f32x4 (&acc)[SH::T][SH::T]) {
@@ -116,10 +132,11 @@ __device__ __forceinline__ void tile_product(const Operand& left, const Operand&
                                                      at_r[n - E], 0, 0, 0);
     };
     // where a lane's two pieces of a row lie (pieces g and g + 4)
-    const uint32_t lo_l = ((wave >> 1) * T * 16 + r) * 128 + ((g ^ turn(r)) << 4);
-    const uint32_t lo_r = SH::kOperand + ((wave & 1) * T * 16 + r) * 128 + ((g ^ turn(r)) << 4);
+    const uint32_t first = part_row(0, r), in = first * 128 + ((g ^ turn(first)) << 4);
+    const uint32_t lo_l = (wave >> 1) * T * 2048 + in, lo_r = SH::kOperand + (wave & 1) * T * 2048 + in;
     auto read = [&](const uint8_t* stage, uint32_t lo, int t) {
-        return Part{{*reinterpret_cast<const f16x8*>(stage + lo + t * 2048), *reinterpret_cast<const f16x8*>(stage + (lo ^ 64) + t * 2048)}};
+        const uint8_t* p = stage + part_row(t, 0) * 128;
+        return Part{{*reinterpret_cast<const f16x8*>(p + lo), *reinterpret_cast<const f16x8*>(p + (lo ^ 64))}};
     };
 
     for (uint32_t s = 0; s < SH::S && s < blocks; ++s) {
@@ -216,6 +233,41 @@ __device__ __forceinline__ f16x4 turned_over(f16x4 v) {
     return __builtin_bit_cast(f16x4, xu32x2{__builtin_amdgcn_perm(a, oa, pick), __builtin_amdgcn_perm(b, ob, pick)});
 }
 
+// A block's two rows of 8 columns as two columns' 8 rows: o[w] is column 4 w +
+// (lane & 3) of the lane group's 8, and the 8 rows from the quad's first on.
+__device__ __forceinline__ void over_rows(f16x8 (&o)[2]) {
+    auto half = [](f16x8 v, auto w) {
+        constexpr int W = decltype(w)::value;
+        return turned_over(__builtin_shufflevector(v, v, W, W + 1, W + 2, W + 3));
+    };
+    typedef std::integral_constant<int, 0> First;
+    typedef std::integral_constant<int, 4> Second;
+    const f16x8 a = __builtin_shufflevector(half(o[0], First{}), half(o[1], First{}), 0, 1, 2, 3, 4, 5, 6, 7);
+    const f16x8 b = __builtin_shufflevector(half(o[0], Second{}), half(o[1], Second{}), 0, 1, 2, 3, 4, 5, 6, 7);
+    o[0] = a;
+    o[1] = b;
+}
+__device__ __forceinline__ void store_over(_Float16* m, uint32_t stride, uint32_t i, uint32_t j, f16x8 (&o)[2]) {
+    const uint32_t q = __lane_id() & 3;
+    over_rows(o);
+    *reinterpret_cast<f16x8*>(m + (uint64_t)(j + q) * stride + (i - q)) = o[0];
+    *reinterpret_cast<f16x8*>(m + (uint64_t)(j + 4 + q) * stride + (i - q)) = o[1];
+}
+
+// The first `left` of 8 values of 16 bits, at any element's address.
+__device__ __forceinline__ void store_some(__bf16* p, f16x8 o, int32_t left) {
+    typedef xu32x4 __attribute__((aligned(2))) Word;
+    const xu32x4 w = __builtin_bit_cast(xu32x4, o);
+    if (left >= 8) {
+        *reinterpret_cast<Word*>(p) = w;
+        return;
+    }
+    uint16_t* to = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+    for (int q = 0; q < 7; ++q)
+        if (q < left) to[q] = (uint16_t)(w[q / 2] >> (q & 1) * 16);
+}
+
 // Workgroup -> tile.  Workgroups go to the eight XCDs in turn, and an XCD takes
 // one run of neighbouring tiles, so that what its CUs read at one time is a few
 // strips, shared through its L2.
@@ -241,105 +293,184 @@ __device__ __forceinline__ Place banded(uint32_t index, uint32_t rows, uint32_t 
 
 // OVER: the result leaves turned over (kLast).
 template <typename SH, int KIND, bool OVER>
-__global__ __launch_bounds__(256, SH::T == 8 ? 1 : 2) void step_product(OrthArgs p, uint32_t tiles, uint32_t side_tiles) {
+__global__ __launch_bounds__(256, SH::kOnCu) void step_product(OrthArgs p, uint32_t tiles, uint32_t side_tiles) {
     extern __shared__ __align__(16) uint8_t lds[];
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr bool SYMMETRIC = KIND == kGram || KIND == kSquare;
+    constexpr bool SYMMETRIC = KIND <= kMix;
     constexpr int T = SH::T;
     const uint32_t place = of_run(blockIdx.x, gridDim.x >> 3), matrix = place / tiles, index = place % tiles;
     if (matrix >= p.batch) return;
     const Place at = SYMMETRIC ? lower(index) : banded(index, tiles / side_tiles, side_tiles);
     const uint32_t i0 = at.i * SH::kSide, j0 = at.j * SH::kSide;
     const uint64_t y_at = (uint64_t)matrix * p.length * p.side, s_at = (uint64_t)matrix * p.side * p.side;
-    const _Float16 *hi = p.hi + y_at, *across = p.across + y_at, *A = p.gram + s_at, *P = p.poly + s_at;
+    const _Float16 *hi = p.hi + y_at, *across = p.across + y_at, *M = p.matrix + s_at, *N = p.other + s_at;
     f32x4 acc[T][T];
 #pragma unroll
     for (int i = 0; i < T; ++i)
 #pragma unroll
         for (int j = 0; j < T; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    // addresses in scalar registers, where the loads to LDS want them
     auto rows_of = [](const _Float16* m, uint32_t from, uint32_t rows, uint32_t stride) {
-        return Operand{reinterpret_cast<const uint8_t*>(m + (uint64_t)from * stride), stride * 2, rows - from};
+        const uint64_t p = (uint64_t)(m + (uint64_t)from * stride);
+        const uint64_t scalar = (uint64_t)uniform((uint32_t)(p >> 32)) << 32 | uniform((uint32_t)p);
+        return Operand{reinterpret_cast<const uint8_t*>(scalar), stride * 2, rows - from};
     };
     if constexpr (KIND == kGram)
         tile_product<SH>(rows_of(across, i0, p.side, p.length), rows_of(across, j0, p.side, p.length), p.length / 64, lds, acc);
-    else if constexpr (KIND == kSquare)
-        tile_product<SH>(rows_of(A, i0, p.side, p.side), rows_of(A, j0, p.side, p.side), p.side / 64, lds, acc);
+    else if constexpr (SYMMETRIC)
+        tile_product<SH>(rows_of(M, i0, p.side, p.side), rows_of(N, j0, p.side, p.side), p.side / 64, lds, acc);
     else
-        tile_product<SH>(rows_of(hi, i0, p.length, p.side), rows_of(P, j0, p.side, p.side), p.side / 64, lds, acc);
+        tile_product<SH>(rows_of(hi, i0, p.length, p.side), rows_of(M, j0, p.side, p.side), p.side / 64, lds, acc);
 
-    const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4, q4 = r & 3;
-    const uint32_t ri = i0 + (wave >> 1) * T * 16 + r, rj = j0 + (wave & 1) * T * 16 + g * 4;
+    // Results leave in blocks of two by two parts: of a block, a lane has 8
+    // neighbouring columns of two rows, four apart.
+    const uint32_t lane = __lane_id(), wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    const uint32_t wi = i0 + (wave >> 1) * T * 16, wj = j0 + (wave & 1) * T * 16, ri = wi + part_row(0, r), rj = wj + g * 8;
     const uint32_t end_i = SYMMETRIC ? p.side : p.length;
-    const float* rest = (KIND == kSquare ? p.gram_rest : p.poly_rest) + (uint64_t)matrix * p.side;
+    auto results = [&](int b, int h) {
+        const int ti = b / (T / 2) * 2 + h, tj = b % (T / 2) * 2;
+        return __builtin_shufflevector(late(acc[ti][tj]), late(acc[ti][tj + 1]), 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    constexpr int kBlocks = T * T / 4, kAhead = kBlocks < 2 ? kBlocks : 2;  // loads run ahead by so many
+    // side and length are multiples of 64: a block is there or not as a whole
+    auto there = [&](int b) { return wi + b / (T / 2) * 32 < end_i && wj + b % (T / 2) * 32 < p.side; };
+    const float *rest_m = p.rest_m + (uint64_t)matrix * p.side, *rest_n = p.rest_n + (uint64_t)matrix * p.side;
+    if constexpr (SYMMETRIC) {
+        _Float16* out = p.made + s_at;
+        float* left_over = p.rest_made + (uint64_t)matrix * p.side;
+        struct Was {
+            f16x8 m[2], n[2];
+        };
+        auto fetch = [&](int b) {
+            const uint32_t i = ri + b / (T / 2) * 32, j = rj + b % (T / 2) * 32;
+            Was w;
 #pragma unroll
-    for (int ti = 0; ti < T; ++ti) {
-        const uint32_t i = ri + ti * 16;
-        if (i - r >= end_i) break;  // whole parts: side and length are multiples of 64
-        const float rest_i = KIND == kSquare ? rest[i] : 0.0f;
-#pragma unroll
-        for (int tj = 0; tj < T; ++tj) {
-            const uint32_t j = rj + tj * 16;
-            if (j - g * 4 >= p.side) break;
-            f32x4 v = late(acc[ti][tj]);
-            if constexpr (SYMMETRIC) {
-                if constexpr (KIND == kGram) {
-                    v *= p.inverse_square;
-                } else {
-                    const f16x4 was = *reinterpret_cast<const f16x4*>(A + (uint64_t)i * p.side + j);
-                    const f32x4 rest_j = *reinterpret_cast<const f32x4*>(rest + j);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        v[q] = (float)was[q] * (p.b + p.c * (rest_i + rest_j[q])) + p.c * v[q];
-                        if (i == j + q) v[q] += p.b * rest_i;
-                    }
-                }
-                _Float16* out = (KIND == kGram ? p.gram : p.poly) + s_at;
-                const f16x4 h = __builtin_convertvector(v, f16x4);
-                *reinterpret_cast<f16x4*>(out + (uint64_t)i * p.side + j) = h;
-                if (at.i != at.j) {
-                    *reinterpret_cast<f16x4*>(out + (uint64_t)(j + q4) * p.side + (i - q4)) = turned_over(h);
-                } else if (i - j < 4) {
-                    float* left_over = (KIND == kGram ? p.gram_rest : p.poly_rest) + (uint64_t)matrix * p.side;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (i == j + q) left_over[i] = v[q] - (float)h[q];
-                }
+            for (int h = 0; h < 2; ++h) {
+                const uint64_t e = (uint64_t)(i + 4 * h) * p.side + j;
+                w.m[h] = *reinterpret_cast<const f16x8*>(M + e);
+                w.n[h] = KIND == kMix ? *reinterpret_cast<const f16x8*>(N + e) : w.m[h];
+            }
+            return w;
+        };
+        auto value = [&](int b, int h, const Was& was) __attribute__((always_inline)) {
+            f32x8 v = results(b, h);
+            if constexpr (KIND == kGram) {
+                v *= p.inverse_square;
             } else {
-                const uint64_t e = y_at + (uint64_t)i * p.side + j;
-                const f16x4 h = *reinterpret_cast<const f16x4*>(p.hi + e), l = *reinterpret_cast<const f16x4*>(p.lo + e);
-                const f32x4 factor = p.a + *reinterpret_cast<const f32x4*>(rest + j);
-                v += factor * (__builtin_convertvector(h, f32x4) + __builtin_convertvector(l, f32x4));
-                if constexpr (KIND == kApply) {
-                    const f16x4 nh = __builtin_convertvector(v, f16x4);
-                    *reinterpret_cast<f16x4*>(p.next + e) = nh;
-                    *reinterpret_cast<f16x4*>(p.lo + e) = __builtin_convertvector(v - __builtin_convertvector(nh, f32x4), f16x4);
-                    *reinterpret_cast<f16x4*>(p.across + y_at + (uint64_t)(j + q4) * p.length + (i - q4)) = turned_over(nh);
-                } else {
-                    v *= p.inverse;
-                    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-                    bf16x4 o = __builtin_convertvector(v, bf16x4);
-                    uint32_t row = i, col = j;
-                    if (OVER) {
-                        o = __builtin_bit_cast(bf16x4, turned_over(__builtin_bit_cast(f16x4, o)));
-                        row = j + q4;
-                        col = i - q4;
-                    }
-                    if (row < p.n) {
-                        __bf16* out = p.out + ((uint64_t)matrix * p.n + row) * p.k + col;
-                        struct Four {
-                            __bf16 v[4];
-                        };
-                        if (col + 4 <= p.k) {
-                            *reinterpret_cast<Four*>(out) = Four{{o[0], o[1], o[2], o[3]}};
-                        } else {
+                // with what the diagonals of M and N were rounded by, to the first order
+                const uint32_t row = ri + b / (T / 2) * 32 + 4 * h, j = rj + b % (T / 2) * 32;
+                const f32x8 m = __builtin_convertvector(was.m[h], f32x8), n = __builtin_convertvector(was.n[h], f32x8);
+                v = p.gamma * (v + m * *reinterpret_cast<const f32x8*>(rest_n + j) + rest_m[row] * n) + p.alpha * m + p.beta * n;
+            }
+            return v;
+        };
+        auto leave = [&](int b, const Was& was) __attribute__((always_inline)) {
+            const uint32_t i = ri + b / (T / 2) * 32, j = rj + b % (T / 2) * 32;
+            f16x8 o[2];
 #pragma unroll
-                            for (int q = 0; q < 3; ++q)
-                                if (col + q < p.k) out[q] = o[q];
-                        }
+            for (int h = 0; h < 2; ++h) {
+                o[h] = __builtin_convertvector(value(b, h, was), f16x8);
+                *reinterpret_cast<f16x8*>(out + (uint64_t)(i + 4 * h) * p.side + j) = o[h];
+            }
+            store_over(out, p.side, i, j, o);
+        };
+        // What is left of the diagonal leaves turned over too, as what is right of
+        // it: the two halves of M N are only equal up to rounding, and which tile
+        // an element is in must not change it.
+        if (wi > wj && i0 + SH::kSide <= p.side) {
+            Was was[kAhead];
+            if (KIND != kGram)
+#pragma unroll
+                for (int b = 0; b < kAhead; ++b) was[b] = fetch(b);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const Was now = was[b % kAhead];
+                if (KIND != kGram && b + kAhead < kBlocks) was[b % kAhead] = fetch(b + kAhead);
+                leave(b, now);
+            }
+        } else if (wi >= wj) {
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+                if ((wi > wj || b / (T / 2) > b % (T / 2)) && there(b)) leave(b, KIND == kGram ? Was{} : fetch(b));
+        }
+        if (wi == wj) {
+#pragma unroll
+            for (int d = 0; d < T / 2; ++d) {
+                const int b = d * (T / 2) + d;
+                if (!there(b)) continue;
+                const uint32_t j = rj + d * 32;
+                const Was was = KIND == kGram ? Was{} : fetch(b);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t row = ri + d * 32 + 4 * h;
+                    const f32x8 v = value(b, h, was);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        float e = v[q];
+                        if (KIND != kGram && j + q == row) e += p.alpha * rest_m[row] + p.beta * rest_n[row];
+                        const _Float16 o = (_Float16)e;
+                        if (j + q <= row) out[(uint64_t)row * p.side + j + q] = o;
+                        if (j + q < row) out[(uint64_t)(j + q) * p.side + row] = o;
+                        if (j + q == row) left_over[row] = e - (float)o;
                     }
                 }
             }
         }
+    } else {
+        struct Was {
+            f16x8 hi[2], lo[2];
+        };
+        auto fetch = [&](int b) {
+            const uint32_t i = ri + b / (T / 2) * 32, j = rj + b % (T / 2) * 32;
+            Was w;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint64_t e = y_at + (uint64_t)(i + 4 * h) * p.side + j;
+                w.hi[h] = *reinterpret_cast<const f16x8*>(p.hi + e);
+                w.lo[h] = *reinterpret_cast<const f16x8*>(p.lo + e);
+            }
+            return w;
+        };
+        auto leave = [&](auto whole) __attribute__((always_inline)) {
+            constexpr bool WHOLE = decltype(whole)::value;
+            Was was[kAhead];
+#pragma unroll
+            for (int b = 0; b < kAhead; ++b)
+                if (WHOLE || there(b)) was[b] = fetch(b);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const Was now = was[b % kAhead];
+                if (b + kAhead < kBlocks && (WHOLE || there(b + kAhead))) was[b % kAhead] = fetch(b + kAhead);
+                if (!WHOLE && !there(b)) continue;
+                const uint32_t i = ri + b / (T / 2) * 32, j = rj + b % (T / 2) * 32;
+                const f32x8 factor = p.factor + *reinterpret_cast<const f32x8*>(rest_m + j);
+                f16x8 o[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const f32x8 v = results(b, h) + factor * (__builtin_convertvector(now.hi[h], f32x8) + __builtin_convertvector(now.lo[h], f32x8));
+                    if constexpr (KIND == kApply) {
+                        const uint64_t e = y_at + (uint64_t)(i + 4 * h) * p.side + j;
+                        o[h] = __builtin_convertvector(v, f16x8);
+                        *reinterpret_cast<f16x8*>(p.next + e) = o[h];
+                        *reinterpret_cast<f16x8*>(p.lo + e) = __builtin_convertvector(v - __builtin_convertvector(o[h], f32x8), f16x8);
+                    } else {
+                        o[h] = __builtin_bit_cast(f16x8, __builtin_convertvector(v * p.inverse, bf16x8));
+                    }
+                }
+                if constexpr (KIND == kApply) {
+                    store_over(p.across + y_at, p.length, i, j, o);
+                } else {
+                    __bf16* out = p.out + (uint64_t)matrix * p.n * p.k;
+                    if (OVER) over_rows(o);
+                    const uint32_t row = OVER ? j + (r & 3) : i, col = OVER ? i - (r & 3) : j;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (row + 4 * h < p.n) store_some(out + (uint64_t)(row + 4 * h) * p.k + col, o[h], (int32_t)(p.k - col));
+                }
+            }
+        };
+        if (i0 + SH::kSide <= p.length && j0 + SH::kSide <= p.side) leave(std::true_type{});
+        else leave(std::false_type{});
     }
 #endif
 }
@@ -423,13 +554,30 @@ __global__ __launch_bounds__(256) void normalize(OrthArgs p, uint32_t col_tiles)
 
 uint64_t tiles_of(const OrthArgs& a, int kind, uint32_t t) {
     const uint64_t side = (a.side + t - 1) / t, length = (a.length + t - 1) / t;
-    return kind == kGram || kind == kSquare ? side * (side + 1) / 2 : side * length;
+    return kind <= kMix ? side * (side + 1) / 2 : side * length;
 }
 
+// Which tiles.  Wide ones read least from LDS but are one to a CU, so that their
+// stores stand beside no other tile's products, and their rounds end late where
+// they hardly fill the CUs.  A round of tiles takes about per_sum hundredths of
+// the summed length and a fixed part, in units of what 256 x 256 tiles take for
+// one of it.  Measured, in us, at 256 / 128 / 64 wide:
+//   A^2   of 32 x 2048 384/394/541, 1 x 4096 93/105/160, 37 x 1024 89/64/77, 4 x 1408 48/26/25,
+//         1 x 1024 42/18/10, 128 x 128 23/12/8
+//   Y^T Y of 32 x 7168 x 2048 914/1043/2053, 37 x 1408 x 1024 85/85/110, 8 x 5056 x 640 92/49/28
+//   Y P   of 32 x 7168 x 2048 2668/2796/3550, 1 x 14336 x 4096 502/528/734, 37 x 1408 x 1024
+//         239/227/278, 8 x 5056 x 640 104/89/94, 1 x 2048 x 2048 56/30/31
 uint32_t tile_side(const OrthArgs& a, int kind) {
-    if (a.batch * tiles_of(a, kind, 256) >= 256) return 256;
-    if (a.batch * tiles_of(a, kind, 128) >= 256) return 128;
-    return 64;
+    const bool symmetric = kind <= kMix;
+    const uint64_t sum = kind == kGram ? a.length : a.side;
+    auto cost = [&](uint32_t t, uint32_t on_cu, uint64_t per_sum, uint64_t fixed) {
+        const uint64_t tiles = a.batch * tiles_of(a, kind, t), at_once = 256 * on_cu;
+        return (tiles + at_once - 1) / at_once * (per_sum * sum / 100 + fixed);
+    };
+    const bool alone = a.batch * tiles_of(a, kind, 128) <= 256;
+    const uint64_t wide = cost(256, 1, 100, symmetric ? 400 : 1000), mid = cost(128, 2, alone ? 53 : 62, symmetric ? 150 : 450),
+                   small = cost(64, 2, 29, symmetric ? 100 : 200);
+    return wide <= mid && wide <= small ? 256 : mid <= small ? 128 : 64;
 }
 
 template <typename SH, int KIND, bool OVER>
@@ -461,6 +609,50 @@ void prepare(const OrthArgs& a, bool over, hipStream_t stream) {
     else hipLaunchKernelGGL((normalize<T, false>), dim3(tiles, a.batch), dim3(256), 0, stream, a, cols);
 }
 
+// Whether two steps are taken at once where another one follows: from this side
+// on (below it their roundings average out less), and where Y is long enough
+// that the three products of side x side more cost less than one Y^T Y and one
+// Y P.  One step twice against both at once, us: 37 x 1408 x 1024 778/653, 32 x 7168
+// x 2048 7930/5650; but 4 x 2048 x 1408 212/210, 1 x 4096 x 4096 604/690.
+bool in_pairs(const OrthArgs& a) { return a.side >= 512 && 8ull * a.length >= 11ull * a.side; }
+
+// Makes gamma M N + alpha M + beta N of the matrices m and n as the matrix `to`.
+zc_status mix(OrthArgs& a, int m, int n, int to, float gamma, float alpha, float beta, hipStream_t stream) {
+    a.matrix = a.square[m];
+    a.other = a.square[n];
+    a.made = a.square[to];
+    a.rest_m = a.rest[m];
+    a.rest_n = a.rest[n];
+    a.rest_made = a.rest[to];
+    a.gamma = gamma;
+    a.alpha = alpha;
+    a.beta = beta;
+    return m == n ? product_of<kSquare>(a, stream) : product_of<kMix>(a, stream);
+}
+
+// The matrix by which one step, or two, go from Y to factor Y + Y M.  Of two:
+//   B = b A + c A^2, T = a A + B A, A' = a T + T B  (that is (a + B) A (a + B), the
+//   A of the step between), B' = b A' + c A'^2,
+//   (a + B) (a + B') = a^2 + M, M = B' B + a B' + a B,
+// so that Y is read and written once for both.  All of these are polynomials of
+// A, which commute and are symmetric.
+zc_status step_matrix(OrthArgs& a, bool two, int& m, hipStream_t stream) {
+    a.matrix = a.other = nullptr;
+    a.made = a.square[0];
+    a.rest_made = a.rest[0];
+    if (zc_status e = product_of<kGram>(a, stream)) return e;
+    a.factor = a.a;
+    m = 1;
+    if (zc_status e = mix(a, 0, 0, 1, a.c, a.b, 0, stream)) return e;         // B
+    if (!two) return ZC_OK;
+    a.factor = a.a * a.a;
+    m = 0;
+    if (zc_status e = mix(a, 1, 0, 2, 1, 0, a.a, stream)) return e;           // T
+    if (zc_status e = mix(a, 2, 1, 0, 1, a.a, 0, stream)) return e;           // A'
+    if (zc_status e = mix(a, 0, 0, 2, a.c, a.b, 0, stream)) return e;         // B'
+    return mix(a, 2, 1, 0, 1, a.a, a.a, stream);                              // M
+}
+
 }  // namespace
 
 zc_status launch_orthogonalize(OrthArgs a, uint32_t dtype, uint32_t steps, hipStream_t stream) {
@@ -472,12 +664,16 @@ zc_status launch_orthogonalize(OrthArgs a, uint32_t dtype, uint32_t steps, hipSt
     if (dtype == ZC_BF16) prepare<__bf16>(a, over, stream);
     else if (dtype == ZC_FP16) prepare<_Float16>(a, over, stream);
     else prepare<float>(a, over, stream);
-    for (uint32_t s = 0; s < steps; ++s) {
+    for (uint32_t s = 0; s < steps;) {
+        const bool two = in_pairs(a) && s + 2 < steps;
+        int m;
         a.hi = from;
         a.next = to;
-        if (zc_status e = product_of<kGram>(a, stream)) return e;
-        if (zc_status e = product_of<kSquare>(a, stream)) return e;
-        if (s + 1 == steps) return over ? product_of<kLast, true>(a, stream) : product_of<kLast>(a, stream);
+        if (zc_status e = step_matrix(a, two, m, stream)) return e;
+        a.matrix = a.square[m];
+        a.rest_m = a.rest[m];
+        s += two ? 2 : 1;
+        if (s == steps) return over ? product_of<kLast, true>(a, stream) : product_of<kLast>(a, stream);
         if (zc_status e = product_of<kApply>(a, stream)) return e;
         std::swap(from, to);
     }

@@ -41,19 +41,34 @@ def steps_wide(X, steps, a, b, c, rounded):
         return X
     scale = 2.0 ** math.floor(math.log2(X.shape[1]) / 2)
     half = lambda v: v.to(torch.float16).double()
-    for step in range(steps):
+
+    def kept(m):  # a matrix in fp16, and what its diagonal was rounded by
+        h = half(m)
+        return h, (m - h).diagonal()
+
+    def whole(m):
+        return m[0] + torch.diag(m[1])
+
+    def times(m, n):
+        return m[0] @ n[0] + m[1][:, None] * n[0] + m[0] * n[1]
+
+    side, length = (-(-v // 64) * 64 for v in X.shape)
+    done = 0
+    while done < steps:
         hi = half(X * scale) / scale
-        if step == 0:
-            X = hi + half((X - hi) * scale) / scale
-        whole = hi @ hi.t()
-        A = half(whole)
-        rest = (whole - A).diagonal()
-        P = A * (b + c * (rest[:, None] + rest)) + c * (A @ A) + b * torch.diag(rest)
-        h = half(P)
-        X = (a + (P - h).diagonal())[:, None] * X + h @ hi
-        if step + 1 < steps:
-            hi = half(X * scale) / scale
-            X = hi + half((X - hi) * scale) / scale
+        X = hi + half((X - hi) * scale) / scale
+        two = side >= 512 and 8 * length >= 11 * side and done + 2 < steps
+        A = kept(hi @ hi.t())
+        B = kept(b * whole(A) + c * times(A, A))
+        factor = a
+        if two:
+            T = kept(a * whole(A) + times(B, A))
+            A = kept(a * whole(T) + times(T, B))
+            D = kept(b * whole(A) + c * times(A, A))
+            B = kept(a * whole(D) + a * whole(B) + times(D, B))
+            factor = a * a
+        X = (factor + B[1])[:, None] * X + B[0] @ hi
+        done += 2 if two else 1
     return X
 
 
