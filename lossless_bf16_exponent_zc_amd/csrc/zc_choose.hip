@@ -1,5 +1,8 @@
 // zc_choose.hip -- the router: each token's choice of experts, the balance
 // loss, and the gradient of both.
+//
+// A token belongs to L neighbouring lanes of one wave, lane l holding experts
+// l * V to l * V + V - 1 in registers from the load of the logits on.
 #include "zc_experts_kernels.h"
 
 #include <type_traits>
@@ -10,19 +13,66 @@ namespace {
 
 constexpr float kInf = __builtin_inff();
 
-// A token belongs to L neighbouring lanes of one wave, lane l holding experts
-// l * V to l * V + V - 1.
-template <int L>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-    for (int d = 1; d < L; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
+// A lane's number that the compiler does not look through: what follows from it
+// is made anew for every token instead of being held over the loop (16
+// comparisons alone would take 32 scalar registers).
+__device__ __forceinline__ uint32_t anew(uint32_t v) {
+    asm volatile("" : "+v"(v));
     return v;
 }
+
+// The lane d further in a group: within 16 lanes a turn of the row by DPP.
+template <int D>
+__device__ __forceinline__ uint32_t turned(uint32_t v) {
+    if constexpr (D < 16) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + D, 0xF, 0xF, true);
+    else return __shfl_xor(v, D);
+}
+template <int D>
+__device__ __forceinline__ float turned(float v) {
+    return __uint_as_float(turned<D>(__float_as_uint(v)));
+}
+template <int D>
+__device__ __forceinline__ double turned(double v) {
+    const xu32x2 w = __builtin_bit_cast(xu32x2, v);
+    return __builtin_bit_cast(double, xu32x2{turned<D>(w[0]), turned<D>(w[1])});
+}
+// f over all lanes of a group, the same result in each (f commutes, and turns
+// by 1, 2, 4, 8 add in the same pairs in every lane).
+template <int L, int D = 1, typename T, typename F>
+__device__ __forceinline__ T over_group(T v, F f) {
+    if constexpr (D < L) return over_group<L, D * 2>(f(v, turned<D>(v)), f);
+    else return v;
+}
 template <int L>
-__device__ __forceinline__ float group_sum(float v) {
+__device__ __forceinline__ float group_max(float v) {
+    return over_group<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int L, typename T>
+__device__ __forceinline__ T group_sum(T v) {
+    // by exchange, so that every lane adds the same pairs
 #pragma unroll
     for (int d = 1; d < L; d <<= 1) v += __shfl_xor(v, d);
     return v;
+}
+
+// The larger and the smaller of two keys, none of them NaN.
+__device__ __forceinline__ double larger(double a, double b) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+#else
+    return a > b ? a : b;
+#endif
+}
+__device__ __forceinline__ double smaller(double a, double b) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    double r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+#else
+    return a < b ? a : b;
+#endif
 }
 
 // What LDS holds of one wave is seen by its other lanes.
@@ -31,68 +81,233 @@ __device__ __forceinline__ void wave_sees() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// V logits of a lane, -inf past the last expert.
+// e^x and 1/x in the hardware's rounding (x log2 e rounded once: |x| 2^-24 of
+// the result; 1 unit in the last place).
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+__device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf(x); }
+// 1/x, 0 for 0, NaN for NaN.
+__device__ __forceinline__ float share_of(float x) { return x == 0.0f ? 0.0f : inverse(x); }
+
 template <typename T, int V>
-__device__ __forceinline__ void load_logits(const T* row, uint32_t e0, uint32_t experts, float (&x)[V]) {
-    constexpr int kEach = 16 / sizeof(T) < V ? 16 / sizeof(T) : V;
+__device__ __forceinline__ void load_as(const T* row, uint32_t e0, uint32_t experts, float (&x)[V]) {
+    constexpr int kWord = 16 / sizeof(T), kEach = kWord < V ? kWord : V;
+    const int32_t left = (int32_t)experts - (int32_t)e0;
 #pragma unroll
     for (int j = 0; j < V; j += kEach) {
-        const int32_t left = (int32_t)experts - (int32_t)(e0 + j);
-        T v[16 / sizeof(T)];
-        const xu32x4 w = load_word(row + (left > 0 ? e0 + j : 0), left < kEach ? left : 16 / (int32_t)sizeof(T) > kEach ? kEach : left);
+        T v[kWord];
+        const xu32x4 w = load_word(row + (left > j ? e0 + j : 0), left - j < kEach ? left - j : kEach);
         __builtin_memcpy(v, &w, 16);
 #pragma unroll
-        for (int q = 0; q < kEach; ++q) x[j + q] = q < left ? to_float(v[q]) : -kInf;
+        for (int q = 0; q < kEach; ++q) x[j + q] = to_float(v[q]);
+    }
+    if (left < V) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = j < left ? x[j] : -kInf;
     }
 }
 
-// Scores of a token, all times one factor: softmax e^(x - max), sigmoid
-// e^(x - low) / (1 + e^x) with low = min(max, 0), so that the largest neither
-// overflows nor underflows; the score itself is s * back.  Infinite or NaN
-// logits but -inf make them NaN.
-template <int V, int L, bool SIGMOID>
-__device__ __forceinline__ float scores(const float (&x)[V], float (&s)[V], float& total) {
+// V logits of a lane, -inf past the last expert.
+template <int V>
+__device__ __forceinline__ void load_logits(const void* logits, uint64_t at, uint32_t dtype, uint32_t e0, uint32_t experts,
+                                            float (&x)[V]) {
+    if (dtype == ZC_BF16) load_as(static_cast<const __bf16*>(logits) + at, e0, experts, x);
+    else if (dtype == ZC_FP16) load_as(static_cast<const _Float16*>(logits) + at, e0, experts, x);
+    else load_as(static_cast<const float*>(logits) + at, e0, experts, x);
+}
+__device__ __forceinline__ float one_logit(const void* logits, uint64_t at, uint32_t dtype) {
+    if (dtype == ZC_BF16) return to_float(static_cast<const __bf16*>(logits)[at]);
+    if (dtype == ZC_FP16) return to_float(static_cast<const _Float16*>(logits)[at]);
+    return static_cast<const float*>(logits)[at];
+}
+
+// Scores of a token, all times one factor: softmax e^(x - base), base the
+// largest; sigmoid e^(x - base) / (1 + e^x), base = min(largest, 0), so that the
+// largest neither overflows nor underflows.  The score itself is s * back.
+// Infinite or NaN logits but -inf make softmax's NaN.
+__device__ __forceinline__ float score_of(float x, float base, bool sigmoid) {
+    if (!sigmoid) return exp_of(x - base);
+    const float t = exp_of(-fabsf(x)), down = inverse(1.0f + t);
+    if (base < 0.0f) return exp_of(x - base) * down;  // every x is below 0
+    return x < 0.0f ? t * down : x >= 0.0f ? down : x;
+}
+
+struct Scored {
+    float base, total, part, back;  // part: 1 / total
+};
+template <int L, int V>
+__device__ __forceinline__ Scored scores(const float (&x)[V], float (&s)[V], bool sigmoid) {
     float top = -kInf;
 #pragma unroll
     for (int j = 0; j < V; ++j) top = fmaxf(top, x[j]);
     top = group_max<L>(top);
-    float sum = 0.0f, low = 0.0f;
-    if (SIGMOID) {
-        low = top < 0.0f && top > -kInf ? top : 0.0f;
+    Scored r;
+    r.base = top == -kInf || (sigmoid && top > 0.0f) ? 0.0f : top;
+    float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            s[j] = low < 0.0f ? expf(x[j] - low) / (1.0f + expf(x[j])) : 1.0f / (1.0f + expf(-x[j]));
-            sum += s[j];
-        }
-    } else {
-        const float m = top == -kInf ? 0.0f : top;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            s[j] = expf(x[j] - m);
-            sum += s[j];
-        }
+    for (int j = 0; j < V; ++j) {
+        s[j] = score_of(x[j], r.base, sigmoid);
+        sum += s[j];
     }
-    total = group_sum<L>(sum);
-    return SIGMOID ? expf(low) : total > 0.0f ? 1.0f / total : total == 0.0f ? 0.0f : total;
+    r.total = group_sum<L>(sum);
+    r.part = share_of(r.total);
+    r.back = sigmoid ? exp_of(r.base) : r.part;
+    return r;
 }
 
-template <typename T, int L, int V, bool SIGMOID>
+// A comparison's value and its expert in one double that orders as they do,
+// larger values first and lower indices first among equals: a float leaves 29
+// bits of a double's mantissa free.  NaN and -inf become kClosed, or less by
+// their index.
+constexpr double kClosed = -0x1p128, kNone = -0x1p130;
+__device__ __forceinline__ double key_of(float v, uint32_t e) {
+    const double d = smaller(larger((double)(v + 0.0f), kClosed), -kClosed);  // -0 is 0
+    xu32x2 w = __builtin_bit_cast(xu32x2, d);
+    w[0] |= (kMaxExperts - 1 - e) ^ ((uint32_t)((int32_t)w[1] >> 31) & (kMaxExperts - 1));
+    return __builtin_bit_cast(double, w);
+}
+__device__ __forceinline__ int32_t expert_of(double key) {
+    const xu32x2 w = __builtin_bit_cast(xu32x2, key);
+    const uint32_t c = (w[0] ^ (uint32_t)((int32_t)w[1] >> 31)) & (kMaxExperts - 1);
+    return key <= kClosed ? -1 : (int32_t)(kMaxExperts - 1 - c);
+}
+__device__ __forceinline__ double value_of(double key) {
+    xu32x2 w = __builtin_bit_cast(xu32x2, key);
+    w[0] &= ~(kMaxExperts - 1);
+    return __builtin_bit_cast(double, w);
+}
+
+__device__ __forceinline__ void order(double& a, double& b) {
+    const double x = larger(a, b);
+    b = smaller(a, b);
+    a = x;
+}
+// Sorts N keys, largest first (Batcher's odd-even merges).
+template <int N, int STRIDE = 1, int M>
+__device__ __forceinline__ void merge(double (&k)[M], int at) {
+    if constexpr (STRIDE * 2 < N) {
+        merge<N, STRIDE * 2>(k, at);
+        merge<N, STRIDE * 2>(k, at + STRIDE);
+#pragma unroll
+        for (int i = STRIDE; i + STRIDE < N; i += STRIDE * 2) order(k[at + i], k[at + i + STRIDE]);
+    } else {
+        order(k[at], k[at + STRIDE]);
+    }
+}
+template <int N, int M>
+__device__ __forceinline__ void sort(double (&k)[M], int at = 0) {
+    if constexpr (N > 1) {
+        sort<N / 2>(k, at);
+        sort<N / 2>(k, at + N / 2);
+        merge<N>(k, at);
+    }
+}
+
+// The best D of a lane's keys, largest first.
+template <int V, int D>
+__device__ __forceinline__ void best_of(double (&k)[V], double (&best)[D]) {
+    if constexpr (D < V) {
+        sort<D>(k, 0);
+        sort<D>(k, D);
+#pragma unroll
+        for (int i = 0; i < D; ++i) best[i] = larger(k[i], k[2 * D - 1 - i]);  // the larger half, up and down again
+#pragma unroll
+        for (int d = D / 2; d; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < D; ++i)
+                if (!(i & d)) order(best[i], best[i + d]);
+    } else {
+        sort<V>(k);
+#pragma unroll
+        for (int i = 0; i < D; ++i) best[i] = k[i];
+    }
+}
+
+// Scores with a bias, compared in 64 bits one choice after the other: the way
+// for the few tokens whose scores 32 bits do not tell apart.
+template <int L, int V>
+__device__ __forceinline__ void choose_exactly(const ChooseArgs& a, uint64_t at, uint32_t e0, uint32_t l, int32_t (&ids)[64 / L]) {
+    float x[V];
+    load_logits<V>(a.logits, at, a.dtype, e0, a.experts, x);
+    double key[V], sum = 0.0;
+    float top = -kInf;
+#pragma unroll
+    for (int j = 0; j < V; ++j) top = fmaxf(top, x[j]);
+    top = group_max<L>(top);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        key[j] = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x[j])) : exp((double)x[j] - (double)top);
+        sum += key[j];
+        __builtin_amdgcn_sched_barrier(0);  // one after the other: side by side they take all registers
+    }
+    sum = group_sum<L>(sum);
+    uint32_t open = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        key[j] = (a.sigmoid ? key[j] : key[j] / sum) + (e0 + j < a.experts ? (double)a.bias[e0 + j] : 0.0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (x[j] > -kInf && key[j] > -(double)kInf) open |= 1u << j;  // neither closed nor NaN
+    }
+#pragma unroll
+    for (int h = 0; h < 64 / L; ++h) ids[h] = -1;
+    for (uint32_t k = 0; k < a.topk; ++k) {
+        double best = 0.0;
+        uint32_t of = ~0u;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if ((open >> j & 1) && (of == ~0u || key[j] > best)) {
+                best = key[j];
+                of = e0 + j;
+            }
+#pragma unroll
+        for (int d = 1; d < L; d <<= 1) {
+            const double other = __shfl_xor(best, d);
+            const uint32_t other_of = __shfl_xor(of, d);
+            if (other_of != ~0u && (of == ~0u || other > best || (other == best && other_of < of))) {
+                best = other;
+                of = other_of;
+            }
+        }
+        if (of - e0 < (uint32_t)V) open &= ~(1u << (of - e0));
+#pragma unroll
+        for (int h = 0; h < 64 / L; ++h)
+            if (k == h * L + l) ids[h] = (int32_t)of;
+    }
+}
+
+// Sum over a workgroup, in every thread; `shared` has room for 4.
+__device__ __forceinline__ double workgroup_sum(double v, double* shared) {
+    v = group_sum<64>(v);
+    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = shared[0] + shared[1] + shared[2] + shared[3];
+    __syncthreads();
+    return v;
+}
+
+__device__ __forceinline__ float loss_of(const ChooseArgs& a, double dot, uint32_t live) {
+    const double t = (double)live;
+    return live ? (float)((double)a.balance * a.experts * dot / ((double)a.topk * t * t)) : 0.0f;
+}
+
+// D: choices that one lane may have to give, at most.
+template <int L, int V, int D>
 __global__ __launch_bounds__(256) void choose(ChooseArgs a) {
     constexpr uint32_t G = 256 / L;  // tokens at a time
-    constexpr int kPitch = V + 4;
-    __shared__ __align__(16) float held[256 * kPitch];  // scores by lane; sums at the end
+    __shared__ float held[256 * V];
     __shared__ uint32_t hist[kMaxExperts];
     __shared__ uint32_t live_tokens;
-    const uint32_t tid = threadIdx.x, l = tid % L, g = tid / L, e0 = l * V;
+    __shared__ double shared[4];
+    const uint32_t tid = threadIdx.x, l = tid % L, g = tid / L;
     for (uint32_t e = tid; e < a.experts; e += 256) hist[e] = 0;
     if (tid == 0) live_tokens = 0;
     if (blockIdx.x == 0 && tid == 0) *a.arrived = 0;
     __syncthreads();
+    const bool sigmoid = a.sigmoid;
     float sums[V], bias[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         sums[j] = 0.0f;
-        bias[j] = a.bias && e0 + j < a.experts ? a.bias[e0 + j] : 0.0f;
+        bias[j] = a.bias && l * V + j < a.experts ? a.bias[l * V + j] : 0.0f;
     }
     uint32_t live = 0;
     for (uint32_t t = blockIdx.x * G + g; t < a.tokens; t += gridDim.x * G) {
@@ -106,112 +321,111 @@ __global__ __launch_bounds__(256) void choose(ChooseArgs a) {
             continue;
         }
         live += l == 0;
-        float x[V], s[V], total;
-        load_logits<T, V>(static_cast<const T*>(a.logits) + t * a.stride, e0, a.experts, x);
-        const float back = scores<V, L, SIGMOID>(x, s, total);
-        const float part = total > 0.0f ? 1.0f / total : total == 0.0f ? 0.0f : total;
+        const uint64_t at = t * a.stride;
+        const uint32_t e0 = anew(l * V);
+        float x[V], s[V];
+        load_logits<V>(a.logits, at, a.dtype, e0, a.experts, x);
+        const Scored r = scores<L, V>(x, s, sigmoid);
+        double keys[V], best[D];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            sums[j] += s[j] * part;
-            held[tid * kPitch + j] = s[j];
+            sums[j] += s[j] * r.part;
+            const float v = !a.bias ? x[j] : x[j] > -kInf ? s[j] * r.back + bias[j] : -kInf;
+            keys[j] = key_of(v, e0 + j);
         }
-        // what is compared, in 64 bits
-        double key[V];
-        float top = -kInf;
-        if (a.bias) {
+        best_of<V, D>(keys, best);
+        // the group's best, again and again; the lane that had it moves up
+        int32_t id[64 / L];
+        bool unsure = false;
+        double before = -kNone;
 #pragma unroll
-            for (int j = 0; j < V; ++j) top = fmaxf(top, x[j]);
-            top = group_max<L>(top);
-            double sum = 0.0;
+        for (int h = 0; h < 64 / L; ++h) {
+            id[h] = -1;
+            if (h * L >= (int)a.topk + 1) break;
+            for (uint32_t q = 0; q < L && h * L + q <= a.topk; ++q) {
+                const double top = over_group<L>(best[0], larger);
+                // 32-bit scores are off by less than 2^-19 of 1 or of the bias
+                if (a.bias && before > kClosed) {
+                    const double v = value_of(top), gap = value_of(before) - v;
+                    unsure |= !(gap > 0x1p-18 * (1.0 + fabs(v)));
+                }
+                before = top;
+                if (h * L + q == a.topk) break;
+                if (q == l) id[h] = expert_of(top);
+                if (best[0] == top) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                key[j] = SIGMOID ? 1.0 / (1.0 + exp(-(double)x[j])) : exp((double)x[j] - (double)top);
-                sum += key[j];
+                    for (int i = 0; i + 1 < D; ++i) best[i] = best[i + 1];
+                    best[D - 1] = kNone;
+                }
             }
-#pragma unroll
-            for (int d = 1; d < L; d <<= 1) sum += __shfl_xor(sum, d);
-#pragma unroll
-            for (int j = 0; j < V; ++j) key[j] = (SIGMOID ? key[j] : key[j] / sum) + (double)bias[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) key[j] = (double)x[j];
         }
-        uint32_t open = 0;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (x[j] > -kInf && key[j] > -(double)kInf) open |= 1u << j;  // neither closed nor NaN
-        wave_sees();
+        if (unsure) choose_exactly<L, V>(a, at, e0, l, id);
         float mine[64 / L], chosen = 0.0f;
 #pragma unroll
         for (int h = 0; h < 64 / L; ++h) {
             mine[h] = 0.0f;
-            if (h * L >= (int)a.topk) break;
-            int32_t id = -1;
-            for (uint32_t r = 0; r < L && h * L + r < a.topk; ++r) {
-                double best = 0.0;
-                uint32_t at = ~0u;
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if ((open >> j & 1) && (at == ~0u || key[j] > best)) {
-                        best = key[j];
-                        at = e0 + j;
-                    }
-#pragma unroll
-                for (int d = 1; d < L; d <<= 1) {
-                    const double other = __shfl_xor(best, d);
-                    const uint32_t oat = __shfl_xor(at, d);
-                    if (oat != ~0u && (at == ~0u || other > best || (other == best && oat < at))) {
-                        best = other;
-                        at = oat;
-                    }
-                }
-                if (at - e0 < (uint32_t)V) open &= ~(1u << (at - e0));
-                if (r == l) id = (int32_t)at;
-            }
             if (h * L + l < a.topk) {
-                ids[h * L + l] = id;
-                if (id >= 0) {
-                    mine[h] = held[((g * L) + id / V) * kPitch + id % V];
-                    atomicAdd(&hist[id], 1u);
+                ids[h * L + l] = id[h];
+                if (id[h] >= 0) {
+                    mine[h] = score_of(one_logit(a.logits, at + id[h], a.dtype), r.base, sigmoid);
+                    atomicAdd(&hist[id[h]], 1u);
                 }
             }
             chosen += mine[h];
         }
-        chosen = group_sum<L>(chosen);
         // a NaN among the token's logits reaches its weights wherever it was chosen
-        const float factor = total != total ? total : a.normalize ? (chosen > 0.0f ? a.scale / chosen : chosen == 0.0f ? 0.0f : chosen) : a.scale * back;
+        float factor = a.scale * r.back;
+        if (a.normalize) factor = a.scale * share_of(group_sum<L>(chosen));
+        if (r.total != r.total) factor = r.total;
 #pragma unroll
         for (int h = 0; h < 64 / L; ++h)
             if (h * L + l < a.topk) weights[h * L + l] = mine[h] * factor;
-        wave_sees();
     }
     __syncthreads();
     if (live) atomicAdd(&live_tokens, live);
 #pragma unroll
-    for (int j = 0; j < V; ++j) held[g * (L * V) + e0 + j] = sums[j];
+    for (int j = 0; j < V; ++j) held[g * (L * V) + l * V + j] = sums[j];
     __syncthreads();
+    const bool alone = gridDim.x == 1;  // nothing is left to add up
+    double dot = 0.0;
     for (uint32_t e = tid; e < a.experts; e += 256) {
         float s = 0.0f;
         for (uint32_t q = 0; q < G; ++q) s += held[q * (L * V) + e];
-        a.part_sums[(uint64_t)blockIdx.x * a.experts + e] = s;
-        a.part_counts[(uint64_t)blockIdx.x * a.experts + e] = hist[e];
+        if (alone) {
+            a.sums[e] = s;
+            a.counts[e] = (int32_t)hist[e];
+            dot += (double)s * hist[e];
+        } else {
+            a.part_sums[(uint64_t)blockIdx.x * a.experts + e] = s;
+            a.part_counts[(uint64_t)blockIdx.x * a.experts + e] = hist[e];
+        }
     }
-    if (tid == 0) a.part_live[blockIdx.x] = live_tokens;
+    if (alone) {
+        dot = workgroup_sum(dot, shared);
+        if (tid == 0) {
+            *a.counted = (int32_t)live_tokens;
+            *a.loss = loss_of(a, dot, live_tokens);
+        }
+    } else if (tid == 0) {
+        a.part_live[blockIdx.x] = live_tokens;
+    }
 }
 
 // Sums of what the workgroups of `choose` left, 16 experts a workgroup, and by
 // the last of them the loss.
 __global__ __launch_bounds__(256) void finish_choice(ChooseArgs a, uint32_t parts) {
-    __shared__ double sum[256];
+    __shared__ double sum[256], shared[4];
     __shared__ uint32_t count[256], last;
     const uint32_t c = threadIdx.x & 15, first = threadIdx.x >> 4, e = blockIdx.x * 16 + c;
     double s = 0.0;
     uint32_t n = 0;
-    if (e < a.experts)
+    if (e < a.experts) {
+#pragma unroll 8
         for (uint32_t q = first; q < parts; q += 16) {
             s += a.part_sums[(uint64_t)q * a.experts + e];
             n += a.part_counts[(uint64_t)q * a.experts + e];
         }
+    }
     sum[threadIdx.x] = s;
     count[threadIdx.x] = n;
     __syncthreads();
@@ -224,8 +438,7 @@ __global__ __launch_bounds__(256) void finish_choice(ChooseArgs a, uint32_t part
             a.sums[e] = (float)s;
             a.counts[e] = (int32_t)n;
         }
-        double dot = s * n;
-        for (int d = 1; d < 16; d <<= 1) dot += __shfl_xor(dot, d);
+        const double dot = group_sum<16>(s * n);
         if (threadIdx.x == 0) {
             __hip_atomic_store(&a.dots[blockIdx.x], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             last = __hip_atomic_fetch_add(a.arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
@@ -233,126 +446,155 @@ __global__ __launch_bounds__(256) void finish_choice(ChooseArgs a, uint32_t part
     }
     __syncthreads();
     if (!last) return;
-    uint32_t live = 0;
+    double live = 0.0;  // whole numbers below 2^31
     for (uint32_t q = threadIdx.x; q < parts; q += 256) live += a.part_live[q];
-    count[threadIdx.x] = live;
-    __syncthreads();
+    live = workgroup_sum(live, shared);
     if (threadIdx.x == 0) {
         double dot = 0.0;
         for (uint32_t q = 0; q < gridDim.x; ++q) dot += __hip_atomic_load(&a.dots[q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        live = 0;
-        for (uint32_t q = 0; q < 256; ++q) live += count[q];
         *a.counted = (int32_t)live;
-        const double t = (double)live;
-        *a.loss = live ? (float)((double)a.balance * a.experts * dot / ((double)a.topk * t * t)) : 0.0f;
+        *a.loss = loss_of(a, dot, (uint32_t)live);
     }
 }
 
-template <typename T, int L, int V, bool SIGMOID>
+template <typename T, int V>
+__device__ __forceinline__ void store_as(T* p, const float (&d)[V], int32_t left) {
+    constexpr int kWord = 16 / sizeof(T), kEach = kWord < V ? kWord : V;
+    typedef xu32x4 __attribute__((aligned(2))) Word;
+    typedef xu32x2 __attribute__((aligned(2))) Half;
+    T v[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = (T)d[j];
+    if (left >= V) {
+#pragma unroll
+        for (int j = 0; j < V; j += kEach) {
+            if constexpr (kEach * sizeof(T) == 16) {
+                xu32x4 w;
+                __builtin_memcpy(&w, v + j, 16);
+                *reinterpret_cast<Word*>(p + j) = w;
+            } else {
+                xu32x2 w;
+                __builtin_memcpy(&w, v + j, 8);
+                *reinterpret_cast<Half*>(p + j) = w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j < left) p[j] = v[j];
+    }
+}
+
+template <int L, int V>
 __global__ __launch_bounds__(256) void choose_backward(ChooseGradArgs a) {
     constexpr uint32_t G = 256 / L;
-    constexpr int kPitch = V + 4;
+    constexpr int kPitch = V + 4;  // lanes' runs begin in different banks
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
     __shared__ __align__(16) float held[256 * kPitch];
-    const uint32_t tid = threadIdx.x, l = tid % L, g = tid / L, e0 = l * V;
+    const uint32_t tid = threadIdx.x, l = tid % L, g = tid / L;
+    const bool sigmoid = a.sigmoid;
+    float* mine_held = held + tid * kPitch;
+    auto place = [&](uint32_t id) { return held + (g * L + id / V) * kPitch + id % V; };
     // the loss's gradient for p, the same for every token
     float of_loss[V];
     {
         const double n = (double)*a.counted;
         const double f = n > 0.0 ? (double)a.balance * a.experts * (a.dloss ? (double)*a.dloss : 1.0) / ((double)a.topk * n * n) : 0.0;
 #pragma unroll
-        for (int j = 0; j < V; ++j) of_loss[j] = e0 + j < a.experts ? (float)(f * a.counts[e0 + j]) : 0.0f;
+        for (int j = 0; j < V; ++j) of_loss[j] = l * V + j < a.experts ? (float)(f * a.counts[l * V + j]) : 0.0f;
     }
+#pragma unroll
+    for (int j = 0; j < V; j += 4) *reinterpret_cast<f32x4*>(mine_held + j) = f32x4{0, 0, 0, 0};
     for (uint32_t t = blockIdx.x * G + g; t < a.tokens; t += gridDim.x * G) {
-        T* out = static_cast<T*>(a.dlogits) + t * a.out_stride;
+        const uint64_t at = t * a.stride;
+        const uint32_t e0 = anew(l * V);
+        const int32_t left = (int32_t)a.experts - (int32_t)e0;
         float d[V];
         if (a.mask && !a.mask[t]) {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (e0 + j < a.experts) out[e0 + j] = (T)0.0f;
-            continue;
-        }
-        const T* row = static_cast<const T*>(a.logits) + t * a.stride;
-        float x[V], s[V], total;
-        load_logits<T, V>(row, e0, a.experts, x);
-        const float back = scores<V, L, SIGMOID>(x, s, total);
-#pragma unroll
-        for (int j = 0; j < V; ++j) held[tid * kPitch + j] = s[j];
-        wave_sees();
-        // the chosen: scores, and the weights' gradient
-        float mine[64 / L], dw[64 / L], chosen = 0.0f, both = 0.0f;
-        int32_t id[64 / L];
-#pragma unroll
-        for (int h = 0; h < 64 / L; ++h) {
-            const uint32_t k = h * L + l;
-            id[h] = a.dweights && k < a.topk ? a.ids[(uint64_t)t * a.topk + k] : -1;
-            if ((uint32_t)id[h] >= a.experts) id[h] = -1;
-            mine[h] = id[h] >= 0 ? held[((g * L) + id[h] / V) * kPitch + id[h] % V] : 0.0f;
-            dw[h] = id[h] >= 0 ? a.dweights[(uint64_t)t * a.topk + k] * a.scale : 0.0f;
-            chosen += mine[h];
-            both += mine[h] * dw[h];
-        }
-        wave_sees();
-        chosen = group_sum<L>(chosen);
-        both = group_sum<L>(both);
-#pragma unroll
-        for (int j = 0; j < V; ++j) held[tid * kPitch + j] = 0.0f;
-        wave_sees();
-        // by way of the weights, for s as it is held here
-        const float inv = chosen > 0.0f ? 1.0f / chosen : chosen == 0.0f ? 0.0f : chosen;
-#pragma unroll
-        for (int h = 0; h < 64 / L; ++h)
-            if (id[h] >= 0) held[((g * L) + id[h] / V) * kPitch + id[h] % V] = a.normalize ? (dw[h] - both * inv) * inv : dw[h] * back;
-        wave_sees();
-        const float part = total > 0.0f ? 1.0f / total : total == 0.0f ? 0.0f : total;
-        float dot = 0.0f;
-        if (SIGMOID) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) dot += of_loss[j] * s[j];
-            dot = group_sum<L>(dot) * part;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float up = held[tid * kPitch + j] + (of_loss[j] - dot) * part;
-                d[j] = up * s[j] * (1.0f / (1.0f + expf(x[j])));
-            }
+            for (int j = 0; j < V; ++j) d[j] = 0.0f;
         } else {
-            // d / d p: what is held is for s = p * total
+            float x[V], s[V];
+            load_logits<V>(a.logits, at, a.dtype, e0, a.experts, x);
+            int32_t id[64 / L];
+            float of_choice[64 / L], dw[64 / L];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                d[j] = held[tid * kPitch + j] * total + of_loss[j];
-                dot += d[j] * s[j];
+            for (int h = 0; h < 64 / L; ++h) {
+                const uint32_t k = h * L + l;
+                id[h] = a.dweights && k < a.topk ? a.ids[(uint64_t)t * a.topk + k] : -1;
+                if ((uint32_t)id[h] >= a.experts) id[h] = -1;
+                of_choice[h] = id[h] >= 0 ? one_logit(a.logits, at + id[h], a.dtype) : 0.0f;
+                dw[h] = id[h] >= 0 ? a.dweights[(uint64_t)t * a.topk + k] * a.scale : 0.0f;
             }
-            dot = group_sum<L>(dot) * part;
+            const Scored r = scores<L, V>(x, s, sigmoid);
+            // d / d s of the chosen by way of the weights, for s as it is held here
+            float chosen = 0.0f, both = 0.0f;
+            if (a.normalize) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) d[j] = (d[j] - dot) * (s[j] * part);
+                for (int h = 0; h < 64 / L; ++h) {
+                    const float v = id[h] >= 0 ? score_of(of_choice[h], r.base, sigmoid) : 0.0f;
+                    chosen += v;
+                    both += v * dw[h];
+                }
+                chosen = share_of(group_sum<L>(chosen));
+                both = group_sum<L>(both) * chosen;
+            }
+#pragma unroll
+            for (int h = 0; h < 64 / L; ++h)
+                if (id[h] >= 0) *place(id[h]) = a.normalize ? (dw[h] - both) * chosen : dw[h] * r.back;
+            wave_sees();
+#pragma unroll
+            for (int j = 0; j < V; j += 4) {
+                const f32x4 w = *reinterpret_cast<const f32x4*>(mine_held + j);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) d[j + q] = w[q];
+            }
+            wave_sees();
+#pragma unroll
+            for (int h = 0; h < 64 / L; ++h)
+                if (id[h] >= 0) *place(id[h]) = 0.0f;  // as it was, for the next token
+            float dot = 0.0f;
+            if (sigmoid) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) dot += of_loss[j] * s[j];
+                dot = group_sum<L>(dot) * r.part;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    // 1 - sigmoid(x)
+                    const float u = exp_of(-fabsf(x[j])), down = inverse(1.0f + u);
+                    d[j] = (d[j] + (of_loss[j] - dot) * r.part) * s[j] * (x[j] > 0.0f ? u * down : down);
+                }
+            } else {
+                // d / d p: what is held is for s = p * total
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    d[j] = d[j] * r.total + of_loss[j];
+                    dot += d[j] * s[j];
+                }
+                dot = group_sum<L>(dot) * r.part;
+#pragma unroll
+                for (int j = 0; j < V; ++j) d[j] = (d[j] - dot) * (s[j] * r.part);
+            }
         }
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (e0 + j < a.experts) out[e0 + j] = (T)d[j];
-        wave_sees();
+        const uint64_t out = t * a.out_stride + e0;
+        if (a.dtype == ZC_BF16) store_as(static_cast<__bf16*>(a.dlogits) + out, d, left);
+        else if (a.dtype == ZC_FP16) store_as(static_cast<_Float16*>(a.dlogits) + out, d, left);
+        else store_as(static_cast<float*>(a.dlogits) + out, d, left);
     }
 }
 
-constexpr uint32_t kParts = 512;  // workgroups of a choice, at most
+constexpr uint32_t kParts = 1024;  // workgroups of a choice, at most
 
 uint32_t tokens_at_a_time(uint32_t experts) { return experts <= 256 ? 16 : experts <= 512 ? 8 : 4; }
 
-// f(T, L, V, SIGMOID) for what a call asks for.
+// f(L, V) for a number of experts.
 template <typename F>
-void with_shape(uint32_t dtype, uint32_t experts, bool sigmoid, F f) {
-    auto by_score = [&](auto t, auto l, auto v) {
-        if (sigmoid) f(t, l, v, std::true_type{});
-        else f(t, l, v, std::false_type{});
-    };
-    auto by_experts = [&](auto t) {
-        if (experts <= 64) by_score(t, std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
-        else if (experts <= 128) by_score(t, std::integral_constant<int, 16>{}, std::integral_constant<int, 8>{});
-        else if (experts <= 256) by_score(t, std::integral_constant<int, 16>{}, std::integral_constant<int, 16>{});
-        else if (experts <= 512) by_score(t, std::integral_constant<int, 32>{}, std::integral_constant<int, 16>{});
-        else by_score(t, std::integral_constant<int, 64>{}, std::integral_constant<int, 16>{});
-    };
-    if (dtype == ZC_BF16) by_experts((__bf16)0.0f);
-    else if (dtype == ZC_FP16) by_experts((_Float16)0.0f);
-    else by_experts(0.0f);
+void with_shape(uint32_t experts, F f) {
+    if (experts <= 64) f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
+    else if (experts <= 128) f(std::integral_constant<int, 16>{}, std::integral_constant<int, 8>{});
+    else if (experts <= 256) f(std::integral_constant<int, 16>{}, std::integral_constant<int, 16>{});
+    else if (experts <= 512) f(std::integral_constant<int, 32>{}, std::integral_constant<int, 16>{});
+    else f(std::integral_constant<int, 64>{}, std::integral_constant<int, 16>{});
 }
 
 }  // namespace
@@ -363,20 +605,21 @@ uint32_t choose_parts(uint64_t tokens, uint32_t experts) {
     return n < 1 ? 1 : n > kParts ? kParts : (uint32_t)n;
 }
 
-zc_status launch_choose(const ChooseArgs& a, uint32_t dtype, bool sigmoid, hipStream_t stream) {
+zc_status launch_choose(const ChooseArgs& a, hipStream_t stream) {
     const uint32_t parts = choose_parts(a.tokens, a.experts);
-    with_shape(dtype, a.experts, sigmoid, [&](auto t, auto l, auto v, auto score) {
-        hipLaunchKernelGGL((choose<decltype(t), l.value, v.value, score.value>), dim3(parts), dim3(256), 0, stream, a);
+    with_shape(a.experts, [&](auto l, auto v) {
+        constexpr int L = decltype(l)::value, V = decltype(v)::value, FEW = V < 8 ? V : 8;
+        if (a.topk <= 8) hipLaunchKernelGGL((choose<L, V, FEW>), dim3(parts), dim3(256), 0, stream, a);
+        else hipLaunchKernelGGL((choose<L, V, V>), dim3(parts), dim3(256), 0, stream, a);
     });
-    hipLaunchKernelGGL(finish_choice, dim3((a.experts + 15) / 16), dim3(256), 0, stream, a, parts);
+    if (parts > 1) hipLaunchKernelGGL(finish_choice, dim3((a.experts + 15) / 16), dim3(256), 0, stream, a, parts);
     return ZC_OK;
 }
 
-zc_status launch_choose_backward(const ChooseGradArgs& a, uint32_t dtype, bool sigmoid, hipStream_t stream) {
+zc_status launch_choose_backward(const ChooseGradArgs& a, hipStream_t stream) {
     const uint32_t g = tokens_at_a_time(a.experts), n = (a.tokens + g - 1) / g;
-    with_shape(dtype, a.experts, sigmoid, [&](auto t, auto l, auto v, auto score) {
-        hipLaunchKernelGGL((choose_backward<decltype(t), l.value, v.value, score.value>), dim3(n < 4096 ? n : 4096), dim3(256), 0,
-                           stream, a);
+    with_shape(a.experts, [&](auto l, auto v) {
+        hipLaunchKernelGGL((choose_backward<decltype(l)::value, decltype(v)::value>), dim3(n < 4096 ? n : 4096), dim3(256), 0, stream, a);
     });
     return ZC_OK;
 }

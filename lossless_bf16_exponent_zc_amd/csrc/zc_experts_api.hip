@@ -321,14 +321,14 @@ zc_status zc_choose(const void* d_logits, uint64_t stride, uint32_t dtype, uint6
     if (ws_bytes < zc_choose_workspace_bytes(tokens, topk, experts)) return ZC_ERR_CAPACITY;
     const uint64_t parts = choose_parts(tokens, experts);
     uint8_t* ws = static_cast<uint8_t*>(d_ws);
-    ChooseArgs a{d_logits, stride, d_bias, d_mask, (uint32_t)tokens, topk, experts, normalize ? 1u : 0u, scale, balance,
-                 d_ids, d_weights, d_counts, d_sums, d_counted, d_loss};
+    ChooseArgs a{d_logits, stride, d_bias, d_mask, dtype, (uint32_t)tokens, topk, experts, score == ZC_SIGMOID,
+                 normalize ? 1u : 0u, scale, balance, d_ids, d_weights, d_counts, d_sums, d_counted, d_loss};
     a.arrived = reinterpret_cast<uint32_t*>(ws);
     a.dots = reinterpret_cast<double*>(ws + kDotsAt);
     a.part_live = reinterpret_cast<uint32_t*>(ws + kDotsAt + kDots * 8);
     a.part_sums = reinterpret_cast<float*>(a.part_live + parts);
     a.part_counts = reinterpret_cast<uint32_t*>(a.part_sums + parts * experts);
-    return finished(launch_choose(a, dtype, score == ZC_SIGMOID, stream));
+    return finished(launch_choose(a, stream));
 }
 
 zc_status zc_choose_backward(const void* d_logits, uint64_t stride, uint32_t dtype, uint64_t tokens, uint32_t topk,
@@ -343,9 +343,9 @@ zc_status zc_choose_backward(const void* d_logits, uint64_t stride, uint32_t dty
     if (bad_matrix(d_logits, stride, experts, dtype) || bad_matrix(d_dlogits, dlogits_stride, experts, dtype) ||
         !aligned(d_dweights, 4) || (d_dweights && bad_words(d_ids)))
         return ZC_ERR_INVALID_ARG;
-    const ChooseGradArgs a{d_logits, stride, d_mask, (uint32_t)tokens, topk, experts, normalize ? 1u : 0u, scale, balance,
-                           d_ids, d_counts, d_counted, d_dweights, d_dloss, d_dlogits, dlogits_stride};
-    return finished(launch_choose_backward(a, dtype, score == ZC_SIGMOID, stream));
+    const ChooseGradArgs a{d_logits, stride, d_mask, dtype, (uint32_t)tokens, topk, experts, score == ZC_SIGMOID,
+                           normalize ? 1u : 0u, scale, balance, d_ids, d_counts, d_counted, d_dweights, d_dloss, d_dlogits, dlogits_stride};
+    return finished(launch_choose_backward(a, stream));
 }
 
 uint64_t zc_orthogonalize_workspace_bytes(uint32_t batch, uint32_t n, uint32_t k) { return orth_layout(batch, n, k).bytes; }

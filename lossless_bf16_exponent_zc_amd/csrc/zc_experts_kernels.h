@@ -101,8 +101,8 @@ struct ChooseArgs {
     uint64_t stride;         // elements
     const float* bias;       // or null
     const uint8_t* mask;     // or null: every token counts
-    uint32_t tokens, topk, experts;
-    uint32_t normalize;
+    uint32_t dtype, tokens, topk, experts;
+    uint32_t sigmoid, normalize;
     float scale, balance;
     int32_t* ids;
     float* weights;
@@ -122,8 +122,8 @@ struct ChooseGradArgs {
     const void* logits;
     uint64_t stride;         // elements
     const uint8_t* mask;     // or null
-    uint32_t tokens, topk, experts;
-    uint32_t normalize;
+    uint32_t dtype, tokens, topk, experts;
+    uint32_t sigmoid, normalize;
     float scale, balance;
     const int32_t* ids;
     const int32_t* counts;
@@ -181,8 +181,8 @@ zc_status launch_product(const ProductArgs& a, hipStream_t stream);
 zc_status launch_weight_grad(const WeightGradArgs& a, const WeightGradPlan& plan, void* ws, hipStream_t stream);
 
 uint32_t choose_parts(uint64_t tokens, uint32_t experts);  // workgroups of the first kernel
-zc_status launch_choose(const ChooseArgs& a, uint32_t dtype, bool sigmoid, hipStream_t stream);
-zc_status launch_choose_backward(const ChooseGradArgs& a, uint32_t dtype, bool sigmoid, hipStream_t stream);
+zc_status launch_choose(const ChooseArgs& a, hipStream_t stream);
+zc_status launch_choose_backward(const ChooseGradArgs& a, hipStream_t stream);
 
 zc_status launch_orthogonalize(OrthArgs a, uint32_t dtype, uint32_t steps, hipStream_t stream);
 
