@@ -89,30 +89,40 @@ __device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf
 __device__ __forceinline__ float share_of(float x) { return x == 0.0f ? 0.0f : inverse(x); }
 
 template <typename T, int V>
-__device__ __forceinline__ void load_as(const T* row, uint32_t e0, uint32_t experts, float (&x)[V]) {
+__device__ __forceinline__ void load_as(const T* row, uint32_t e0, uint32_t experts, bool whole, float (&x)[V]) {
+    typedef xu32x4 __attribute__((aligned(2))) Four;
+    typedef xu32x2 __attribute__((aligned(2))) Two;
     constexpr int kWord = 16 / sizeof(T), kEach = kWord < V ? kWord : V;
     const int32_t left = (int32_t)experts - (int32_t)e0;
 #pragma unroll
     for (int j = 0; j < V; j += kEach) {
         T v[kWord];
-        const xu32x4 w = load_word(row + (left > j ? e0 + j : 0), left - j < kEach ? left - j : kEach);
+        xu32x4 w{};
+        if (!whole) {
+            w = load_word(row + (left > j ? e0 + j : 0), left - j < kEach ? left - j : kEach);
+        } else if constexpr (kEach == kWord) {
+            w = *reinterpret_cast<const Four*>(row + e0 + j);
+        } else {
+            const xu32x2 h = *reinterpret_cast<const Two*>(row + e0 + j);
+            w = xu32x4{h[0], h[1], 0, 0};
+        }
         __builtin_memcpy(v, &w, 16);
 #pragma unroll
         for (int q = 0; q < kEach; ++q) x[j + q] = to_float(v[q]);
     }
-    if (left < V) {
+    if (!whole) {
 #pragma unroll
         for (int j = 0; j < V; ++j) x[j] = j < left ? x[j] : -kInf;
     }
 }
 
-// V logits of a lane, -inf past the last expert.
+// V logits of a lane, -inf past the last expert.  whole: no lane has one.
 template <int V>
 __device__ __forceinline__ void load_logits(const void* logits, uint64_t at, uint32_t dtype, uint32_t e0, uint32_t experts,
-                                            float (&x)[V]) {
-    if (dtype == ZC_BF16) load_as(static_cast<const __bf16*>(logits) + at, e0, experts, x);
-    else if (dtype == ZC_FP16) load_as(static_cast<const _Float16*>(logits) + at, e0, experts, x);
-    else load_as(static_cast<const float*>(logits) + at, e0, experts, x);
+                                            bool whole, float (&x)[V]) {
+    if (dtype == ZC_BF16) load_as(static_cast<const __bf16*>(logits) + at, e0, experts, whole, x);
+    else if (dtype == ZC_FP16) load_as(static_cast<const _Float16*>(logits) + at, e0, experts, whole, x);
+    else load_as(static_cast<const float*>(logits) + at, e0, experts, whole, x);
 }
 __device__ __forceinline__ float one_logit(const void* logits, uint64_t at, uint32_t dtype) {
     if (dtype == ZC_BF16) return to_float(static_cast<const __bf16*>(logits)[at]);
@@ -124,11 +134,14 @@ __device__ __forceinline__ float one_logit(const void* logits, uint64_t at, uint
 // largest; sigmoid e^(x - base) / (1 + e^x), base = min(largest, 0), so that the
 // largest neither overflows nor underflows.  The score itself is s * back.
 // Infinite or NaN logits but -inf make softmax's NaN.
-__device__ __forceinline__ float score_of(float x, float base, bool sigmoid) {
-    if (!sigmoid) return exp_of(x - base);
+__device__ __forceinline__ float sigmoid_of(float x) {
     const float t = exp_of(-fabsf(x)), down = inverse(1.0f + t);
-    if (base < 0.0f) return exp_of(x - base) * down;  // every x is below 0
-    return x < 0.0f ? t * down : x >= 0.0f ? down : x;
+    return (x < 0.0f ? t : 1.0f) * down;
+}
+// the same times e^-base, every x being below 0
+__device__ __forceinline__ float low_sigmoid_of(float x, float base) { return exp_of(x - base) * inverse(1.0f + exp_of(x)); }
+__device__ __forceinline__ float score_of(float x, float base, bool sigmoid) {
+    return !sigmoid ? exp_of(x - base) : base < 0.0f ? low_sigmoid_of(x, base) : sigmoid_of(x);
 }
 
 struct Scored {
@@ -143,11 +156,19 @@ __device__ __forceinline__ Scored scores(const float (&x)[V], float (&s)[V], boo
     Scored r;
     r.base = top == -kInf || (sigmoid && top > 0.0f) ? 0.0f : top;
     float sum = 0.0f;
+    if (!sigmoid) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        s[j] = score_of(x[j], r.base, sigmoid);
-        sum += s[j];
+        for (int j = 0; j < V; ++j) s[j] = exp_of(x[j] - r.base);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] = sigmoid_of(x[j]);
+        if (r.base < 0.0f) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] = low_sigmoid_of(x[j], r.base);
+        }
     }
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum += s[j];
     r.total = group_sum<L>(sum);
     r.part = share_of(r.total);
     r.back = sigmoid ? exp_of(r.base) : r.part;
@@ -223,38 +244,49 @@ __device__ __forceinline__ void best_of(double (&k)[V], double (&best)[D]) {
 }
 
 // Scores with a bias, compared in 64 bits one choice after the other: the way
-// for the few tokens whose scores 32 bits do not tell apart.
+// for the few tokens whose scores 32 bits do not tell apart.  The exponentials
+// go one after the other, by way of LDS (a lane's values 256 apart): side by
+// side they would take all registers.
 template <int L, int V>
-__device__ __forceinline__ void choose_exactly(const ChooseArgs& a, uint64_t at, uint32_t e0, uint32_t l, int32_t (&ids)[64 / L]) {
+__device__ __forceinline__ void choose_exactly(const ChooseArgs& a, uint64_t at, uint32_t e0, uint32_t l, double* keys,
+                                               int32_t (&ids)[64 / L]) {
     float x[V];
-    load_logits<V>(a.logits, at, a.dtype, e0, a.experts, x);
-    double key[V], sum = 0.0;
+    load_logits<V>(a.logits, at, a.dtype, e0, a.experts, a.experts == L * V, x);
     float top = -kInf;
-#pragma unroll
-    for (int j = 0; j < V; ++j) top = fmaxf(top, x[j]);
-    top = group_max<L>(top);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        key[j] = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x[j])) : exp((double)x[j] - (double)top);
-        sum += key[j];
-        __builtin_amdgcn_sched_barrier(0);  // one after the other: side by side they take all registers
-    }
-    sum = group_sum<L>(sum);
     uint32_t open = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        key[j] = (a.sigmoid ? key[j] : key[j] / sum) + (e0 + j < a.experts ? (double)a.bias[e0 + j] : 0.0);
-        __builtin_amdgcn_sched_barrier(0);
-        if (x[j] > -kInf && key[j] > -(double)kInf) open |= 1u << j;  // neither closed nor NaN
+        top = fmaxf(top, x[j]);
+        keys[j * 256] = (double)x[j];
+        if (x[j] > -kInf) open |= 1u << j;  // neither closed nor NaN
     }
+    top = group_max<L>(top);
+    double sum = 0.0;
+#pragma unroll 1
+    for (int j = 0; j < V; ++j) {
+        const double v = keys[j * 256], e = exp(a.sigmoid ? -v : v - (double)top), score = a.sigmoid ? 1.0 / (1.0 + e) : e;
+        keys[j * 256] = score;
+        sum += score;
+    }
+    sum = group_sum<L>(sum);
+#pragma unroll 1
+    for (int j = 0; j < V; ++j) {
+        const double v = (a.sigmoid ? keys[j * 256] : keys[j * 256] / sum) + (e0 + j < a.experts ? (double)a.bias[e0 + j] : 0.0);
+        keys[j * 256] = v;
+        if (!(v > -(double)kInf)) open &= ~(1u << j);
+    }
+    double key[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) key[j] = keys[j * 256];
 #pragma unroll
     for (int h = 0; h < 64 / L; ++h) ids[h] = -1;
+#pragma unroll 1
     for (uint32_t k = 0; k < a.topk; ++k) {
-        double best = 0.0;
+        double best = -(double)kInf;
         uint32_t of = ~0u;
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if ((open >> j & 1) && (of == ~0u || key[j] > best)) {
+            if ((open >> j & 1) && key[j] > best) {
                 best = key[j];
                 of = e0 + j;
             }
@@ -262,7 +294,7 @@ __device__ __forceinline__ void choose_exactly(const ChooseArgs& a, uint64_t at,
         for (int d = 1; d < L; d <<= 1) {
             const double other = __shfl_xor(best, d);
             const uint32_t other_of = __shfl_xor(of, d);
-            if (other_of != ~0u && (of == ~0u || other > best || (other == best && other_of < of))) {
+            if (other > best || (other == best && other_of < of)) {
                 best = other;
                 of = other_of;
             }
@@ -291,9 +323,9 @@ __device__ __forceinline__ float loss_of(const ChooseArgs& a, double dot, uint32
 
 // D: choices that one lane may have to give, at most.
 template <int L, int V, int D>
-__global__ __launch_bounds__(256) void choose(ChooseArgs a) {
+__global__ __launch_bounds__(256, D > 8 ? 2 : 3) void choose(ChooseArgs a) {
     constexpr uint32_t G = 256 / L;  // tokens at a time
-    __shared__ float held[256 * V];
+    __shared__ double keys_in_lds[256 * V];  // choose_exactly's; at the end, the sums
     __shared__ uint32_t hist[kMaxExperts];
     __shared__ uint32_t live_tokens;
     __shared__ double shared[4];
@@ -303,6 +335,7 @@ __global__ __launch_bounds__(256) void choose(ChooseArgs a) {
     if (blockIdx.x == 0 && tid == 0) *a.arrived = 0;
     __syncthreads();
     const bool sigmoid = a.sigmoid;
+    float* const held = reinterpret_cast<float*>(keys_in_lds);
     float sums[V], bias[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -324,15 +357,17 @@ __global__ __launch_bounds__(256) void choose(ChooseArgs a) {
         const uint64_t at = t * a.stride;
         const uint32_t e0 = anew(l * V);
         float x[V], s[V];
-        load_logits<V>(a.logits, at, a.dtype, e0, a.experts, x);
+        load_logits<V>(a.logits, at, a.dtype, e0, a.experts, a.experts == L * V, x);
         const Scored r = scores<L, V>(x, s, sigmoid);
         double keys[V], best[D];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            sums[j] += s[j] * r.part;
-            const float v = !a.bias ? x[j] : x[j] > -kInf ? s[j] * r.back + bias[j] : -kInf;
-            keys[j] = key_of(v, e0 + j);
+        for (int j = 0; j < V; ++j) sums[j] += s[j] * r.part;
+        if (a.bias) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] = x[j] > -kInf ? s[j] * r.back + bias[j] : -kInf;
         }
+#pragma unroll
+        for (int j = 0; j < V; ++j) keys[j] = key_of(x[j], e0 + j);
         best_of<V, D>(keys, best);
         // the group's best, again and again; the lane that had it moves up
         int32_t id[64 / L];
@@ -341,13 +376,14 @@ __global__ __launch_bounds__(256) void choose(ChooseArgs a) {
 #pragma unroll
         for (int h = 0; h < 64 / L; ++h) {
             id[h] = -1;
-            if (h * L >= (int)a.topk + 1) break;
-            for (uint32_t q = 0; q < L && h * L + q <= a.topk; ++q) {
+            const uint32_t rounds = a.topk + (a.bias ? 1 : 0);  // with a bias, the first one not chosen too
+            for (uint32_t q = 0; q < L && h * L + q < rounds; ++q) {
                 const double top = over_group<L>(best[0], larger);
-                // 32-bit scores are off by less than 2^-19 of 1 or of the bias
+                // 32-bit scores are off by at most 6 units of 2^-24 (of softmax's,
+                // past the sum that all share), sums with the bias by one of theirs
                 if (a.bias && before > kClosed) {
                     const double v = value_of(top), gap = value_of(before) - v;
-                    unsure |= !(gap > 0x1p-18 * (1.0 + fabs(v)));
+                    unsure |= !(gap > 0x1p-20 * (1.0 + fabs(v)));
                 }
                 before = top;
                 if (h * L + q == a.topk) break;
@@ -359,7 +395,7 @@ __global__ __launch_bounds__(256) void choose(ChooseArgs a) {
                 }
             }
         }
-        if (unsure) choose_exactly<L, V>(a, at, e0, l, id);
+        if (unsure) choose_exactly<L, V>(a, at, e0, l, keys_in_lds + tid, id);
         float mine[64 / L], chosen = 0.0f;
 #pragma unroll
         for (int h = 0; h < 64 / L; ++h) {
@@ -411,17 +447,20 @@ __global__ __launch_bounds__(256) void choose(ChooseArgs a) {
     }
 }
 
-// Sums of what the workgroups of `choose` left, 16 experts a workgroup, and by
-// the last of them the loss.
+// Sums of what the workgroups of `choose` left, kOf experts a workgroup, and by
+// the last of them the loss.  Its time is that of one round trip to memory, as
+// long as there are enough workgroups: 8192 tokens, 256 experts, 512 parts:
+// with 16 experts each 7.3 us.
+constexpr uint32_t kOf = 8;
 __global__ __launch_bounds__(256) void finish_choice(ChooseArgs a, uint32_t parts) {
     __shared__ double sum[256], shared[4];
     __shared__ uint32_t count[256], last;
-    const uint32_t c = threadIdx.x & 15, first = threadIdx.x >> 4, e = blockIdx.x * 16 + c;
+    const uint32_t c = threadIdx.x % kOf, first = threadIdx.x / kOf, e = blockIdx.x * kOf + c;
     double s = 0.0;
     uint32_t n = 0;
     if (e < a.experts) {
-#pragma unroll 8
-        for (uint32_t q = first; q < parts; q += 16) {
+#pragma unroll 16
+        for (uint32_t q = first; q < parts; q += 256 / kOf) {
             s += a.part_sums[(uint64_t)q * a.experts + e];
             n += a.part_counts[(uint64_t)q * a.experts + e];
         }
@@ -429,16 +468,21 @@ __global__ __launch_bounds__(256) void finish_choice(ChooseArgs a, uint32_t part
     sum[threadIdx.x] = s;
     count[threadIdx.x] = n;
     __syncthreads();
-    if (threadIdx.x < 16) {
-        for (uint32_t q = 1; q < 16; ++q) {
-            s += sum[q * 16 + c];
-            n += count[q * 16 + c];
+    if (threadIdx.x < 64) {  // of four parts of each sum, then of eight lanes
+        for (uint32_t q = 1; q < 4; ++q) {
+            s += sum[q * 64 + threadIdx.x];
+            n += count[q * 64 + threadIdx.x];
         }
-        if (e < a.experts) {
+#pragma unroll
+        for (int d = kOf; d < 64; d <<= 1) {
+            s += __shfl_xor(s, d);
+            n += __shfl_xor(n, d);
+        }
+        if (threadIdx.x < kOf && e < a.experts) {
             a.sums[e] = (float)s;
             a.counts[e] = (int32_t)n;
         }
-        const double dot = group_sum<16>(s * n);
+        const double dot = group_sum<kOf>(s * n);
         if (threadIdx.x == 0) {
             __hip_atomic_store(&a.dots[blockIdx.x], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             last = __hip_atomic_fetch_add(a.arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
@@ -448,14 +492,16 @@ __global__ __launch_bounds__(256) void finish_choice(ChooseArgs a, uint32_t part
     if (!last) return;
     double live = 0.0;  // whole numbers below 2^31
     for (uint32_t q = threadIdx.x; q < parts; q += 256) live += a.part_live[q];
+    double dot = 0.0;
+    if (threadIdx.x < gridDim.x) dot = __hip_atomic_load(&a.dots[threadIdx.x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     live = workgroup_sum(live, shared);
+    dot = workgroup_sum(dot, shared);
     if (threadIdx.x == 0) {
-        double dot = 0.0;
-        for (uint32_t q = 0; q < gridDim.x; ++q) dot += __hip_atomic_load(&a.dots[q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         *a.counted = (int32_t)live;
         *a.loss = loss_of(a, dot, (uint32_t)live);
     }
 }
+static_assert(kMaxExperts / kOf <= 256, "one thread per workgroup");
 
 template <typename T, int V>
 __device__ __forceinline__ void store_as(T* p, const float (&d)[V], int32_t left) {
@@ -486,15 +532,14 @@ __device__ __forceinline__ void store_as(T* p, const float (&d)[V], int32_t left
 }
 
 template <int L, int V>
-__global__ __launch_bounds__(256) void choose_backward(ChooseGradArgs a) {
-    constexpr uint32_t G = 256 / L;
+__global__ __launch_bounds__(256, 4) void choose_backward(ChooseGradArgs a) {
+    constexpr uint32_t G = 256 / L, H = 64 / L;
     constexpr int kPitch = V + 4;  // lanes' runs begin in different banks
     typedef float f32x4 __attribute__((ext_vector_type(4)));
-    __shared__ __align__(16) float held[256 * kPitch];
+    __shared__ __align__(16) float held[256 * kPitch], given[256 * kPitch];  // scores; what comes by way of the weights
     const uint32_t tid = threadIdx.x, l = tid % L, g = tid / L;
     const bool sigmoid = a.sigmoid;
-    float* mine_held = held + tid * kPitch;
-    auto place = [&](uint32_t id) { return held + (g * L + id / V) * kPitch + id % V; };
+    auto place = [&](uint32_t id) { return (g * L + id / V) * kPitch + id % V; };
     // the loss's gradient for p, the same for every token
     float of_loss[V];
     {
@@ -504,77 +549,80 @@ __global__ __launch_bounds__(256) void choose_backward(ChooseGradArgs a) {
         for (int j = 0; j < V; ++j) of_loss[j] = l * V + j < a.experts ? (float)(f * a.counts[l * V + j]) : 0.0f;
     }
 #pragma unroll
-    for (int j = 0; j < V; j += 4) *reinterpret_cast<f32x4*>(mine_held + j) = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < V; j += 4) *reinterpret_cast<f32x4*>(given + tid * kPitch + j) = f32x4{0, 0, 0, 0};
     for (uint32_t t = blockIdx.x * G + g; t < a.tokens; t += gridDim.x * G) {
-        const uint64_t at = t * a.stride;
         const uint32_t e0 = anew(l * V);
         const int32_t left = (int32_t)a.experts - (int32_t)e0;
-        float d[V];
-        if (a.mask && !a.mask[t]) {
+        // all that is read of a token is asked for at once
+        float x[V], s[V], d[V], dw[H];
+        int32_t id[H];
+        load_logits<V>(a.logits, t * a.stride, a.dtype, e0, a.experts, a.experts == L * V, x);
+#pragma unroll
+        for (int h = 0; h < (int)H; ++h) {
+            const uint32_t k = h * L + l;
+            id[h] = a.dweights && k < a.topk ? a.ids[(uint64_t)t * a.topk + k] : -1;
+            dw[h] = a.dweights && k < a.topk ? a.dweights[(uint64_t)t * a.topk + k] * a.scale : 0.0f;
+        }
+        const bool live = !a.mask || a.mask[t];
+        const Scored r = scores<L, V>(x, s, sigmoid);
+#pragma unroll
+        for (int j = 0; j < V; j += 4) *reinterpret_cast<f32x4*>(held + tid * kPitch + j) = f32x4{s[j], s[j + 1], s[j + 2], s[j + 3]};
+        wave_sees();
+        // d / d s of the chosen by way of the weights, for s as it is held here
+        float chosen = 0.0f, both = 0.0f;
+#pragma unroll
+        for (int h = 0; h < (int)H; ++h) {
+            if ((uint32_t)id[h] >= a.experts) id[h] = -1;
+            if (id[h] < 0) dw[h] = 0.0f;
+            if (a.normalize && id[h] >= 0) {
+                const float v = held[place(id[h])];
+                chosen += v;
+                both += v * dw[h];
+            }
+        }
+        if (a.normalize) {
+            chosen = share_of(group_sum<L>(chosen));
+            both = group_sum<L>(both) * chosen;
+        }
+#pragma unroll
+        for (int h = 0; h < (int)H; ++h)
+            if (id[h] >= 0) given[place(id[h])] = a.normalize ? (dw[h] - both) * chosen : dw[h] * r.back;
+        wave_sees();
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            const f32x4 w = *reinterpret_cast<const f32x4*>(given + tid * kPitch + j);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) d[j + q] = w[q];
+        }
+        wave_sees();
+#pragma unroll
+        for (int h = 0; h < (int)H; ++h)
+            if (id[h] >= 0) given[place(id[h])] = 0.0f;  // as it was, for the next token
+        float dot = 0.0f;
+        if (sigmoid) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) dot += of_loss[j] * s[j];
+            dot = group_sum<L>(dot) * r.part;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                // 1 - sigmoid(x)
+                const float u = exp_of(-fabsf(x[j])), down = inverse(1.0f + u);
+                d[j] = (d[j] + (of_loss[j] - dot) * r.part) * s[j] * (x[j] > 0.0f ? u * down : down);
+            }
+        } else {
+            // d / d p: what is given is for s = p * total
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                d[j] = d[j] * r.total + of_loss[j];
+                dot += d[j] * s[j];
+            }
+            dot = group_sum<L>(dot) * r.part;
+#pragma unroll
+            for (int j = 0; j < V; ++j) d[j] = (d[j] - dot) * (s[j] * r.part);
+        }
+        if (!live) {
 #pragma unroll
             for (int j = 0; j < V; ++j) d[j] = 0.0f;
-        } else {
-            float x[V], s[V];
-            load_logits<V>(a.logits, at, a.dtype, e0, a.experts, x);
-            int32_t id[64 / L];
-            float of_choice[64 / L], dw[64 / L];
-#pragma unroll
-            for (int h = 0; h < 64 / L; ++h) {
-                const uint32_t k = h * L + l;
-                id[h] = a.dweights && k < a.topk ? a.ids[(uint64_t)t * a.topk + k] : -1;
-                if ((uint32_t)id[h] >= a.experts) id[h] = -1;
-                of_choice[h] = id[h] >= 0 ? one_logit(a.logits, at + id[h], a.dtype) : 0.0f;
-                dw[h] = id[h] >= 0 ? a.dweights[(uint64_t)t * a.topk + k] * a.scale : 0.0f;
-            }
-            const Scored r = scores<L, V>(x, s, sigmoid);
-            // d / d s of the chosen by way of the weights, for s as it is held here
-            float chosen = 0.0f, both = 0.0f;
-            if (a.normalize) {
-#pragma unroll
-                for (int h = 0; h < 64 / L; ++h) {
-                    const float v = id[h] >= 0 ? score_of(of_choice[h], r.base, sigmoid) : 0.0f;
-                    chosen += v;
-                    both += v * dw[h];
-                }
-                chosen = share_of(group_sum<L>(chosen));
-                both = group_sum<L>(both) * chosen;
-            }
-#pragma unroll
-            for (int h = 0; h < 64 / L; ++h)
-                if (id[h] >= 0) *place(id[h]) = a.normalize ? (dw[h] - both) * chosen : dw[h] * r.back;
-            wave_sees();
-#pragma unroll
-            for (int j = 0; j < V; j += 4) {
-                const f32x4 w = *reinterpret_cast<const f32x4*>(mine_held + j);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) d[j + q] = w[q];
-            }
-            wave_sees();
-#pragma unroll
-            for (int h = 0; h < 64 / L; ++h)
-                if (id[h] >= 0) *place(id[h]) = 0.0f;  // as it was, for the next token
-            float dot = 0.0f;
-            if (sigmoid) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) dot += of_loss[j] * s[j];
-                dot = group_sum<L>(dot) * r.part;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    // 1 - sigmoid(x)
-                    const float u = exp_of(-fabsf(x[j])), down = inverse(1.0f + u);
-                    d[j] = (d[j] + (of_loss[j] - dot) * r.part) * s[j] * (x[j] > 0.0f ? u * down : down);
-                }
-            } else {
-                // d / d p: what is held is for s = p * total
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    d[j] = d[j] * r.total + of_loss[j];
-                    dot += d[j] * s[j];
-                }
-                dot = group_sum<L>(dot) * r.part;
-#pragma unroll
-                for (int j = 0; j < V; ++j) d[j] = (d[j] - dot) * (s[j] * r.part);
-            }
         }
         const uint64_t out = t * a.out_stride + e0;
         if (a.dtype == ZC_BF16) store_as(static_cast<__bf16*>(a.dlogits) + out, d, left);
@@ -583,7 +631,11 @@ __global__ __launch_bounds__(256) void choose_backward(ChooseGradArgs a) {
     }
 }
 
-constexpr uint32_t kParts = 1024;  // workgroups of a choice, at most
+// Workgroups of a choice, and of its gradient, at most: what the CUs hold at
+// once, which go on to the next tokens.  65,536 tokens on 256 experts, in us:
+// choices in 512 / 768 / 1024 workgroups 47/42/47, with a bias 73/61/68; gradients
+// in 1024 / 4096 27/44.
+constexpr uint32_t kParts = 768, kBackward = 1024;
 
 uint32_t tokens_at_a_time(uint32_t experts) { return experts <= 256 ? 16 : experts <= 512 ? 8 : 4; }
 
@@ -612,14 +664,14 @@ zc_status launch_choose(const ChooseArgs& a, hipStream_t stream) {
         if (a.topk <= 8) hipLaunchKernelGGL((choose<L, V, FEW>), dim3(parts), dim3(256), 0, stream, a);
         else hipLaunchKernelGGL((choose<L, V, V>), dim3(parts), dim3(256), 0, stream, a);
     });
-    if (parts > 1) hipLaunchKernelGGL(finish_choice, dim3((a.experts + 15) / 16), dim3(256), 0, stream, a, parts);
+    if (parts > 1) hipLaunchKernelGGL(finish_choice, dim3((a.experts + kOf - 1) / kOf), dim3(256), 0, stream, a, parts);
     return ZC_OK;
 }
 
 zc_status launch_choose_backward(const ChooseGradArgs& a, hipStream_t stream) {
     const uint32_t g = tokens_at_a_time(a.experts), n = (a.tokens + g - 1) / g;
     with_shape(a.experts, [&](auto l, auto v) {
-        hipLaunchKernelGGL((choose_backward<decltype(l)::value, decltype(v)::value>), dim3(n < 4096 ? n : 4096), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((choose_backward<decltype(l)::value, decltype(v)::value>), dim3(n < kBackward ? n : kBackward), dim3(256), 0, stream, a);
     });
     return ZC_OK;
 }

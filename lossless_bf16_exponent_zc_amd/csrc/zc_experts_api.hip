@@ -9,8 +9,8 @@ namespace {
 constexpr uint64_t kMaxRows = 0x7FFFFFFFull;
 constexpr uint32_t kMaxWidth = 1u << 24;
 constexpr uint32_t kMaxBatch = 65535, kMaxSide = 1u << 16, kMaxSteps = 64;  // of an update
-constexpr uint64_t kDotsAt = 256, kDots = 64;  // in a choice's workspace: one double per 16 experts
-static_assert(kMaxExperts <= 16 * kDots, "one double per 16 experts");
+constexpr uint64_t kDotsAt = 256, kDots = 128;  // in a choice's workspace: one double per 8 experts
+static_assert(kMaxExperts <= 8 * kDots, "one double per 8 experts");
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 uint64_t up64(uint64_t n, uint64_t m) { return (n + m - 1) / m * m; }

@@ -552,6 +552,178 @@ __global__ __launch_bounds__(256) void normalize(OrthArgs p, uint32_t col_tiles)
     }
 }
 
+// A whole update of a matrix of side up to 64 and length up to 512 in one
+// workgroup, with Y (hi, lo), A and P in LDS: the steps of such a matrix take
+// less than the launches that go between them (1 x 64 x 256: 71 us in 17
+// launches).  Sums, factors and roundings are those of the tiled products.
+constexpr uint32_t kSmallLength = 512;
+constexpr uint32_t small_lds(uint32_t length) { return 2 * length * 128 + 2 * 8192 + 2 * 256; }
+
+template <typename T, bool OVER>
+__global__ __launch_bounds__(512) void update_small(OrthArgs p, uint32_t steps) {
+    extern __shared__ __align__(16) uint8_t lds[];
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ double sum[8];
+    typedef short i16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+    const uint32_t tid = threadIdx.x, lane = __lane_id(), wave = uniform(tid >> 6), r = lane & 15, g = lane >> 4;
+    const uint32_t L = p.length;
+    uint8_t *const hi = lds, *const lo = lds + L * 128, *const A = lds + 2 * L * 128, *const P = A + 8192;
+    float *const rest_a = reinterpret_cast<float*>(P + 8192), *const rest_p = rest_a + 64;
+    // rows of 64 fp16, their 16-byte pieces turned: Y's in pairs, so that reads
+    // along rows and across them find different banks
+    auto y_at = [](uint32_t row, uint32_t col) {
+        return row * 128 + (((col >> 3) ^ ((row & 2) | ((row >> 1) & 4))) << 4) + (col & 7) * 2;
+    };
+    auto m_at = [](uint32_t row, uint32_t col) { return row * 128 + (((col >> 3) ^ ((row >> 1) & 7)) << 4) + (col & 7) * 2; };
+    // f(row, col, value) of every value of x
+    constexpr uint32_t kEach = 16 / sizeof(T);
+    const uint32_t size = p.n * p.k;
+    const T* x = static_cast<const T*>(p.x) + (uint64_t)blockIdx.x * size;
+    auto each = [&](auto f) {
+#pragma unroll 4
+        for (uint32_t e = tid * kEach; e < size; e += 512 * kEach) {
+            const xu32x4 word = load_word(x + e, size - e < kEach ? (int32_t)(size - e) : (int32_t)kEach);
+            T v[kEach];
+            __builtin_memcpy(v, &word, 16);
+            uint32_t row = e / p.k, col = e % p.k;
+#pragma unroll
+            for (uint32_t q = 0; q < kEach; ++q) {
+                if (e + q < size) f(row, col, to_float(v[q]));
+                if (++col == p.k) {
+                    col = 0;
+                    ++row;
+                }
+            }
+        }
+    };
+    for (uint32_t at = tid * 16; at < 2 * L * 128; at += 512 * 16) *reinterpret_cast<xu32x4*>(lds + at) = xu32x4{0, 0, 0, 0};
+    double s = 0.0;
+    each([&](uint32_t, uint32_t, float v) { s = fma((double)v, (double)v, s); });
+    for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+    if (lane == 0) sum[wave] = s;
+    __syncthreads();
+    s = 0.0;
+    for (int w = 0; w < 8; ++w) s += sum[w];
+    const double whole = sqrt(s) + (double)p.eps, f = whole == 0.0 ? 0.0 : (double)p.scale / whole;
+    each([&](uint32_t row, uint32_t col, float v) {
+        const float y = (float)((double)v * f);
+        const _Float16 h = (_Float16)y;
+        const uint32_t at = OVER ? y_at(col, row) : y_at(row, col);
+        *reinterpret_cast<_Float16*>(hi + at) = h;
+        *reinterpret_cast<_Float16*>(lo + at) = (_Float16)(y - (float)h);
+    });
+    __syncthreads();
+
+    // 16 rows, or columns, of an operand: c = 8 g to 8 g + 7 of the 32 from c0 on
+    auto along = [&](const uint8_t* m, uint32_t at) { return *reinterpret_cast<const f16x8*>(m + at); };
+    auto across = [&](uint32_t t, uint32_t c0) {
+        i16x4 q[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)  // lane 4 a + b of a group brings columns 4 b to 4 b + 3 of row a, and gets column 4 a + b
+            q[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(hi + y_at(c0 + 8 * g + 4 * u + (r >> 2), t * 16 + (r & 3) * 4)));
+        return __builtin_bit_cast(f16x8, __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    // of the matrices 64 x 64 a wave has two of the 16 parts: rows i, columns j to j + 3
+    const uint32_t ti = wave & 3, tj0 = wave >> 2 << 1, i = ti * 16 + r;
+    for (uint32_t step = 0; step < steps; ++step) {
+        f32x4 acc[4] = {};
+        for (uint32_t c0 = 0; c0 < L; c0 += 32) {
+            const f16x8 left = across(ti, c0);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(across(tj0 + t, c0), left, acc[t], 0, 0, 0);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t j = (tj0 + t) * 16 + g * 4;
+            const f32x4 v = acc[t] * p.inverse_square;
+            const f16x4 h = __builtin_convertvector(v, f16x4);
+            *reinterpret_cast<f16x4*>(A + m_at(i, j)) = h;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (i == j + q) rest_a[i] = v[q] - (float)h[q];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) acc[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (uint32_t c0 = 0; c0 < 64; c0 += 32) {
+            const f16x8 left = along(A, m_at(i, c0 + 8 * g));
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(along(A, m_at((tj0 + t) * 16 + r, c0 + 8 * g)), left, acc[t], 0, 0, 0);
+        }
+        const float rest_i = rest_a[i];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t j = (tj0 + t) * 16 + g * 4;
+            const f32x4 m = __builtin_convertvector(*reinterpret_cast<const f16x4*>(A + m_at(i, j)), f32x4);
+            f32x4 v = p.c * (acc[t] + m * *reinterpret_cast<const f32x4*>(rest_a + j) + rest_i * m) + p.b * m;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (i == j + q) v[q] += p.b * rest_i;
+            const f16x4 h = __builtin_convertvector(v, f16x4);
+            *reinterpret_cast<f16x4*>(P + m_at(i, j)) = h;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (i == j + q) rest_p[i] = v[q] - (float)h[q];
+        }
+        __syncthreads();
+        const bool last = step + 1 == steps;
+        f16x8 right[4][2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) right[t][h] = along(P, m_at(t * 16 + r, h * 32 + 8 * g));
+        // every wave its own rows of Y, which no other one reads here
+        for (uint32_t part = wave; part < L / 16; part += 8) {
+            const uint32_t row = part * 16 + r;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f16x8 left = along(hi, y_at(row, h * 32 + 8 * g));
+#pragma unroll
+                for (int t = 0; t < 4; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(right[t][h], left, acc[t], 0, 0, 0);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const uint32_t j = t * 16 + g * 4, at = y_at(row, j);
+                const f32x4 was = __builtin_convertvector(*reinterpret_cast<const f16x4*>(hi + at), f32x4) +
+                                  __builtin_convertvector(*reinterpret_cast<const f16x4*>(lo + at), f32x4);
+                const f32x4 v = acc[t] + (p.a + *reinterpret_cast<const f32x4*>(rest_p + j)) * was;
+                if (!last) {
+                    const f16x4 h = __builtin_convertvector(v, f16x4);
+                    *reinterpret_cast<f16x4*>(hi + at) = h;
+                    *reinterpret_cast<f16x4*>(lo + at) = __builtin_convertvector(v - __builtin_convertvector(h, f32x4), f16x4);
+                } else {
+                    __bf16* out = p.out + (uint64_t)blockIdx.x * size;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t a = OVER ? j + q : row, b = OVER ? row : j + q;
+                        if (a < p.n && b < p.k) out[a * p.k + b] = (__bf16)(v[q] * p.inverse);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+#endif
+}
+
+template <typename T, bool OVER>
+zc_status launch_small(const OrthArgs& a, uint32_t steps, hipStream_t stream) {
+    const uint32_t bytes = small_lds(a.length);
+    if (hipFuncSetAttribute(reinterpret_cast<const void*>(update_small<T, OVER>), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            (int)bytes) != hipSuccess) {
+        (void)hipGetLastError();  // reported here, not by the next launch
+        return ZC_ERR_HIP;
+    }
+    hipLaunchKernelGGL((update_small<T, OVER>), dim3(a.batch), dim3(512), bytes, stream, a, steps);
+    return ZC_OK;
+}
+static_assert(small_lds(kSmallLength) + 64 <= 160 * 1024, "Y, A and P in one CU's LDS");
+
 uint64_t tiles_of(const OrthArgs& a, int kind, uint32_t t) {
     const uint64_t side = (a.side + t - 1) / t, length = (a.length + t - 1) / t;
     return kind <= kMix ? side * (side + 1) / 2 : side * length;
@@ -659,6 +831,13 @@ zc_status launch_orthogonalize(OrthArgs a, uint32_t dtype, uint32_t steps, hipSt
     // more workgroups than a launch may have, with the smallest tiles
     if (!fits((uint64_t)a.batch * (a.length / 64) * (a.side / 64))) return ZC_ERR_UNSUPPORTED;
     const bool over = a.n < a.k;
+    if (a.side == 64 && a.length <= kSmallLength) {
+        auto small = [&](auto t) {
+            typedef decltype(t) T;
+            return over ? launch_small<T, true>(a, steps, stream) : launch_small<T, false>(a, steps, stream);
+        };
+        return dtype == ZC_BF16 ? small((__bf16)0.0f) : dtype == ZC_FP16 ? small((_Float16)0.0f) : small(0.0f);
+    }
     _Float16 *from = a.hi_a, *to = a.hi_b;
     a.next = from;
     if (dtype == ZC_BF16) prepare<__bf16>(a, over, stream);
