@@ -36,6 +36,14 @@ __device__ __forceinline__ double turned(double v) {
     const xu32x2 w = __builtin_bit_cast(xu32x2, v);
     return __builtin_bit_cast(double, xu32x2{turned<D>(w[0]), turned<D>(w[1])});
 }
+struct Best {
+    double key;
+    uint32_t of;
+};
+template <int D>
+__device__ __forceinline__ Best turned(const Best& v) {
+    return Best{turned<D>(v.key), turned<D>(v.of)};
+}
 // f over all lanes of a group, the same result in each (f commutes, and turns
 // by 1, 2, 4, 8 add in the same pairs in every lane).
 template <int L, int D = 1, typename T, typename F>
@@ -244,9 +252,9 @@ __device__ __forceinline__ void best_of(double (&k)[V], double (&best)[D]) {
 }
 
 // Scores with a bias, compared in 64 bits one choice after the other: the way
-// for the few tokens whose scores 32 bits do not tell apart.  The exponentials
-// go one after the other, by way of LDS (a lane's values 256 apart): side by
-// side they would take all registers.
+// for the few tokens whose scores 32 bits do not tell apart: a wave that gets
+// here ends some 8 us later.  The exponentials go four by four, by way of LDS
+// (a lane's values 256 apart): all side by side they would take all registers.
 template <int L, int V>
 __device__ __forceinline__ void choose_exactly(const ChooseArgs& a, uint64_t at, uint32_t e0, uint32_t l, double* keys,
                                                int32_t (&ids)[64 / L]) {
@@ -262,14 +270,14 @@ __device__ __forceinline__ void choose_exactly(const ChooseArgs& a, uint64_t at,
     }
     top = group_max<L>(top);
     double sum = 0.0;
-#pragma unroll 1
+#pragma unroll 4
     for (int j = 0; j < V; ++j) {
         const double v = keys[j * 256], e = exp(a.sigmoid ? -v : v - (double)top), score = a.sigmoid ? 1.0 / (1.0 + e) : e;
         keys[j * 256] = score;
         sum += score;
     }
     sum = group_sum<L>(sum);
-#pragma unroll 1
+#pragma unroll 4
     for (int j = 0; j < V; ++j) {
         const double v = (a.sigmoid ? keys[j * 256] : keys[j * 256] / sum) + (e0 + j < a.experts ? (double)a.bias[e0 + j] : 0.0);
         keys[j * 256] = v;
@@ -282,23 +290,14 @@ __device__ __forceinline__ void choose_exactly(const ChooseArgs& a, uint64_t at,
     for (int h = 0; h < 64 / L; ++h) ids[h] = -1;
 #pragma unroll 1
     for (uint32_t k = 0; k < a.topk; ++k) {
-        double best = -(double)kInf;
-        uint32_t of = ~0u;
+        Best best{-(double)kInf, ~0u};
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if ((open >> j & 1) && key[j] > best) {
-                best = key[j];
-                of = e0 + j;
-            }
-#pragma unroll
-        for (int d = 1; d < L; d <<= 1) {
-            const double other = __shfl_xor(best, d);
-            const uint32_t other_of = __shfl_xor(of, d);
-            if (other > best || (other == best && other_of < of)) {
-                best = other;
-                of = other_of;
-            }
-        }
+            if ((open >> j & 1) && key[j] > best.key) best = Best{key[j], e0 + j};
+        best = over_group<L>(best, [](const Best& p, const Best& q) {
+            return q.key > p.key || (q.key == p.key && q.of < p.of) ? q : p;
+        });
+        const uint32_t of = best.of;
         if (of - e0 < (uint32_t)V) open &= ~(1u << (of - e0));
 #pragma unroll
         for (int h = 0; h < 64 / L; ++h)
@@ -465,6 +464,8 @@ __global__ __launch_bounds__(256) void finish_choice(ChooseArgs a, uint32_t part
             n += a.part_counts[(uint64_t)q * a.experts + e];
         }
     }
+    double live = 0.0;  // whole numbers below 2^31; every workgroup, so that the last one need not wait for them
+    for (uint32_t q = threadIdx.x; q < parts; q += 256) live += a.part_live[q];
     sum[threadIdx.x] = s;
     count[threadIdx.x] = n;
     __syncthreads();
@@ -490,8 +491,6 @@ __global__ __launch_bounds__(256) void finish_choice(ChooseArgs a, uint32_t part
     }
     __syncthreads();
     if (!last) return;
-    double live = 0.0;  // whole numbers below 2^31
-    for (uint32_t q = threadIdx.x; q < parts; q += 256) live += a.part_live[q];
     double dot = 0.0;
     if (threadIdx.x < gridDim.x) dot = __hip_atomic_load(&a.dots[threadIdx.x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     live = workgroup_sum(live, shared);

@@ -576,24 +576,20 @@ __global__ __launch_bounds__(512) void update_small(OrthArgs p, uint32_t steps) 
         return row * 128 + (((col >> 3) ^ ((row & 2) | ((row >> 1) & 4))) << 4) + (col & 7) * 2;
     };
     auto m_at = [](uint32_t row, uint32_t col) { return row * 128 + (((col >> 3) ^ ((row >> 1) & 7)) << 4) + (col & 7) * 2; };
-    // f(row, col, value) of every value of x
-    constexpr uint32_t kEach = 16 / sizeof(T);
-    const uint32_t size = p.n * p.k;
+    // f(row, col, value) of every value of x, in little code: with one workgroup,
+    // instructions come from memory once and are waited for
+    const uint32_t size = p.n * p.k, down = 512 / p.k, right_by = 512 % p.k;
     const T* x = static_cast<const T*>(p.x) + (uint64_t)blockIdx.x * size;
     auto each = [&](auto f) {
+        uint32_t row = tid / p.k, col = tid % p.k;
 #pragma unroll 4
-        for (uint32_t e = tid * kEach; e < size; e += 512 * kEach) {
-            const xu32x4 word = load_word(x + e, size - e < kEach ? (int32_t)(size - e) : (int32_t)kEach);
-            T v[kEach];
-            __builtin_memcpy(v, &word, 16);
-            uint32_t row = e / p.k, col = e % p.k;
-#pragma unroll
-            for (uint32_t q = 0; q < kEach; ++q) {
-                if (e + q < size) f(row, col, to_float(v[q]));
-                if (++col == p.k) {
-                    col = 0;
-                    ++row;
-                }
+        for (uint32_t e = tid; e < size; e += 512) {
+            f(row, col, to_float(x[e]));
+            row += down;
+            col += right_by;
+            if (col >= p.k) {
+                col -= p.k;
+                ++row;
             }
         }
     };
@@ -628,10 +624,18 @@ __global__ __launch_bounds__(512) void update_small(OrthArgs p, uint32_t steps) 
     const uint32_t ti = wave & 3, tj0 = wave >> 2 << 1, i = ti * 16 + r;
     for (uint32_t step = 0; step < steps; ++step) {
         f32x4 acc[4] = {};
-        for (uint32_t c0 = 0; c0 < L; c0 += 32) {
-            const f16x8 left = across(ti, c0);
+        for (uint32_t c = 0; c < L; c += 64) {
+            f16x8 part[2][3];  // asked for at once
 #pragma unroll
-            for (int t = 0; t < 2; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(across(tj0 + t, c0), left, acc[t], 0, 0, 0);
+            for (int h = 0; h < 2; ++h) {
+                part[h][0] = across(ti, c + 32 * h);
+                part[h][1] = across(tj0, c + 32 * h);
+                part[h][2] = across(tj0 + 1, c + 32 * h);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(part[h][1 + t], part[h][0], acc[t], 0, 0, 0);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
