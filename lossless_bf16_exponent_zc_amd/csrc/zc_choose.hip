@@ -2,7 +2,18 @@
 // loss, and the gradient of both.
 //
 // A token belongs to L neighbouring lanes of one wave, lane l holding experts
-// l * V to l * V + V - 1 in registers from the load of the logits on.
+// l * V to l * V + V - 1 in registers from the load of the logits on, so that
+// they are read once: scores, the shares' sums and the choice all come from
+// there.  16 experts a lane (fewer where there are few) keep the number of
+// steps between lanes, which a wave waits for, at four for up to 256 experts.
+//
+// The choice is bound by instructions, not by memory: 65,536 tokens on 256
+// experts, topk 8, take 43 us (57 to 65 with a bias), of which the logits are 7
+// (bf16) to 14 (32 bits), about 280 vector instructions a token: a third of
+// them the sorted keys, a third the rounds that take the best of 16 lanes.  Its
+// gradient takes 27 us (bf16) to 37 (32 bits), 67 to 134 MB at 2.5 to 3.6 TB/s.
+// Few tokens are bound by their chain of round trips: 8 tokens 6.4 us (7.9 with
+// a bias), gradient 5.3; 8192 tokens 14 and 10.
 #include "zc_experts_kernels.h"
 
 #include <type_traits>
@@ -231,23 +242,44 @@ __device__ __forceinline__ void sort(double (&k)[M], int at = 0) {
     }
 }
 
-// The best D of a lane's keys, largest first.
+// Sorts N keys that go up and then down, or down and then up, largest first.
+template <int N>
+__device__ __forceinline__ void sort_bitonic(double (&k)[N]) {
+#pragma unroll
+    for (int d = N / 2; d; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (!(i & d)) order(k[i], k[i + d]);
+}
+
+// The best D of a lane's V keys, largest first, kNone past the V-th.
 template <int V, int D>
 __device__ __forceinline__ void best_of(double (&k)[V], double (&best)[D]) {
     if constexpr (D < V) {
+        static_assert(V == 2 * D, "two sorted halves");
         sort<D>(k, 0);
         sort<D>(k, D);
 #pragma unroll
-        for (int i = 0; i < D; ++i) best[i] = larger(k[i], k[2 * D - 1 - i]);  // the larger half, up and down again
-#pragma unroll
-        for (int d = D / 2; d; d >>= 1)
-#pragma unroll
-            for (int i = 0; i < D; ++i)
-                if (!(i & d)) order(best[i], best[i + d]);
+        for (int i = 0; i < D; ++i) best[i] = larger(k[i], k[2 * D - 1 - i]);
+        sort_bitonic(best);
     } else {
         sort<V>(k);
 #pragma unroll
-        for (int i = 0; i < D; ++i) best[i] = k[i];
+        for (int i = 0; i < D; ++i) best[i] = i < V ? k[i < V ? i : 0] : kNone;
+    }
+}
+
+// The best D of all lanes of a group, in each of them.
+template <int L, int D, int STEP = 1>
+__device__ __forceinline__ void best_of_group(double (&best)[D]) {
+    if constexpr (STEP < L) {
+        double other[D];
+#pragma unroll
+        for (int i = 0; i < D; ++i) other[i] = turned<STEP>(best[D - 1 - i]);
+#pragma unroll
+        for (int i = 0; i < D; ++i) best[i] = larger(best[i], other[i]);
+        sort_bitonic(best);
+        best_of_group<L, D, STEP * 2>(best);
     }
 }
 
@@ -320,9 +352,12 @@ __device__ __forceinline__ float loss_of(const ChooseArgs& a, double dot, uint32
     return live ? (float)((double)a.balance * a.experts * dot / ((double)a.topk * t * t)) : 0.0f;
 }
 
-// D: choices that one lane may have to give, at most.
-template <int L, int V, int D>
-__global__ __launch_bounds__(256, D > 8 ? 2 : 3) void choose(ChooseArgs a) {
+// Up to kFew choices are taken from the lanes' best kFew, joined pair by pair of
+// lanes; more of them one after the other from all.
+constexpr int kFew = 8;
+template <int L, int V, bool MANY>
+__global__ __launch_bounds__(256, MANY ? 2 : 3) void choose(ChooseArgs a) {
+    constexpr int D = MANY ? V : kFew;  // keys that a lane keeps
     constexpr uint32_t G = 256 / L;  // tokens at a time
     __shared__ double keys_in_lds[256 * V];  // choose_exactly's; at the end, the sums
     __shared__ uint32_t hist[kMaxExperts];
@@ -368,29 +403,60 @@ __global__ __launch_bounds__(256, D > 8 ? 2 : 3) void choose(ChooseArgs a) {
 #pragma unroll
         for (int j = 0; j < V; ++j) keys[j] = key_of(x[j], e0 + j);
         best_of<V, D>(keys, best);
-        // the group's best, again and again; the lane that had it moves up
         int32_t id[64 / L];
+        // What two 32-bit scores have to be apart for their order to be sure, in
+        // units of 2^-24: a sigmoid is off by at most 5 (its exponential by 1.5 |x|
+        // + 2 of itself), a softmax by 3 and by 27 that its sum has, of what two
+        // scores differ by; the sum with the bias is rounded by as many as its size.
+        const double tells = sigmoid ? 0x1p-20 : 0x1p-18;
         bool unsure = false;
-        double before = -kNone;
+        auto compare = [&](double before, double next) {
+            const double v = value_of(next), gap = value_of(before) - v;
+            unsure |= before > kClosed && !(gap > tells * (1.0 + fabs(v)));
+        };
+        if constexpr (!MANY) {
+            best_of_group<L>(best);
+            double own = kNone;
 #pragma unroll
-        for (int h = 0; h < 64 / L; ++h) {
-            id[h] = -1;
-            const uint32_t rounds = a.topk + (a.bias ? 1 : 0);  // with a bias, the first one not chosen too
-            for (uint32_t q = 0; q < L && h * L + q < rounds; ++q) {
-                const double top = over_group<L>(best[0], larger);
-                // 32-bit scores are off by at most 6 units of 2^-24 (of softmax's,
-                // past the sum that all share), sums with the bias by one of theirs
-                if (a.bias && before > kClosed) {
-                    const double v = value_of(top), gap = value_of(before) - v;
-                    unsure |= !(gap > 0x1p-20 * (1.0 + fabs(v)));
+            for (int i = 0; i < D; ++i) own = (uint32_t)i == l ? best[i] : own;
+            id[0] = l < a.topk ? expert_of(own) : -1;
+#pragma unroll
+            for (int h = 1; h < 64 / L; ++h) id[h] = -1;
+            if (a.bias) {
+                double past = kNone;  // the first one not among them
+#pragma unroll
+                for (int j = 0; j < V; ++j) past = larger(past, keys[j] < best[D - 1] ? keys[j] : kNone);
+                past = over_group<L>(past, larger);
+                // lane k compares choice k with the next
+                double next = past;
+#pragma unroll
+                for (int i = 1; i < D; ++i) next = (uint32_t)i == l + 1 ? best[i] : next;
+                if (l < a.topk) compare(own, next);
+                if (unsure) {  // unless the two are one score: the same logit and bias
+                    const int32_t e = expert_of(own), f = expert_of(next);
+                    unsure = f < 0 || one_logit(a.logits, at + e, a.dtype) != one_logit(a.logits, at + f, a.dtype) || a.bias[e] != a.bias[f];
                 }
-                before = top;
-                if (h * L + q == a.topk) break;
-                if (q == l) id[h] = expert_of(top);
-                if (best[0] == top) {
+                const uint64_t of_wave = __ballot(unsure);
+                unsure = (L == 64 ? of_wave : of_wave >> (__lane_id() & ~(L - 1)) & ((1ull << (L & 63)) - 1)) != 0;
+            }
+        } else {
+            // the group's best, again and again; the lane that had it moves up
+            const uint32_t rounds = a.topk + (a.bias ? 1 : 0);  // with a bias, the first one not chosen too
+            double before = kNone;
 #pragma unroll
-                    for (int i = 0; i + 1 < D; ++i) best[i] = best[i + 1];
-                    best[D - 1] = kNone;
+            for (int h = 0; h < 64 / L; ++h) {
+                id[h] = -1;
+                for (uint32_t q = 0; q < L && h * L + q < rounds; ++q) {
+                    const double top = over_group<L>(best[0], larger);
+                    if (a.bias) compare(before, top);
+                    before = top;
+                    if (h * L + q == a.topk) break;
+                    if (q == l) id[h] = expert_of(top);
+                    if (best[0] == top) {
+#pragma unroll
+                        for (int i = 0; i + 1 < D; ++i) best[i] = best[i + 1];
+                        best[D - 1] = kNone;
+                    }
                 }
             }
         }
@@ -659,9 +725,9 @@ uint32_t choose_parts(uint64_t tokens, uint32_t experts) {
 zc_status launch_choose(const ChooseArgs& a, hipStream_t stream) {
     const uint32_t parts = choose_parts(a.tokens, a.experts);
     with_shape(a.experts, [&](auto l, auto v) {
-        constexpr int L = decltype(l)::value, V = decltype(v)::value, FEW = V < 8 ? V : 8;
-        if (a.topk <= 8) hipLaunchKernelGGL((choose<L, V, FEW>), dim3(parts), dim3(256), 0, stream, a);
-        else hipLaunchKernelGGL((choose<L, V, V>), dim3(parts), dim3(256), 0, stream, a);
+        constexpr int L = decltype(l)::value, V = decltype(v)::value;
+        if (a.topk <= kFew) hipLaunchKernelGGL((choose<L, V, false>), dim3(parts), dim3(256), 0, stream, a);
+        else hipLaunchKernelGGL((choose<L, V, true>), dim3(parts), dim3(256), 0, stream, a);
     });
     if (parts > 1) hipLaunchKernelGGL(finish_choice, dim3((a.experts + kOf - 1) / kOf), dim3(256), 0, stream, a, parts);
     return ZC_OK;
