@@ -12,7 +12,11 @@ in; the sending side combines them with the router's weights.  The backward
 pass takes the same way back: gradients of the combination, of both products
 (inputs and weights) and of the dispatch.
 
-The step is compared with the same layer in plain torch, without 8-bit blocks.
+`routed_step` is the whole step: the router's choice of experts with its balance
+loss before that, and after it the gradient of both down to the router's weights
+and the orthogonalised updates of the experts'.
+
+The steps are compared with the same layer in plain torch, without 8-bit blocks.
 """
 import os
 import sys
@@ -118,6 +122,42 @@ def plain_step(x, ids, weights, w1, w2, dy):
     return (y.detach(),) + torch.autograd.grad(y, (x, weights, w1, w2), dy.float())
 
 
+def routed_step(x, gate, w1, w2, dy, topk, balance=0.01):
+    """train_step from the router on, gate [experts, hidden].  Returns the
+    choice, y and the gradients of x, gate, w1 and w2 (for y's dy and the balance
+    loss), and the updates of w1 and w2."""
+    logits = x.float() @ gate.float().T
+    router = zc.Router(x.shape[0], topk, gate.shape[0], normalize=True, balance=balance)
+    choice = router.empty_choice()
+    router.choose(logits, choice, router.empty_workspace())
+    y, dx, dweights, dw1, dw2, *_ = train_step(x, choice.ids, choice.weights, w1, w2, dy)
+    dlogits = torch.empty_like(logits)
+    router.choose_backward(logits, choice, dweights, None, dlogits)
+    dx = dx.float() + dlogits @ gate.float()
+    updates = [torch.empty_like(d) for d in (dw1, dw2)]
+    for d, u in zip((dw1, dw2), updates):
+        zc.orthogonalize(d, u)
+    return choice, y, dx, dlogits.T @ x.float(), dw1, dw2, updates
+
+
+def plain_routed_step(x, gate, w1, w2, dy, ids, counts, balance=0.01):
+    """The same for given choices, in 32-bit torch: y, the loss, the gradients."""
+    x, gate, w1, w2 = (t.float().requires_grad_() for t in (x, gate, w1, w2))
+    (tokens, topk), experts = ids.shape, gate.shape[0]
+    p = torch.softmax(x @ gate.T, 1)
+    picked = p.gather(1, ids.long())
+    weights = picked / picked.sum(1, keepdim=True)
+    loss = balance * experts / (topk * tokens ** 2) * (counts * p.sum(0)).sum()
+    y = torch.zeros_like(x)
+    for e in range(experts):
+        t, k = torch.nonzero(ids == e, as_tuple=True)
+        if t.numel():
+            part = torch.nn.functional.silu(x[t] @ w1[e].T) @ w2[e].T
+            y = y.index_add(0, t, part * weights[t, k][:, None])
+    grads = torch.autograd.grad((y * dy.float()).sum() + loss, (x, gate, w1, w2))
+    return (y.detach(), loss.detach()) + grads
+
+
 def inputs(tokens, hidden, inner, experts, topk, seed=0):
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
@@ -140,6 +180,15 @@ def main(tokens=2048, hidden=1024, inner=512, experts=32, topk=4):
     print(f"exchanged {rows.numel() * 2} bytes as {size}, values unchanged")
     for name, a, b in zip(("y", "dx", "dweights", "dw1", "dw2"), got, plain_step(*data)):
         print(f"{name:9s} off by {off(a, b):.4f} (8-bit blocks against 32-bit torch)")
+    x, _, _, w1, w2, dy = data
+    gate = torch.randn(experts, hidden, generator=torch.Generator().manual_seed(1)).cuda() * hidden ** -0.5
+    choice, y, dx, dgate, *_, updates = routed_step(x, gate, w1, w2, dy, topk)
+    want = plain_routed_step(x, gate, w1, w2, dy, choice.ids, choice.counts)
+    print(f"balance loss {float(choice.loss):.6f}, in torch {float(want[1]):.6f}")
+    for name, a, b in (("y", y, want[0]), ("dx", dx, want[2]), ("dgate", dgate, want[3])):
+        print(f"{name:9s} off by {off(a, b):.4f}, routed")
+    size = [torch.linalg.svdvals(u[0].float()) for u in updates]
+    print("singular values of the first expert's updates:", *(f"{float(v.min()):.2f} to {float(v.max()):.2f}" for v in size))
 
 
 if __name__ == "__main__":

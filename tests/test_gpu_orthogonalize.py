@@ -96,7 +96,7 @@ def check(x, out, steps=5, coefficients=MUON, eps=1e-7):
             assert off <= 1.2 * (model.to(torch.bfloat16).double() - exact).norm(), (float(off / whole), float(cost / whole))
 
 
-SIZES = [(1, 1, 1), (3, 1, 7), (2, 7, 1), (2, 5, 3), (1, 16, 16), (2, 63, 65), (2, 65, 63), (1, 64, 64), (1, 64, 256),
+SIZES = [(300, 33, 20), (5, 64, 512), (2, 512, 63), (2, 64, 513), (1, 512, 704), (1, 512, 705), (1, 1, 1), (3, 1, 7), (2, 7, 1), (2, 5, 3), (1, 16, 16), (2, 63, 65), (2, 65, 63), (1, 64, 64), (1, 64, 256),
          (20, 64, 48), (1, 100, 1000), (1, 1000, 100), (3, 129, 257), (3, 257, 129), (1, 300, 300), (2, 512, 640),
          (1, 640, 512), (1, 577, 1100), (1, 1025, 514), (1, 1, 2000), (1, 2000, 1), (1, 40, 4100)]
 
@@ -135,7 +135,7 @@ def test_steps_and_coefficients(steps, coefficients):
 
 
 def test_zeros_and_what_is_not_finite():
-    for n, k in ((70, 130), (130, 70)):
+    for n, k in ((70, 130), (130, 70), (40, 61), (500, 64), (600, 530)):
         x = matrices(6, n, k, dtype=torch.float32)
         x[1] = 0
         x[3, 5, 60], x[5, 0, 0] = math.nan, -math.inf
@@ -174,8 +174,9 @@ def test_smallest_elements_of_each_type():
 
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("offset", [1, 2, 3])
-def test_any_address_and_nothing_beside_it(dtype, offset):
-    batch, n, k = 3, 67, 81
+@pytest.mark.parametrize("n,k", [(67, 81), (81, 67), (33, 45), (520, 719)])
+def test_any_address_and_nothing_beside_it(dtype, offset, n, k):
+    batch = 3
     x = matrices(batch, n, k, dtype=TYPES[dtype])
     room = torch.full((offset + batch * n * k + 9,), math.nan, dtype=x.dtype, device="cuda")
     view = room[offset:offset + batch * n * k].view(batch, n, k)
@@ -187,20 +188,22 @@ def test_any_address_and_nothing_beside_it(dtype, offset):
     assert (target[:offset] == 7).all() and (target[offset + batch * n * k:] == 7).all()
 
 
-def test_in_place():
-    x = matrices(4, 130, 190)
+@pytest.mark.parametrize("n,k", [(130, 190), (60, 50), (512, 800)])
+def test_in_place(n, k):
+    x = matrices(4, n, k)
     apart, own = torch.empty_like(x, device="cuda"), x.cuda()
     zc.orthogonalize(x.cuda(), apart)
     zc.orthogonalize(own, own)
     assert torch.equal(apart, own)
 
 
-def test_a_matrix_does_not_depend_on_its_neighbours_or_the_workspace():
-    x = matrices(9, 200, 333, dtype=torch.float32).cuda()
+@pytest.mark.parametrize("n,k", [(200, 333), (30, 70), (900, 600)])
+def test_a_matrix_does_not_depend_on_its_neighbours_or_the_workspace(n, k):
+    x = matrices(9, n, k, dtype=torch.float32).cuda()
     x[4] = x[8] = x[0]
-    out = torch.empty(9, 200, 333, dtype=torch.bfloat16, device="cuda")
-    one = torch.empty(1, 200, 333, dtype=torch.bfloat16, device="cuda")
-    ws = torch.empty(zc.orthogonalize_workspace_bytes(9, 200, 333), dtype=torch.uint8, device="cuda")
+    out = torch.empty(9, n, k, dtype=torch.bfloat16, device="cuda")
+    one = torch.empty(1, n, k, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(zc.orthogonalize_workspace_bytes(9, n, k), dtype=torch.uint8, device="cuda")
     for fill in (0, 255, 0x7B):  # NaN and large numbers among them
         ws.fill_(fill)
         zc.orthogonalize(x, out, ws)
@@ -227,13 +230,14 @@ def test_offsets_past_32_bits():
     assert torch.equal(big[596], want[0]) and torch.equal(big[597:], want[1:]) and torch.equal(big[511], want[0])
 
 
-def test_another_stream_and_a_captured_graph():
-    inputs = [matrices(3, 150, 260, seed=s).cuda() for s in range(2)]
+@pytest.mark.parametrize("n,k", [(150, 260), (48, 64), (520, 800)])
+def test_another_stream_and_a_captured_graph(n, k):
+    inputs = [matrices(3, n, k, seed=s).cuda() for s in range(2)]
     want = [torch.empty_like(v) for v in inputs]
     for v, w in zip(inputs, want):
         zc.orthogonalize(v, w)
     static, out = inputs[0].clone(), torch.empty_like(want[0])
-    ws = torch.empty(zc.orthogonalize_workspace_bytes(3, 150, 260), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(zc.orthogonalize_workspace_bytes(3, n, k), dtype=torch.uint8, device="cuda")
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     zc.orthogonalize(static, out, ws, stream=side)

@@ -124,18 +124,39 @@ def test_gradient_against_differences(score, normalize):
             assert abs(float(out[t, e]) - (value(up) - value(down)) / (2 * h)) < 1e-5
 
 
-@pytest.mark.parametrize("biased", [False, True])
-def test_ties_go_to_the_lower_index(biased):
+@pytest.mark.parametrize("topk", [5, 8, 12])
+@pytest.mark.parametrize("bias", [None, 0.0, 0.25])
+def test_ties_go_to_the_lower_index(bias, topk):
     x = torch.zeros(9, 300)
     x[3, 7::11] = 1.0
     x[4] = -0.0
     x[5, ::2] = -0.0
     x[6] = torch.finfo(torch.float32).min
     x[6, 250] = -INF
-    bias = torch.zeros(300) if biased else None
-    router = zc.Router(9, 12, 300)
-    ids, *_ = check_choice(run(x, router, bias), x, router, bias)
-    assert ids[0].tolist() == list(range(12)) == ids[4].tolist() == ids[6].tolist()
+    x[7] = torch.arange(300) // 4 * 0.125
+    x[8] = x[7].flip(0)
+    bias = None if bias is None else torch.full((300,), bias)
+    for score in zc.Router.SCORES:
+        router = zc.Router(9, topk, 300, score=score)
+        ids, *_ = check_choice(run(x, router, bias), x, router, bias)
+        assert ids[0].tolist() == list(range(topk)) == ids[4].tolist() == ids[6].tolist()
+
+
+def test_infinite_logits_and_biases():
+    """+inf is above every number, for logits and for biases, ties by index."""
+    x = torch.zeros(4, 70)
+    x[0, 40] = x[0, 20] = INF
+    x[1, 5] = torch.finfo(torch.float32).max
+    x[1, 6] = INF
+    bias = torch.zeros(70)
+    for topk in (3, 20):
+        router = zc.Router(4, topk, 70, score="sigmoid")
+        c = run(x, router)
+        assert c.ids[0, :2].tolist() == [20, 40] and c.ids[1, :2].tolist() == [6, 5]
+        assert c.weights[0, :2].tolist() == [1.0, 1.0]
+        bias[33] = bias[9] = INF
+        c = run(x, router, bias)
+        assert (c.ids[:, :2].cpu() == torch.tensor([9, 33])).all() and torch.isfinite(c.weights).all()
 
 
 def test_neighbouring_biased_scores_are_told_apart():
@@ -147,8 +168,26 @@ def test_neighbouring_biased_scores_are_told_apart():
     x[1] = x[0].flip(0)
     bias = torch.linspace(-1e-3, 1e-3, experts)[torch.randperm(experts, generator=torch.Generator().manual_seed(1))]
     for b in (torch.zeros(experts), bias, torch.full((experts,), 0.25)):
-        router = zc.Router(4, 6, experts, score="sigmoid", normalize=True)
-        check_choice(run(x, router, b), x, router, b)
+        for topk in (1, 6, 8, 30):
+            router = zc.Router(4, topk, experts, score="sigmoid", normalize=True)
+            check_choice(run(x, router, b), x, router, b)
+
+
+@pytest.mark.parametrize("experts", [64, 128, 256, 500, 1000])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_order_of_biased_scores_that_nearly_meet(score, experts):
+    """Biases that undo the scores' differences up to some 2^-22, so that every
+    comparison is between sums that 32 bits put in another order."""
+    g = torch.Generator().manual_seed(experts)
+    x = torch.randn(1, experts, generator=g) * 2
+    s = plain.scores(x.double(), score)[0]
+    bias = (0.5 - s + torch.randn(experts, generator=g).double() * 2.0 ** -22).float()
+    x = x.expand(6, -1).contiguous()
+    for topk in (4, 8, 17):
+        router = zc.Router(6, topk, experts, score=score)
+        c = run(x, router, bias)
+        want = plain.choose(x.double(), topk, score=score, bias=bias)[0]
+        assert torch.equal(c.ids.cpu().long(), want)
 
 
 def test_tokens_with_few_open_experts():
