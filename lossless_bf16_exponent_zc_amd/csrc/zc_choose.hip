@@ -441,16 +441,14 @@ __global__ __launch_bounds__(256, MANY ? 2 : 3) void choose(ChooseArgs a) {
             }
         } else {
             // the group's best, again and again; the lane that had it moves up
-            const uint32_t rounds = a.topk + (a.bias ? 1 : 0);  // with a bias, the first one not chosen too
             double before = kNone;
 #pragma unroll
             for (int h = 0; h < 64 / L; ++h) {
                 id[h] = -1;
-                for (uint32_t q = 0; q < L && h * L + q < rounds; ++q) {
+                for (uint32_t q = 0; q < L && h * L + q < a.topk; ++q) {
                     const double top = over_group<L>(best[0], larger);
                     if (a.bias) compare(before, top);
                     before = top;
-                    if (h * L + q == a.topk) break;
                     if (q == l) id[h] = expert_of(top);
                     if (best[0] == top) {
 #pragma unroll
@@ -459,6 +457,7 @@ __global__ __launch_bounds__(256, MANY ? 2 : 3) void choose(ChooseArgs a) {
                     }
                 }
             }
+            if (a.bias) compare(before, over_group<L>(best[0], larger));  // the first one not among them
         }
         if (unsure) choose_exactly<L, V>(a, at, e0, l, keys_in_lds + tid, id);
         float mine[64 / L], chosen = 0.0f;

@@ -190,6 +190,24 @@ def test_order_of_biased_scores_that_nearly_meet(score, experts):
         assert torch.equal(c.ids.cpu().long(), want)
 
 
+@pytest.mark.parametrize("experts", [66, 200, 400, 1000])
+@pytest.mark.parametrize("topk", [8, 33, 64])
+def test_last_choice_and_the_first_one_left_out_nearly_meet(topk, experts):
+    """All choices far apart but the last, whose biased score and that of the
+    next expert differ by about 2^-25: 64 bits know which one is chosen."""
+    tokens, last = 100, topk - 1
+    g = torch.Generator().manual_seed(topk)
+    x = torch.full((tokens, experts), -8.0)
+    x[:, :last] = torch.linspace(8.0, 2.0, last)
+    x[:, last] = torch.rand(tokens, generator=g) * 2 - 1
+    x[:, topk] = torch.logit(torch.sigmoid(x[:, last].double()) - 0.125).float()
+    bias = torch.zeros(experts)
+    bias[topk] = 0.125
+    router = zc.Router(tokens, topk, experts, score="sigmoid", normalize=True)
+    ids, _, _ = check_choice(run(x, router, bias), x, router, bias)
+    assert 10 < int((ids[:, last] == topk).sum()) < 90
+
+
 def test_tokens_with_few_open_experts():
     x = torch.full((6, 40), -INF)
     x[1, 39] = -5.0
