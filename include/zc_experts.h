@@ -189,9 +189,9 @@ typedef enum zc_score { ZC_SOFTMAX = 0, ZC_SIGMOID = 1 } zc_score;
  * Every token chooses the topk experts of largest l, or with d_bias (float
  * [experts], part of the choice only) of largest s + bias, compared in 64 bits;
  * in that order, ties to the lower index.  A logit or a bias of -Inf closes an
- * expert: it is never chosen, nor is one whose logit is NaN; where fewer than
- * topk are left, the other ids are -1, which zc_route gives no row, and their
- * weights 0.  d_ids int32 and d_weights float [tokens, topk]: a weight is
+ * expert: it is never chosen, nor is one whose logit, or with a bias whose
+ * s + bias, is NaN; where fewer than topk are left, the other ids are -1, which
+ * zc_route gives no row, and their weights 0.  d_ids int32 and d_weights float [tokens, topk]: a weight is
  * scale * s, or with normalize scale * s / (sum of the token's chosen s), which
  * does not underflow where every s does.  NaN, and softmax's +Inf, make the
  * token's scores NaN, and with them its weights, the sums and the loss.
@@ -235,12 +235,13 @@ zc_status zc_choose_backward(const void *d_logits, uint64_t stride, uint32_t dty
  *   steps times  X <- a X + (b A + c A^2) X,  A = X X^T
  * (X <- a X + X (b A + c A^2), A = X^T X, which is the same, where n > k).
  * d_x contiguous [batch, n, k] of one of the three row types, d_out the result,
- * bf16, contiguous; they may be the same memory.  Products take fp16 factors
- * into 32-bit sums and X is kept in 22 bits (a pair of fp16): results are off
- * by 2e-4 to 2e-3 of their root mean square, besides their rounding to bf16 of
- * 1.7e-3, whatever the singular values.  That holds where X and A stay in
- * fp16's range, as they do where no singular value passes about 5.  A matrix
- * with a value that is not finite comes out as NaN, the others as they are.
+ * bf16, contiguous; where x is of 16 bits they may be the same memory, all of
+ * it, and may not overlap otherwise.  Products take fp16 factors into 32-bit
+ * sums and X is kept in 22 bits (a pair of fp16): results are off by 2e-4 to
+ * 2e-3 of their root mean square, besides their rounding to bf16 of 1.7e-3,
+ * whatever the singular values.  That holds where X and A stay in fp16's range,
+ * as they do where no singular value passes about 5.  A matrix with a value that
+ * is not finite comes out as NaN, the others as they are.
  * Limits: batch 0..65535, n and k 1..65536, steps 1..64.
  * zc_orthogonalize_workspace_bytes is 0 past a limit.
  */

@@ -360,6 +360,11 @@ zc_status zc_orthogonalize(const void* d_x, uint32_t dtype, uint32_t batch, uint
         return ZC_ERR_INVALID_ARG;
     const OrthLayout l = orth_layout(batch, n, k);
     if (ws_bytes < l.bytes) return ZC_ERR_CAPACITY;
+    // in place only where a matrix and its result are the same bytes: matrices
+    // that one workgroup updates are read and written at different times
+    const uintptr_t from = reinterpret_cast<uintptr_t>(d_x), to = reinterpret_cast<uintptr_t>(d_out);
+    const uint64_t values = (uint64_t)batch * n * k, each = elem_bytes(dtype);
+    if (from < to + values * 2 && to < from + values * each && (from != to || each != 2)) return ZC_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(d_ws);
     auto half = [&](uint64_t at) { return reinterpret_cast<_Float16*>(ws + at); };
     // a power of two about the square root of the longer side

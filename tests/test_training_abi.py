@@ -86,3 +86,11 @@ def test_orthogonalize_refusals(L):
     assert rc(L.zc_orthogonalize, good, 2, 0) == binding.ZC_OK
     for args in ((0, 8, 8), (1, 0, 8), (1, 8, 65537), (65536, 8, 8), (2**32 + 1, 8, 8), (1, 2**32 + 8, 8), (-1, 8, 8)):
         assert zc.orthogonalize_workspace_bytes(*args) == 0
+
+
+def test_updates_in_place_are_of_16_bits(L):
+    need = zc.orthogonalize_workspace_bytes(2, 8, 12)
+    size = 2 * 8 * 12
+    for dtype, out in ((2, P), (2, P + size * 4 - 2), (0, P + 2), (1, P + size * 2 - 2), (0, P - size * 2 + 2), (2, P - 2)):
+        args = [P, dtype, 2, 8, 12, 5, 3.0, -4.0, 2.0, 0.0, out, P + (1 << 20), need, None]
+        assert rc(L.zc_orthogonalize, args, 1, dtype) == BAD, (dtype, out)
