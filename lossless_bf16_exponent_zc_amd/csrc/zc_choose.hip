@@ -337,6 +337,30 @@ __device__ __forceinline__ void choose_exactly(const ChooseArgs& a, uint64_t at,
     }
 }
 
+// The same for sigmoids, which are each by itself, where what is chosen and the
+// next one are all that come into question: lane k's is `mine` (-1: none), and
+// lane k gets the expert that has rank k among them.
+template <int L>
+__device__ __forceinline__ int32_t in_exact_order(const ChooseArgs& a, uint64_t at, int32_t mine, uint32_t l, int candidates) {
+    double v = -(double)kInf;
+    if (mine >= 0) v = 1.0 / (1.0 + exp(-(double)one_logit(a.logits, at + mine, a.dtype))) + (double)a.bias[mine];
+    uint32_t rank = 0;
+#pragma unroll 1
+    for (int i = 0; i < candidates; ++i) {
+        const double w = __shfl(v, i, L);
+        const int32_t of = __shfl(mine, i, L);
+        rank += of >= 0 && (w > v || (w == v && of < mine));
+    }
+    int32_t id = -1;
+#pragma unroll 1
+    for (int i = 0; i < candidates; ++i) {
+        const uint32_t of_rank = __shfl(rank, i, L);
+        const int32_t of = __shfl(mine, i, L);
+        if (of >= 0 && of_rank == l) id = of;
+    }
+    return id;
+}
+
 // Sum over a workgroup, in every thread; `shared` has room for 4.
 __device__ __forceinline__ double workgroup_sum(double v, double* shared) {
     v = group_sum<64>(v);
@@ -410,9 +434,9 @@ __global__ __launch_bounds__(256, MANY ? 2 : 3) void choose(ChooseArgs a) {
         // scores differ by; the sum with the bias is rounded by as many as its size.
         const double tells = sigmoid ? 0x1p-20 : 0x1p-18;
         bool unsure = false;
-        auto compare = [&](double before, double next) {
+        auto near = [&](double before, double next) {
             const double v = value_of(next), gap = value_of(before) - v;
-            unsure |= before > kClosed && !(gap > tells * (1.0 + fabs(v)));
+            return before > kClosed && !(gap > tells * (1.0 + fabs(v)));
         };
         if constexpr (!MANY) {
             best_of_group<L>(best);
@@ -431,13 +455,24 @@ __global__ __launch_bounds__(256, MANY ? 2 : 3) void choose(ChooseArgs a) {
                 double next = past;
 #pragma unroll
                 for (int i = 1; i < D; ++i) next = (uint32_t)i == l + 1 ? best[i] : next;
-                if (l < a.topk) compare(own, next);
+                unsure = l < a.topk && near(own, next);
                 if (unsure) {  // unless the two are one score: the same logit and bias
                     const int32_t e = expert_of(own), f = expert_of(next);
                     unsure = f < 0 || one_logit(a.logits, at + e, a.dtype) != one_logit(a.logits, at + f, a.dtype) || a.bias[e] != a.bias[f];
                 }
                 const uint64_t of_wave = __ballot(unsure);
                 unsure = (L == 64 ? of_wave : of_wave >> (__lane_id() & ~(L - 1)) & ((1ull << (L & 63)) - 1)) != 0;
+                if (unsure && sigmoid) {
+                    const double last = __shfl(own, (int)a.topk - 1, L);
+                    uint32_t others = 0;  // that may belong among them
+#pragma unroll
+                    for (int j = 0; j < V; ++j) others += keys[j] < last && keys[j] > kClosed && near(last, keys[j]);
+                    if (group_sum<L>(others) <= 1) {
+                        const int32_t of = in_exact_order<L>(a, at, l > a.topk ? -1 : expert_of(l == D ? past : own), l, (int)a.topk + 1);
+                        id[0] = l < a.topk ? of : -1;
+                        unsure = false;
+                    }
+                }
             }
         } else {
             // the group's best, again and again; the lane that had it moves up
@@ -447,7 +482,7 @@ __global__ __launch_bounds__(256, MANY ? 2 : 3) void choose(ChooseArgs a) {
                 id[h] = -1;
                 for (uint32_t q = 0; q < L && h * L + q < a.topk; ++q) {
                     const double top = over_group<L>(best[0], larger);
-                    if (a.bias) compare(before, top);
+                    if (a.bias) unsure |= near(before, top);
                     before = top;
                     if (q == l) id[h] = expert_of(top);
                     if (best[0] == top) {
@@ -457,7 +492,7 @@ __global__ __launch_bounds__(256, MANY ? 2 : 3) void choose(ChooseArgs a) {
                     }
                 }
             }
-            if (a.bias) compare(before, over_group<L>(best[0], larger));  // the first one not among them
+            if (a.bias) unsure |= near(before, over_group<L>(best[0], larger));  // the first one not among them
         }
         if (unsure) choose_exactly<L, V>(a, at, e0, l, keys_in_lds + tid, id);
         float mine[64 / L], chosen = 0.0f;

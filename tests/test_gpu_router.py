@@ -208,6 +208,28 @@ def test_last_choice_and_the_first_one_left_out_nearly_meet(topk, experts):
     assert 10 < int((ids[:, last] == topk).sum()) < 90
 
 
+@pytest.mark.parametrize("experts", [20, 100, 256, 500, 1000])
+@pytest.mark.parametrize("more", [-1, 0, 1, 2])
+def test_order_of_a_choice_whose_scores_nearly_meet(more, experts):
+    """topk + more scores that nearly meet: fewer than are chosen (the others
+    closed), just those, and some that are left out, at places in any lane."""
+    for topk in (2, 5, 8):
+        for seed in range(20):
+            g = torch.Generator().manual_seed(seed)
+            x = torch.full((3, experts), -INF if more < 0 else -8.0)
+            near = torch.randperm(experts, generator=g)[:topk + more]
+            x[:, near] = torch.randn(topk + more, generator=g) * 2
+            bias = torch.zeros(experts)
+            s = plain.scores(x.double(), "sigmoid")[0]
+            bias[near] = (0.5 - s[near] + torch.randn(topk + more, generator=g).double() * 2.0 ** -23).float()
+            bias[near[0]] = bias[near[-1]]
+            x[:, near[0]] = x[:, near[-1]]
+            x[2] = x[2].flip(0)
+            router = zc.Router(3, topk, experts, score="sigmoid", normalize=True)
+            want = plain.choose(x.double(), topk, score="sigmoid", bias=bias)[0]
+            assert torch.equal(run(x, router, bias).ids.cpu().long(), want), (topk, seed)
+
+
 def test_tokens_with_few_open_experts():
     x = torch.full((6, 40), -INF)
     x[1, 39] = -5.0
