@@ -8,12 +8,12 @@
 // steps between lanes, which a wave waits for, at four for up to 256 experts.
 //
 // The choice is bound by instructions, not by memory: 65,536 tokens on 256
-// experts, topk 8, take 43 us (57 to 65 with a bias), of which the logits are 7
-// (bf16) to 14 (32 bits), about 280 vector instructions a token: a third of
-// them the sorted keys, a third the rounds that take the best of 16 lanes.  Its
-// gradient takes 27 us (bf16) to 37 (32 bits), 67 to 134 MB at 2.5 to 3.6 TB/s.
-// Few tokens are bound by their chain of round trips: 8 tokens 6.4 us (7.9 with
-// a bias), gradient 5.3; 8192 tokens 14 and 10.
+// experts, topk 8, take 35 us (47 with a bias), of which the logits are 7 (bf16)
+// to 14 (32 bits), about 250 vector instructions a token: a third of them the
+// sorted keys, a third the joins of 16 lanes' best.  Its gradient takes 27 us
+// (bf16) to 37 (32 bits), 67 to 134 MB at 2.5 to 3.6 TB/s.  Few tokens are bound
+// by their chain of round trips: 8 tokens 5.4 us (7.1 with a bias), gradient
+// 5.3; 8192 tokens 13 (19) and 10.
 #include "zc_experts_kernels.h"
 
 #include <type_traits>
@@ -284,8 +284,8 @@ __device__ __forceinline__ void best_of_group(double (&best)[D]) {
 }
 
 // Scores with a bias, compared in 64 bits one choice after the other: the way
-// for the few tokens whose scores 32 bits do not tell apart: a wave that gets
-// here ends some 8 us later.  The exponentials go four by four, by way of LDS
+// for the few tokens whose scores 32 bits do not tell apart and that
+// in_exact_order does not take: a wave that gets here ends some 8 us later.  The exponentials go four by four, by way of LDS
 // (a lane's values 256 apart): all side by side they would take all registers.
 template <int L, int V>
 __device__ __forceinline__ void choose_exactly(const ChooseArgs& a, uint64_t at, uint32_t e0, uint32_t l, double* keys,
@@ -339,7 +339,9 @@ __device__ __forceinline__ void choose_exactly(const ChooseArgs& a, uint64_t at,
 
 // The same for sigmoids, which are each by itself, where what is chosen and the
 // next one are all that come into question: lane k's is `mine` (-1: none), and
-// lane k gets the expert that has rank k among them.
+// lane k gets the expert that has rank k among them.  One exponential a lane
+// instead of 16 and no rounds: with a bias 8192 tokens 26.7 -> 19.1 us, 65,536
+// 55 -> 47, as of both some tokens need it.
 template <int L>
 __device__ __forceinline__ int32_t in_exact_order(const ChooseArgs& a, uint64_t at, int32_t mine, uint32_t l, int candidates) {
     double v = -(double)kInf;
@@ -549,7 +551,7 @@ __global__ __launch_bounds__(256, MANY ? 2 : 3) void choose(ChooseArgs a) {
 // Sums of what the workgroups of `choose` left, kOf experts a workgroup, and by
 // the last of them the loss.  Its time is that of one round trip to memory, as
 // long as there are enough workgroups: 8192 tokens, 256 experts, 512 parts:
-// with 16 experts each 7.3 us.
+// with 8 experts each 6.1 us, with 16 7.3.
 constexpr uint32_t kOf = 8;
 __global__ __launch_bounds__(256) void finish_choice(ChooseArgs a, uint32_t parts) {
     __shared__ double sum[256], shared[4];
@@ -732,7 +734,7 @@ __global__ __launch_bounds__(256, 4) void choose_backward(ChooseGradArgs a) {
 
 // Workgroups of a choice, and of its gradient, at most: what the CUs hold at
 // once, which go on to the next tokens.  65,536 tokens on 256 experts, in us:
-// choices in 512 / 768 / 1024 workgroups 47/42/47, with a bias 73/61/68; gradients
+// choices in 512 / 768 / 1024 workgroups 36/35/37, with a bias 49/47/51; gradients
 // in 1024 / 4096 27/44.
 constexpr uint32_t kParts = 768, kBackward = 1024;
 
