@@ -8,11 +8,11 @@
 // steps between lanes, which a wave waits for, at four for up to 256 experts.
 //
 // The choice is bound by instructions, not by memory: 65,536 tokens on 256
-// experts, topk 8, take 35 us (47 with a bias), of which the logits are 7 (bf16)
+// experts, topk 8, take 33 us (47 with a bias), of which the logits are 7 (bf16)
 // to 14 (32 bits), about 250 vector instructions a token: a third of them the
 // sorted keys, a third the joins of 16 lanes' best.  Its gradient takes 27 us
 // (bf16) to 37 (32 bits), 67 to 134 MB at 2.5 to 3.6 TB/s.  Few tokens are bound
-// by their chain of round trips: 8 tokens 5.4 us (7.1 with a bias), gradient
+// by their chain of round trips: 8 tokens 4.6 us (7.0 with a bias), gradient
 // 5.3; 8192 tokens 13 (19) and 10.
 #include "zc_experts_kernels.h"
 
@@ -379,13 +379,15 @@ __device__ __forceinline__ float loss_of(const ChooseArgs& a, double dot, uint32
 }
 
 // Up to kFew choices are taken from the lanes' best kFew, joined pair by pair of
-// lanes; more of them one after the other from all.
+// lanes; more of them one after the other from all.  Without a bias there is
+// nothing to do again: 92 registers instead of 168, and 8 tokens take 4.6 us, not
+// 5.4, 65,536 33, not 35.
 constexpr int kFew = 8;
-template <int L, int V, bool MANY>
-__global__ __launch_bounds__(256, MANY ? 2 : 3) void choose(ChooseArgs a) {
+template <int L, int V, bool MANY, bool BIASED>
+__global__ __launch_bounds__(256, MANY ? 2 : BIASED ? 3 : 4) void choose(ChooseArgs a) {
     constexpr int D = MANY ? V : kFew;  // keys that a lane keeps
     constexpr uint32_t G = 256 / L;  // tokens at a time
-    __shared__ double keys_in_lds[256 * V];  // choose_exactly's; at the end, the sums
+    __shared__ double keys_in_lds[(BIASED ? 256 : 128) * V];  // choose_exactly's; at the end, the sums
     __shared__ uint32_t hist[kMaxExperts];
     __shared__ uint32_t live_tokens;
     __shared__ double shared[4];
@@ -400,7 +402,7 @@ __global__ __launch_bounds__(256, MANY ? 2 : 3) void choose(ChooseArgs a) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         sums[j] = 0.0f;
-        bias[j] = a.bias && l * V + j < a.experts ? a.bias[l * V + j] : 0.0f;
+        bias[j] = BIASED && l * V + j < a.experts ? a.bias[l * V + j] : 0.0f;
     }
     uint32_t live = 0;
     for (uint32_t t = blockIdx.x * G + g; t < a.tokens; t += gridDim.x * G) {
@@ -422,7 +424,7 @@ __global__ __launch_bounds__(256, MANY ? 2 : 3) void choose(ChooseArgs a) {
         double keys[V], best[D];
 #pragma unroll
         for (int j = 0; j < V; ++j) sums[j] += s[j] * r.part;
-        if (a.bias) {
+        if constexpr (BIASED) {
 #pragma unroll
             for (int j = 0; j < V; ++j) x[j] = x[j] > -kInf ? s[j] * r.back + bias[j] : -kInf;
         }
@@ -448,7 +450,7 @@ __global__ __launch_bounds__(256, MANY ? 2 : 3) void choose(ChooseArgs a) {
             id[0] = l < a.topk ? expert_of(own) : -1;
 #pragma unroll
             for (int h = 1; h < 64 / L; ++h) id[h] = -1;
-            if (a.bias) {
+            if constexpr (BIASED) {
                 double past = kNone;  // the first one not among them
 #pragma unroll
                 for (int j = 0; j < V; ++j) past = larger(past, keys[j] < best[D - 1] ? keys[j] : kNone);
@@ -484,7 +486,7 @@ __global__ __launch_bounds__(256, MANY ? 2 : 3) void choose(ChooseArgs a) {
                 id[h] = -1;
                 for (uint32_t q = 0; q < L && h * L + q < a.topk; ++q) {
                     const double top = over_group<L>(best[0], larger);
-                    if (a.bias) unsure |= near(before, top);
+                    if constexpr (BIASED) unsure |= near(before, top);
                     before = top;
                     if (q == l) id[h] = expert_of(top);
                     if (best[0] == top) {
@@ -494,9 +496,9 @@ __global__ __launch_bounds__(256, MANY ? 2 : 3) void choose(ChooseArgs a) {
                     }
                 }
             }
-            if (a.bias) unsure |= near(before, over_group<L>(best[0], larger));  // the first one not among them
+            if constexpr (BIASED) unsure |= near(before, over_group<L>(best[0], larger));  // the first one not among them
         }
-        if (unsure) choose_exactly<L, V>(a, at, e0, l, keys_in_lds + tid, id);
+        if (BIASED && unsure) choose_exactly<L, V>(a, at, e0, l, keys_in_lds + tid, id);
         float mine[64 / L], chosen = 0.0f;
 #pragma unroll
         for (int h = 0; h < 64 / L; ++h) {
@@ -734,7 +736,7 @@ __global__ __launch_bounds__(256, 4) void choose_backward(ChooseGradArgs a) {
 
 // Workgroups of a choice, and of its gradient, at most: what the CUs hold at
 // once, which go on to the next tokens.  65,536 tokens on 256 experts, in us:
-// choices in 512 / 768 / 1024 workgroups 36/35/37, with a bias 49/47/51; gradients
+// choices in 768 / 1024 / 1280 workgroups 33/33/35, with a bias 47/50/52; gradients
 // in 1024 / 4096 27/44.
 constexpr uint32_t kParts = 768, kBackward = 1024;
 
@@ -762,8 +764,13 @@ zc_status launch_choose(const ChooseArgs& a, hipStream_t stream) {
     const uint32_t parts = choose_parts(a.tokens, a.experts);
     with_shape(a.experts, [&](auto l, auto v) {
         constexpr int L = decltype(l)::value, V = decltype(v)::value;
-        if (a.topk <= kFew) hipLaunchKernelGGL((choose<L, V, false>), dim3(parts), dim3(256), 0, stream, a);
-        else hipLaunchKernelGGL((choose<L, V, true>), dim3(parts), dim3(256), 0, stream, a);
+        auto launch = [&](auto many, auto biased) {
+            hipLaunchKernelGGL((choose<L, V, decltype(many)::value, decltype(biased)::value>), dim3(parts), dim3(256), 0, stream, a);
+        };
+        const std::true_type yes;
+        const std::false_type no;
+        if (a.topk <= kFew) a.bias ? launch(no, yes) : launch(no, no);
+        else a.bias ? launch(yes, yes) : launch(yes, no);
     });
     if (parts > 1) hipLaunchKernelGGL(finish_choice, dim3((a.experts + kOf - 1) / kOf), dim3(256), 0, stream, a, parts);
     return ZC_OK;
