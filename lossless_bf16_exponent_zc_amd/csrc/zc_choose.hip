@@ -459,19 +459,37 @@ __global__ __launch_bounds__(256, MANY ? 2 : BIASED ? 3 : 4) void choose(ChooseA
                 double next = past;
 #pragma unroll
                 for (int i = 1; i < D; ++i) next = (uint32_t)i == l + 1 ? best[i] : next;
-                unsure = l < a.topk && near(own, next);
-                if (unsure) {  // unless the two are one score: the same logit and bias
+                const bool close = l < a.topk && near(own, next);
+                if (close) {  // unless the two are one score: the same logit and bias
                     const int32_t e = expert_of(own), f = expert_of(next);
                     unsure = f < 0 || one_logit(a.logits, at + e, a.dtype) != one_logit(a.logits, at + f, a.dtype) || a.bias[e] != a.bias[f];
                 }
-                const uint64_t of_wave = __ballot(unsure);
-                unsure = (L == 64 ? of_wave : of_wave >> (__lane_id() & ~(L - 1)) & ((1ull << (L & 63)) - 1)) != 0;
-                if (unsure && sigmoid) {
+                auto in_group = [](bool v) {
+                    const uint64_t of_wave = __ballot(v);
+                    return (L == 64 ? of_wave : of_wave >> (__lane_id() & ~(L - 1)) & ((1ull << (L & 63)) - 1)) != 0;
+                };
+                unsure = in_group(unsure);
+                if (unsure ? sigmoid : in_group(close && l + 1 == a.topk)) {
+                    // Those left out that may belong among the chosen: at least all
+                    // that are near the last choice.  Where that and the next one are
+                    // one score, the lower index stands first, but another one behind
+                    // them may be larger than both.
                     const double last = __shfl(own, (int)a.topk - 1, L);
-                    uint32_t others = 0;  // that may belong among them
+                    const double from = larger(last - 1.01 * tells * (1.0 + fabs(last)), kClosed);
+                    uint32_t others = 0;
 #pragma unroll
-                    for (int j = 0; j < V; ++j) others += keys[j] < last && keys[j] > kClosed && near(last, keys[j]);
-                    if (group_sum<L>(others) <= 1) {
+                    for (int j = 0; j < V; ++j) others += keys[j] < last && keys[j] > from;
+                    const uint32_t all = group_sum<L>(others);
+                    if (!unsure && all > 1) {  // unless they all are that one score
+                        const int32_t e = expert_of(last);
+                        const float its_logit = one_logit(a.logits, at + e, a.dtype), its_bias = a.bias[e];
+                        uint32_t same = 0;
+#pragma unroll 4
+                        for (int32_t f = e0; f < (int32_t)(e0 + V); ++f)
+                            same += f > e && f < (int32_t)a.experts && one_logit(a.logits, at + f, a.dtype) == its_logit && a.bias[f] == its_bias;
+                        unsure = group_sum<L>(same) < all;
+                    }
+                    if (unsure && sigmoid && all <= 1) {
                         const int32_t of = in_exact_order<L>(a, at, l > a.topk ? -1 : expert_of(l == D ? past : own), l, (int)a.topk + 1);
                         id[0] = l < a.topk ? of : -1;
                         unsure = false;

@@ -436,6 +436,44 @@ def test_with_the_routing_it_feeds(tokens, topk, experts, hidden):
     assert abs(float(c.loss) - float(loss.detach())) <= float(loss.detach()) * eps
 
 
+@pytest.mark.parametrize("experts", [20, 100, 256, 500, 1000])
+@pytest.mark.parametrize("topk", [1, 2, 5, 8, 12])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_equal_scores_at_the_border_hide_no_larger_one(score, topk, experts):
+    """The last choice and the first one left out have the same logit and bias,
+    and a later expert is larger by less than 32 bits tell (sigmoids of 20 and
+    21; softmax scores 2^-14 apart beside biases of 1024), behind clearly larger
+    choices, between others, and twice."""
+    level = 1024.0 if score == "softmax" else 0.0
+    equal, larger = (0.0, 2.0 ** -13) if score == "softmax" else (20.0, 21.0)
+    g = torch.Generator().manual_seed(experts + topk)
+    x, bias = torch.full((8, experts), equal - 8.0), torch.full((experts,), level)
+    place = torch.randperm(experts, generator=g)
+    bias[place[:topk - 1]] += torch.arange(topk - 1) * 0.5 + 1  # chosen first
+    at = place[topk - 1:topk + 4].sort().values
+    for t, values in enumerate([(equal, equal, larger), (equal, equal, larger, larger), (equal, equal, equal, larger),
+                                (equal, equal), (equal, larger, equal), (larger, equal, equal), (equal, larger, equal, larger),
+                                (equal, equal, equal, equal, larger)]):
+        x[t, place[:topk - 1]] = equal
+        x[t, at[:len(values)]] = torch.tensor(values)
+    router = zc.Router(8, topk, experts, score=score, normalize=True, balance=0.1)
+    ids, *_ = check_choice(run(x, router, bias), x, router, bias)
+    assert ids[0, -1] == at[2] and ids[3, -1] == at[0]
+
+
+@pytest.mark.parametrize("topk", [1, 2, 8, 9])
+@pytest.mark.parametrize("experts", [64, 256, 600])
+def test_scores_that_saturate(experts, topk):
+    """16-bit logits so large that many sigmoids are 1, or nearly, in 32 bits:
+    without differences in the bias the order is that of 64 bits."""
+    g = torch.Generator().manual_seed(experts)
+    x = (torch.randn(3000, experts, generator=g) * 16).bfloat16()
+    for bias in (torch.zeros(experts), torch.full((experts,), 0.3)):
+        router = zc.Router(3000, topk, experts, score="sigmoid")
+        want = plain.choose(x.double(), topk, score="sigmoid", bias=bias)[0]
+        assert torch.equal(run(x, router, bias).ids.cpu().long(), want)
+
+
 def test_refusals():
     from lossless_bf16_exponent_zc_amd.binding import ZC_ERR_CAPACITY, ZC_ERR_INVALID_ARG, ZC_ERR_UNSUPPORTED
     router = zc.Router(8, 2, 16)
