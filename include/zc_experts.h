@@ -191,9 +191,10 @@ typedef enum zc_score { ZC_SOFTMAX = 0, ZC_SIGMOID = 1 } zc_score;
  * in that order, ties to the lower index.  A logit or a bias of -Inf closes an
  * expert: it is never chosen, nor is one whose logit, or with a bias whose
  * s + bias, is NaN; where fewer than topk are left, the other ids are -1, which
- * zc_route gives no row, and their weights 0.  d_ids int32 and d_weights float [tokens, topk]: a weight is
- * scale * s, or with normalize scale * s / (sum of the token's chosen s), which
- * does not underflow where every s does.  NaN, and softmax's +Inf, make the
+ * zc_route gives no row, and their weights 0.  d_ids int32 and d_weights float
+ * [tokens, topk]: a weight is scale * s, or with normalize scale * s / (sum of
+ * the token's chosen s), a quotient that keeps its digits where the scores
+ * underflow.  NaN, and softmax's +Inf, make the
  * token's scores NaN, and with them its weights, the sums and the loss.
  *
  * d_mask (bytes [tokens], or NULL): tokens where it is 0 choose -1 throughout

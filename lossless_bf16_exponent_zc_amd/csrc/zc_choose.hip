@@ -163,6 +163,10 @@ __device__ __forceinline__ float score_of(float x, float base, bool sigmoid) {
     return !sigmoid ? exp_of(x - base) : base < 0.0f ? low_sigmoid_of(x, base) : sigmoid_of(x);
 }
 
+__device__ __forceinline__ float base_of(float largest, bool sigmoid) {
+    return largest == -kInf || (sigmoid && largest > 0.0f) ? 0.0f : largest;
+}
+
 struct Scored {
     float base, total, part, back;  // part: 1 / total
 };
@@ -173,7 +177,7 @@ __device__ __forceinline__ Scored scores(const float (&x)[V], float (&s)[V], boo
     for (int j = 0; j < V; ++j) top = fmaxf(top, x[j]);
     top = group_max<L>(top);
     Scored r;
-    r.base = top == -kInf || (sigmoid && top > 0.0f) ? 0.0f : top;
+    r.base = base_of(top, sigmoid);
     float sum = 0.0f;
     if (!sigmoid) {
 #pragma unroll
@@ -192,6 +196,30 @@ __device__ __forceinline__ Scored scores(const float (&x)[V], float (&s)[V], boo
     r.part = share_of(r.total);
     r.back = sigmoid ? exp_of(r.base) : r.part;
     return r;
+}
+
+// With a bias the largest logits need not be among the chosen, and the scores of
+// these, relative to the largest of all, lose their digits where they are far
+// below it.  Where their sum is below kFar (2^-126 is the smallest number that
+// the exponential makes), they are made anew, relative to the largest chosen one.
+// Returns their sum.
+constexpr float kFar = 0x1p-24f;
+template <int L>
+__device__ __forceinline__ float among_chosen(const void* logits, uint64_t at, uint32_t dtype, const int32_t (&id)[64 / L],
+                                              bool sigmoid, float (&s)[64 / L]) {
+    float top = -kInf, sum = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 64 / L; ++h) {
+        s[h] = id[h] >= 0 ? one_logit(logits, at + id[h], dtype) : -kInf;
+        top = fmaxf(top, s[h]);
+    }
+    const float base = base_of(group_max<L>(top), sigmoid);
+#pragma unroll
+    for (int h = 0; h < 64 / L; ++h) {
+        s[h] = score_of(s[h], base, sigmoid);
+        sum += s[h];
+    }
+    return group_sum<L>(sum);
 }
 
 // A comparison's value and its expert in one double that orders as they do,
@@ -530,9 +558,13 @@ __global__ __launch_bounds__(256, MANY ? 2 : BIASED ? 3 : 4) void choose(ChooseA
             }
             chosen += mine[h];
         }
-        // a NaN among the token's logits reaches its weights wherever it was chosen
         float factor = a.scale * r.back;
-        if (a.normalize) factor = a.scale * share_of(group_sum<L>(chosen));
+        if (a.normalize) {
+            chosen = group_sum<L>(chosen);
+            if (BIASED && chosen < kFar) chosen = among_chosen<L>(a.logits, at, a.dtype, id, sigmoid, mine);
+            factor = a.scale * share_of(chosen);
+        }
+        // a NaN among the token's logits reaches its weights wherever it was chosen
         if (r.total != r.total) factor = r.total;
 #pragma unroll
         for (int h = 0; h < 64 / L; ++h)
@@ -701,9 +733,13 @@ __global__ __launch_bounds__(256, 4) void choose_backward(ChooseGradArgs a) {
                 both += v * dw[h];
             }
         }
+        bool far = false;
         if (a.normalize) {
-            chosen = share_of(group_sum<L>(chosen));
-            both = group_sum<L>(both) * chosen;
+            chosen = group_sum<L>(chosen);
+            both = group_sum<L>(both);
+            far = chosen < kFar;
+            chosen = far ? 0.0f : share_of(chosen);
+            both *= chosen;
         }
 #pragma unroll
         for (int h = 0; h < (int)H; ++h)
@@ -740,6 +776,34 @@ __global__ __launch_bounds__(256, 4) void choose_backward(ChooseGradArgs a) {
             dot = group_sum<L>(dot) * r.part;
 #pragma unroll
             for (int j = 0; j < V; ++j) d[j] = (d[j] - dot) * (s[j] * r.part);
+        }
+        if (far && live && a.dweights) {  // what comes by way of the weights, times the chosen's shares
+            float share[H], mean = 0.0f;
+#pragma unroll
+            for (int h = 0; h < (int)H; ++h) {
+                const uint32_t k = h * L + l;
+                id[h] = k < a.topk ? a.ids[(uint64_t)t * a.topk + k] : -1;
+                if ((uint32_t)id[h] >= a.experts) id[h] = -1;
+                dw[h] = id[h] >= 0 ? a.dweights[(uint64_t)t * a.topk + k] * a.scale : 0.0f;
+            }
+            const float sum = among_chosen<L>(a.logits, t * a.stride, a.dtype, id, sigmoid, share), part = share_of(sum);
+#pragma unroll
+            for (int h = 0; h < (int)H; ++h) {
+                share[h] *= part;
+                mean += share[h] * dw[h];
+            }
+            mean = group_sum<L>(mean);
+#pragma unroll
+            for (int h = 0; h < (int)H; ++h)
+                if (id[h] >= 0) given[place(id[h])] = (dw[h] - mean) * share[h];
+            wave_sees();
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float u = exp_of(-fabsf(x[j])), down = inverse(1.0f + u);
+                d[j] += given[tid * kPitch + j] * (!sigmoid ? 1.0f : x[j] > 0.0f ? u * down : down);
+                given[tid * kPitch + j] = 0.0f;
+            }
+            wave_sees();
         }
         if (!live) {
 #pragma unroll

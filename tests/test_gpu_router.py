@@ -474,6 +474,38 @@ def test_scores_that_saturate(experts, topk):
         assert torch.equal(run(x, router, bias).ids.cpu().long(), want)
 
 
+@pytest.mark.parametrize("gap", [10, 20, 60, 83, 87, 100, 1000])
+@pytest.mark.parametrize("experts,topk", [(3, 2), (40, 8), (130, 1), (300, 12), (1000, 64)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_weights_of_choices_far_below_the_largest_logit(score, experts, topk, gap):
+    """A bias that keeps the largest logits from being chosen: weights over their
+    sum, and their gradient, are those of the chosen ones alone.  Differences
+    between the chosen are below 24 and so is what their exponents are rounded by."""
+    tokens = 9
+    x, g = logits_of(tokens, experts, torch.float32, gap + experts)
+    x -= gap
+    x[4] += gap  # nothing far below in one
+    bias = torch.randn(experts, generator=g) * 0.1
+    top = torch.randperm(experts, generator=g)[:max(1, (experts - topk) // 2)]
+    x[:, top] = 5.0 - torch.rand(tokens, len(top), generator=g)
+    bias[top] = -INF
+    opt = dict(score=score, normalize=True, scale=1.5, balance=0.5)
+    router = zc.Router(tokens, topk, experts, **opt)
+    c = run(x, router, bias)
+    ids, w, counts, _, counted, _ = plain.choose(x.double(), topk, bias=bias, **opt)
+    assert torch.equal(c.ids.cpu().long(), ids)
+    assert ((c.weights.cpu().double() - w).abs() <= w * (24 + 32) * 2.0 ** -23 + 1e-38).all()
+    dw = torch.randn(tokens, topk, generator=g)
+    for dtype in TYPES.values():
+        out = torch.full((tokens, experts), 7.0, dtype=dtype, device="cuda")
+        router.choose_backward(x.to(dtype).cuda(), c, dw.cuda(), None, out)
+        want, size = plain.gradient(x.to(dtype).double(), ids, counts, counted, dw.double(), 1.0, topk, **opt)
+        # shares further than 120 below the largest are below the smallest number
+        tiny = 2.0 ** -24 if dtype == torch.float16 else 1e-37
+        bound = want.abs() * HALF[dtype] + size * (min(spread(x), 120) + 64) * 2.0 ** -23 + tiny
+        assert ((out.cpu().double() - want).abs() <= bound).all()
+
+
 def test_refusals():
     from lossless_bf16_exponent_zc_amd.binding import ZC_ERR_CAPACITY, ZC_ERR_INVALID_ARG, ZC_ERR_UNSUPPORTED
     router = zc.Router(8, 2, 16)
