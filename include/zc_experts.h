@@ -238,11 +238,20 @@ zc_status zc_choose_backward(const void *d_logits, uint64_t stride, uint32_t dty
  * d_x contiguous [batch, n, k] of one of the three row types, d_out the result,
  * bf16, contiguous; where x is of 16 bits they may be the same memory, all of
  * it, and may not overlap otherwise.  Products take fp16 factors into 32-bit
- * sums and X is kept in 22 bits (a pair of fp16): results are off by 2e-4 to
- * 2e-3 of their root mean square, besides their rounding to bf16 of 1.7e-3,
- * whatever the singular values.  That holds where X and A stay in fp16's range,
- * as they do where no singular value passes about 5.  A matrix with a value that
- * is not finite comes out as NaN, the others as they are.
+ * sums; X is kept as a pair of fp16, within 2^-23 of each element.  With the
+ * coefficients 3.4445, -4.7750, 2.0315 (the quintic published with the Muon
+ * optimiser) results are off, relative to their root mean square and besides
+ * their own rounding to bf16 (1.7e-3), by at most
+ *   5e-4 * steps + 2^-22 * 3.4445^steps
+ * (measured up to 2048 x 7168).  The first part is the factors' rounding, after
+ * five steps 5e-5 to 2.4e-3; it is up to ten times that where it does not average
+ * out: in matrices of less than about 4096 elements, or of equal ones.  The
+ * second is what X and the sums are rounded by, which grows by up to 3.4445 a
+ * step in directions of singular values next to nothing, as in any arithmetic of
+ * 32 bits (rank one 2048 x 7168 after 5, 8 and 12 steps: 4e-4, 4e-3, 0.6; with
+ * all in 32 bits 4e-4, 1e-2, 1.4).  All that holds where X and A stay in
+ * fp16's range, as they do where no singular value passes about 5.  A matrix with
+ * a value that is not finite comes out as NaN, the others as they are.
  * Limits: batch 0..65535, n and k 1..65536, steps 1..64.
  * zc_orthogonalize_workspace_bytes is 0 past a limit.
  */

@@ -11,13 +11,15 @@
 //
 // Numbers.  The products run on v_mfma_f32_16x16x32_f16.  Their factors are
 // fp16, 11 bits at bf16's rate: with bf16 factors results are off by 1e-2 of
-// their rms and more.  Y itself is kept as a pair hi + lo of fp16 (22 bits), of
-// which the products read hi: a step multiplies a small singular value by up to
-// a, five of them by 485, and with them what Y was rounded by, while errors of
-// the products' factors stay where A is large.  (Off from 64 bits by, in the
-// root mean square: Gaussian 512 x 1792 1.1e-3, spectrum 1/i^2 2e-4, rank one
-// and rounding noise 2e-4; without lo 1.5e-3, 2e-2, 1e-1.  The result's own
-// rounding to bf16 is 1.7e-3.)  Near the end A and P are nearly diagonal, and
+// their rms and more.  Y itself is kept as a pair of fp16, hi and 2^11 times what
+// hi was rounded by, within 2^-23 of itself; the products read hi.  A step
+// multiplies a small singular value by up to a, five of them by 485, and with
+// them what Y was rounded by, while errors of the products' factors stay where A
+// is large.  (Off from 64 bits by, in the root mean square: Gaussian 512 x 1792
+// 1.1e-3, spectrum 1/i^2 2e-4, rank one and rounding noise 2e-4; without lo
+// 1.5e-3, 2e-2, 1e-1.  Rank one 512 x 512 after 8, 10 and 12 steps 2e-3, 2e-2 and
+// 0.3, with all in 32 bits 5e-3, 6e-2 and 0.7.  The result's own rounding to bf16
+// is 1.7e-3.)  Near the end A and P are nearly diagonal, and
 // what their diagonals were rounded by is the largest error left; it is kept
 // in 32 bits and put back where P and the new Y are made.
 // Y is held times 2^shift, about the square root of its length, so that its
@@ -62,6 +64,18 @@ struct Operand {
     uint32_t stride;   // bytes between rows
     uint32_t rows;     // that exist from there on
 };
+
+// lo is what hi was rounded by, times kLow: at most as large as hi, so that it is
+// not subnormal before hi is, and 11 bits more of Y are kept whatever its size.
+constexpr float kLow = 2048.0f;
+template <typename F, typename H>
+__device__ __forceinline__ F joined(const H& hi, const H& lo) {
+    return __builtin_elementwise_fma(__builtin_convertvector(lo, F), F(1.0f / kLow), __builtin_convertvector(hi, F));
+}
+template <typename H, typename F>
+__device__ __forceinline__ H remainder(const F& v, const H& hi) {
+    return __builtin_convertvector((v - __builtin_convertvector(hi, F)) * kLow, H);
+}
 
 #if defined(__HIP_DEVICE_COMPILE__)
 
@@ -451,12 +465,12 @@ __global__ __launch_bounds__(256, SH::kOnCu) void step_product(OrthArgs p, uint3
                 f16x8 o[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const f32x8 v = results(b, h) + factor * (__builtin_convertvector(now.hi[h], f32x8) + __builtin_convertvector(now.lo[h], f32x8));
+                    const f32x8 v = results(b, h) + factor * joined<f32x8>(now.hi[h], now.lo[h]);
                     if constexpr (KIND == kApply) {
                         const uint64_t e = y_at + (uint64_t)(i + 4 * h) * p.side + j;
                         o[h] = __builtin_convertvector(v, f16x8);
                         *reinterpret_cast<f16x8*>(p.next + e) = o[h];
-                        *reinterpret_cast<f16x8*>(p.lo + e) = __builtin_convertvector(v - __builtin_convertvector(o[h], f32x8), f16x8);
+                        *reinterpret_cast<f16x8*>(p.lo + e) = remainder<f16x8>(v, o[h]);
                     } else {
                         o[h] = __builtin_bit_cast(f16x8, __builtin_convertvector(v * p.inverse, bf16x8));
                     }
@@ -544,9 +558,9 @@ __global__ __launch_bounds__(256) void normalize(OrthArgs p, uint32_t col_tiles)
         for (int q = 0; q < 8; ++q) {
             const float v = tile[a][b * 8 + q], t = tile[b * 8 + q][a];
             straight[q] = (_Float16)v;
-            straight_lo[q] = (_Float16)(v - (float)straight[q]);
+            straight_lo[q] = (_Float16)((v - (float)straight[q]) * kLow);
             over[q] = (_Float16)t;
-            over_lo[q] = (_Float16)(t - (float)over[q]);
+            over_lo[q] = (_Float16)((t - (float)over[q]) * kLow);
         }
         const uint64_t at_s = y_at + (uint64_t)(i0 + a) * along + j0 + b * 8, at_o = y_at + (uint64_t)(j0 + a) * down + i0 + b * 8;
         *reinterpret_cast<f16x8*>((OVER ? p.across : p.next) + at_s) = straight;
@@ -611,7 +625,7 @@ __global__ __launch_bounds__(512) void update_small(OrthArgs p, uint32_t steps) 
         const _Float16 h = (_Float16)y;
         const uint32_t at = OVER ? y_at(col, row) : y_at(row, col);
         *reinterpret_cast<_Float16*>(hi + at) = h;
-        *reinterpret_cast<_Float16*>(lo + at) = (_Float16)(y - (float)h);
+        *reinterpret_cast<_Float16*>(lo + at) = (_Float16)((y - (float)h) * kLow);
     });
     __syncthreads();
 
@@ -697,13 +711,12 @@ __global__ __launch_bounds__(512) void update_small(OrthArgs p, uint32_t steps) 
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const uint32_t j = t * 16 + g * 4, at = y_at(row, j);
-                const f32x4 was = __builtin_convertvector(*reinterpret_cast<const f16x4*>(hi + at), f32x4) +
-                                  __builtin_convertvector(*reinterpret_cast<const f16x4*>(lo + at), f32x4);
+                const f32x4 was = joined<f32x4>(*reinterpret_cast<const f16x4*>(hi + at), *reinterpret_cast<const f16x4*>(lo + at));
                 const f32x4 v = acc[t] + (p.a + *reinterpret_cast<const f32x4*>(rest_p + j)) * was;
                 if (!last) {
                     const f16x4 h = __builtin_convertvector(v, f16x4);
                     *reinterpret_cast<f16x4*>(hi + at) = h;
-                    *reinterpret_cast<f16x4*>(lo + at) = __builtin_convertvector(v - __builtin_convertvector(h, f32x4), f16x4);
+                    *reinterpret_cast<f16x4*>(lo + at) = remainder<f16x4>(v, h);
                 } else {
                     __bf16* out = p.out + (uint64_t)blockIdx.x * size;
 #pragma unroll

@@ -275,6 +275,80 @@ def test_after_the_weight_gradient():
     check(dw, out)
 
 
+def limit(steps):
+    """What include/zc_experts.h has for the default coefficients, relative to
+    the result's root mean square: of matrices of 4096 unlike elements or more."""
+    return 5e-4 * steps + 2.0 ** -22 * MUON[0] ** steps
+
+
+SPECTRA = ["plain", "rows", "few", "one", "rank8", "one16", "zero rows", "steep"]
+
+
+def spectrum(kind, n, k):
+    g = torch.Generator().manual_seed(n + k)
+    if kind in ("plain", "rows", "few", "steep"):
+        return matrices(1, n, k, kind, dtype=torch.float32)
+    if kind == "rank8":
+        x = torch.randn(n, 8, generator=g) @ torch.randn(8, k, generator=g)
+    elif kind == "zero rows":
+        x = torch.randn(n, k, generator=g)
+        x[16:] = 0
+    else:
+        x = torch.randn(n, 1, generator=g) * torch.randn(1, k, generator=g)
+        if kind == "one16":
+            x = x.bfloat16().float()
+    return x[None]
+
+
+@pytest.mark.parametrize("kind", SPECTRA)
+@pytest.mark.parametrize("n,k", [(64, 64), (64, 300), (70, 2000), (300, 200), (512, 512), (512, 1024), (1100, 520)])
+def test_documented_error(n, k, kind):
+    """Against the iteration in 64 bits alone, whatever the roundings were: the
+    documented limit, with the result's own rounding to bf16 of 2^-8 at most."""
+    x = spectrum(kind, n, k).cuda()
+    out = torch.empty(1, n, k, dtype=torch.bfloat16, device="cuda")
+    for steps in (1, 2, 3, 5, 8, 10, 12):
+        zc.orthogonalize(x, out, steps=steps)
+        exact = steps_of(x[0].cpu(), steps, MUON, False)
+        off = float((out[0].cpu().double() - exact).norm() / exact.norm())
+        assert off <= 2.0 ** -8 + limit(steps), (steps, off, limit(steps))
+
+
+@pytest.mark.parametrize("n,k", [(1, 1), (1, 7), (2, 2), (3, 5), (8, 8), (64, 64), (64, 3000), (300, 300), (640, 1280)])
+def test_documented_error_of_like_elements(n, k):
+    """Equal elements, or few: ten times the limit's first part, as roundings
+    of factors that are all alike do not average out."""
+    g = torch.Generator().manual_seed(n + k)
+    for x in (torch.ones(n, k), torch.eye(n, k), torch.randn(n, k, generator=g) * torch.exp(torch.randn(1, k, generator=g))):
+        out = torch.empty(1, n, k, dtype=torch.bfloat16, device="cuda")
+        for steps in (1, 2, 3, 5, 8, 10):
+            zc.orthogonalize(x[None].cuda(), out, steps=steps)
+            exact = steps_of(x, steps, MUON, False)
+            off = float((out[0].cpu().double() - exact).norm() / exact.norm())
+            assert off <= 2.0 ** -8 + 5e-3 * steps + 2.0 ** -22 * MUON[0] ** steps, (steps, off)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -7, 2.0 ** -11, 2.0 ** -13])
+def test_small_elements_of_a_step_keep_their_digits(size):
+    """One element carries the norm, the others lie where a remainder of fp16
+    without a factor would have no digits.  Steps of X <- 0.5 X (b = c = 0) pass
+    X on as it is held: hi + lo, 2^-22 of an element and 2^-36 of the norm,
+    halved with it, which leave the bf16 result the rounding of the exact one or
+    the next (2^-7 of an element between them) in those few that lie so near
+    the border: 2^-13 of all by the same count, 1 in 200 allowed."""
+    n, k = 130, 256
+    g = torch.Generator().manual_seed(5)
+    x = (torch.rand(1, n, k, generator=g) + 1) * size / 16  # Y is held times 16
+    x[0, 0, 0] = 1.0
+    out = torch.empty(1, n, k, dtype=torch.bfloat16, device="cuda")
+    for steps in (1, 2, 4):
+        zc.orthogonalize(x.cuda(), out, steps=steps, coefficients=(0.5, 0.0, 0.0), eps=0.0)
+        want = (x[0].double() / x[0].double().norm() * 0.5 ** steps)
+        got = out[0].cpu()
+        assert ((got.double() - want).abs() <= want * (2.0 ** -8 + 2.0 ** -16) + 2.0 ** -40).all()
+        assert int((got != want.to(torch.bfloat16)).sum()) <= n * k // 200
+
+
 def test_refusals():
     from lossless_bf16_exponent_zc_amd.binding import ZC_ERR_CAPACITY, ZC_ERR_INVALID_ARG, ZC_ERR_UNSUPPORTED
     x = torch.zeros(2, 8, 12, device="cuda")
