@@ -816,11 +816,14 @@ __global__ __launch_bounds__(256, 4) void choose_backward(ChooseGradArgs a) {
     }
 }
 
-// Workgroups of a choice, and of its gradient, at most: what the CUs hold at
-// once, which go on to the next tokens.  65,536 tokens on 256 experts, in us:
+// Workgroups of a choice, and of its gradient: what the CUs hold at once, which go
+// on to the next tokens.  65,536 tokens on 256 experts, in us:
 // choices in 768 / 1024 / 1280 workgroups 33/33/35, with a bias 47/50/52; gradients
-// in 1024 / 4096 27/44.
-constexpr uint32_t kParts = 768, kBackward = 1024;
+// in 1024 / 4096 27/44.  More of them for a choice where a lane would add up more
+// than kInLane tokens' shares, which are summed in 32 bits there and in 64 from
+// workgroup to workgroup; at most kMostParts, which one launch may have (kInLane
+// holds up to 2^29 tokens, more than memory has logits for where it would not).
+constexpr uint32_t kParts = 768, kBackward = 1024, kInLane = 16, kMostParts = 1u << 23;
 
 uint32_t tokens_at_a_time(uint32_t experts) { return experts <= 256 ? 16 : experts <= 512 ? 8 : 4; }
 
@@ -839,7 +842,8 @@ void with_shape(uint32_t experts, F f) {
 uint32_t choose_parts(uint64_t tokens, uint32_t experts) {
     const uint32_t g = tokens_at_a_time(experts);
     const uint64_t n = (tokens + g - 1) / g;
-    return n < 1 ? 1 : n > kParts ? kParts : (uint32_t)n;
+    const uint64_t most = (n + kInLane - 1) / kInLane;
+    return n < 1 ? 1 : n <= kParts ? (uint32_t)n : most <= kParts ? kParts : most < kMostParts ? (uint32_t)most : kMostParts;
 }
 
 zc_status launch_choose(const ChooseArgs& a, hipStream_t stream) {

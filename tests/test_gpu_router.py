@@ -506,6 +506,22 @@ def test_weights_of_choices_far_below_the_largest_logit(score, experts, topk, ga
         assert ((out.cpu().double() - want).abs() <= bound).all()
 
 
+def test_sums_over_millions_of_tokens():
+    """Equal tokens, whose shares 32-bit sums of thousands would all round to one
+    side: a part is 16 tokens a lane at most, whatever their number."""
+    tokens, experts = 1 << 25, 8
+    row = torch.tensor([0.3, -0.7, 0.1, 0.9, -0.2, 0.55, -0.35, 0.0]).bfloat16()
+    x = row.cuda().expand(tokens, experts).contiguous()
+    router = zc.Router(tokens, 1, experts, balance=0.5)
+    c = router.empty_choice()
+    router.choose(x, c, router.empty_workspace())
+    p = torch.softmax(row.double(), 0)
+    assert (c.ids == 3).all() and int(c.counted) == tokens and c.counts.tolist() == [0, 0, 0, tokens, 0, 0, 0, 0]
+    R = spread(row)
+    assert ((c.sums.cpu().double() - p * tokens).abs() <= p * tokens * (R + 48) * 2.0 ** -23).all()
+    assert abs(float(c.loss) - 0.5 * experts * float(p[3])) <= 0.5 * experts * float(p[3]) * (R + 64) * 2.0 ** -23
+
+
 def test_refusals():
     from lossless_bf16_exponent_zc_amd.binding import ZC_ERR_CAPACITY, ZC_ERR_INVALID_ARG, ZC_ERR_UNSUPPORTED
     router = zc.Router(8, 2, 16)
