@@ -849,8 +849,8 @@ zc_status step_matrix(OrthArgs& a, bool two, int& m, hipStream_t stream) {
 }  // namespace
 
 zc_status launch_orthogonalize(OrthArgs a, uint32_t dtype, uint32_t steps, hipStream_t stream) {
-    // more workgroups than a launch may have, with the smallest tiles
-    if (!fits((uint64_t)a.batch * (a.length / 64) * (a.side / 64))) return ZC_ERR_UNSUPPORTED;
+    // more workgroups than a launch may have, with the smallest tiles, in eights
+    if (!fits(((uint64_t)a.batch * (a.length / 64) * (a.side / 64) + 7) / 8 * 8)) return ZC_ERR_UNSUPPORTED;
     const bool over = a.n < a.k;
     if (a.side == 64 && a.length <= kSmallLength) {
         auto small = [&](auto t) {

@@ -94,3 +94,13 @@ def test_updates_in_place_are_of_16_bits(L):
     for dtype, out in ((2, P), (2, P + size * 4 - 2), (0, P + 2), (1, P + size * 2 - 2), (0, P - size * 2 + 2), (2, P - 2)):
         args = [P, dtype, 2, 8, 12, 5, 3.0, -4.0, 2.0, 0.0, out, P + (1 << 20), need, None]
         assert rc(L.zc_orthogonalize, args, 1, dtype) == BAD, (dtype, out)
+
+
+def test_a_product_of_almost_too_many_tiles_is_refused(L):
+    """Workgroups are launched in eights: 61,455 matrices of 273 tiles of 64 are
+    2^24 - 1, one more than the last multiple of eight that a launch may have."""
+    batch, n = 61455, 273 * 64
+    need = zc.orthogonalize_workspace_bytes(batch, n, 1)
+    far = 1 << 45  # addresses that do not overlap and are never followed
+    assert batch * 273 == 2**24 - 1
+    assert L.zc_orthogonalize(P, 0, batch, n, 1, 5, 3.0, -4.0, 2.0, 0.0, far, 2 * far, need, None) == UNSUP
