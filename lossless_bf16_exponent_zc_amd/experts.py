@@ -357,8 +357,12 @@ def orthogonalize(x, out, ws=None, steps: int = 5, coefficients=(3.4445, -4.7750
     that of singular values next to nothing.  ws: a workspace of
     orthogonalize_workspace_bytes; without one it is taken from torch's
     allocator, on the call's stream."""
+    try:
+        coefficients = tuple(coefficients)
+    except TypeError:
+        _bad("coefficients", f"three numbers expected, not {coefficients!r}")
     if ws is None and stream is not None:
         with torch.cuda.stream(stream):
-            _zc.orthogonalize(x, out, None, steps, tuple(coefficients), eps, None)
+            _zc.orthogonalize(x, out, None, steps, coefficients, eps, None)
     else:
-        _zc.orthogonalize(x, out, ws, steps, tuple(coefficients), eps, stream)
+        _zc.orthogonalize(x, out, ws, steps, coefficients, eps, stream)

@@ -104,3 +104,11 @@ def test_a_product_of_almost_too_many_tiles_is_refused(L):
     far = 1 << 45  # addresses that do not overlap and are never followed
     assert batch * 273 == 2**24 - 1
     assert L.zc_orthogonalize(P, 0, batch, n, 1, 5, 3.0, -4.0, 2.0, 0.0, far, 2 * far, need, None) == UNSUP
+
+
+@pytest.mark.parametrize("coefficients", [3.0, None])
+def test_coefficients_that_are_not_three_numbers_are_refused(coefficients):
+    x = torch.zeros(1, 2, 3)
+    with pytest.raises(zc.ZcError, match="coefficients") as e:
+        zc.orthogonalize(x, x.bfloat16(), coefficients=coefficients)
+    assert e.value.code == BAD
