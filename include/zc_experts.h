@@ -244,7 +244,7 @@ zc_status zc_choose_backward(const void *d_logits, uint64_t stride, uint32_t dty
  * their own rounding to bf16 (1.7e-3), by at most
  *   5e-4 * steps + 2^-22 * 3.4445^steps
  * (measured up to 2048 x 7168).  The first part is the factors' rounding, after
- * five steps 5e-5 to 2.4e-3; it is up to ten times that where it does not average
+ * five steps 5e-5 to 1.5e-3; it is up to ten times that where it does not average
  * out: in matrices of less than about 4096 elements, or of equal ones.  The
  * second is what X and the sums are rounded by, which grows by up to 3.4445 a
  * step in directions of singular values next to nothing, as in any arithmetic of

@@ -55,7 +55,7 @@ OrthLayout orth_layout(uint32_t batch, uint32_t n, uint32_t k) {
     l.lo = take(y);
     l.across = take(y);
     for (uint64_t& at_square : l.square) at_square = take(s);
-    for (uint64_t& at_rest : l.rest) at_rest = take(l.side * batch * 4);
+    for (uint64_t& at_rest : l.rest) at_rest = take(2 * l.side * batch * 4);
     l.bytes = at;
     return l;
 }

@@ -150,13 +150,14 @@ struct OrthArgs {
     _Float16* lo;            // [batch][length][side]
     _Float16* across;        // [batch][side][length], the present hi turned over
     _Float16* square[3];     // [batch][side][side] each
-    float* rest[3];          // [batch][side] each, what their diagonals were rounded by
+    float* rest[3];          // [batch][2][side] each, what their diagonals were rounded by, and to
     // of one product: the matrices read and made
     const _Float16 *matrix, *other;
     const float *rest_m, *rest_n;
     _Float16* made;
     float* rest_made;
     float gamma, alpha, beta, factor;
+    float low;               // what lo's products with the diagonal count
 };
 
 // How a weight gradient is cut: tiles of side x side, each segment summed in up

@@ -15,13 +15,13 @@
 // hi was rounded by, within 2^-23 of itself; the products read hi.  A step
 // multiplies a small singular value by up to a, five of them by 485, and with
 // them what Y was rounded by, while errors of the products' factors stay where A
-// is large.  (Off from 64 bits by, in the root mean square: Gaussian 512 x 1792
-// 1.1e-3, spectrum 1/i^2 2e-4, rank one and rounding noise 2e-4; without lo
-// 1.5e-3, 2e-2, 1e-1.  Rank one 512 x 512 after 8, 10 and 12 steps 2e-3, 2e-2 and
-// 0.3, with all in 32 bits 5e-3, 6e-2 and 0.7.  The result's own rounding to bf16
-// is 1.7e-3.)  Near the end A and P are nearly diagonal, and
-// what their diagonals were rounded by is the largest error left; it is kept
-// in 32 bits and put back where P and the new Y are made.
+// is large.  Near the end A and P are nearly diagonal, and what their diagonals
+// were rounded by is kept in 32 bits and put back where P and the new Y are made,
+// as is the diagonal's product with lo in the last two steps.  (Off from 64 bits
+// by, in the root mean square: Gaussian 512 x 1792 6e-4, spectrum 1/i^2 and rank
+// one in bf16 2e-4; without lo 1.4e-3, 2e-2, 1e-1.  Rank one 512 x 512 after 8, 10
+// and 12 steps 2e-3, 2e-2 and 0.3, with all in 32 bits 5e-3, 6e-2 and 0.7.  The
+// result's own rounding to bf16 is 1.7e-3.)
 // Y is held times 2^shift, about the square root of its length, so that its
 // elements lie in fp16's normal range.
 #include "zc_experts_kernels.h"
@@ -68,14 +68,29 @@ struct Operand {
 // lo is what hi was rounded by, times kLow: at most as large as hi, so that it is
 // not subnormal before hi is, and 11 bits more of Y are kept whatever its size.
 constexpr float kLow = 2048.0f;
-template <typename F, typename H>
-__device__ __forceinline__ F joined(const H& hi, const H& lo) {
-    return __builtin_elementwise_fma(__builtin_convertvector(lo, F), F(1.0f / kLow), __builtin_convertvector(hi, F));
-}
 template <typename H, typename F>
 __device__ __forceinline__ H remainder(const F& v, const H& hi) {
     return __builtin_convertvector((v - __builtin_convertvector(hi, F)) * kLow, H);
 }
+
+// New Y: product + factor (hi + lo) + low lo.
+template <typename F, typename H>
+__device__ __forceinline__ F stepped(const F& product, const F& factor, const F& low, const H& hi, const H& lo) {
+    const F h = __builtin_convertvector(hi, F), l = __builtin_convertvector(lo, F);
+    const F whole = __builtin_elementwise_fma(l, F(1.0f / kLow), h);
+    return __builtin_elementwise_fma(factor, whole, __builtin_elementwise_fma(low, l, product));
+}
+
+// The products read hi alone.  Where P is nearly diagonal, as it is in the end,
+// what lo is missed by most is the diagonal's product with it, which Y + Y P
+// adds by itself: the products of the last two steps, `done` of all being done
+// then.  Not before: where singular values are next to nothing it would be noise
+// in their directions (the rest of P takes it away again), and what grows by a in
+// every step after.  Off by, after five steps, without / in the last / in the
+// last two / in all: Gaussian 512 x 512 1.2e-3 / 1.0e-3 / 0.8e-3 / 0.7e-3, 512 x
+// 1024 1.6e-3 / 1.5e-3 / 0.5e-3 / 0.5e-3, rank one 64 x 64 7e-4 / 7e-4 / 7e-4 /
+// 6e-3.
+__host__ __device__ constexpr float low_of(uint32_t done, uint32_t steps) { return done + 1 >= steps ? 1.0f / kLow : 0.0f; }
 
 #if defined(__HIP_DEVICE_COMPILE__)
 
@@ -352,10 +367,10 @@ __global__ __launch_bounds__(256, SH::kOnCu) void step_product(OrthArgs p, uint3
     constexpr int kBlocks = T * T / 4, kAhead = kBlocks < 2 ? kBlocks : 2;  // loads run ahead by so many
     // side and length are multiples of 64: a block is there or not as a whole
     auto there = [&](int b) { return wi + b / (T / 2) * 32 < end_i && wj + b % (T / 2) * 32 < p.side; };
-    const float *rest_m = p.rest_m + (uint64_t)matrix * p.side, *rest_n = p.rest_n + (uint64_t)matrix * p.side;
+    const float *rest_m = p.rest_m + (uint64_t)matrix * 2 * p.side, *rest_n = p.rest_n + (uint64_t)matrix * 2 * p.side;
     if constexpr (SYMMETRIC) {
         _Float16* out = p.made + s_at;
-        float* left_over = p.rest_made + (uint64_t)matrix * p.side;
+        float* left_over = p.rest_made + (uint64_t)matrix * 2 * p.side;
         struct Was {
             f16x8 m[2], n[2];
         };
@@ -429,7 +444,10 @@ __global__ __launch_bounds__(256, SH::kOnCu) void step_product(OrthArgs p, uint3
                         const _Float16 o = (_Float16)e;
                         if (j + q <= row) out[(uint64_t)row * p.side + j + q] = o;
                         if (j + q < row) out[(uint64_t)(j + q) * p.side + row] = o;
-                        if (j + q == row) left_over[row] = e - (float)o;
+                        if (j + q == row) {
+                            left_over[row] = e - (float)o;
+                            left_over[p.side + row] = (float)o;
+                        }
                     }
                 }
             }
@@ -437,10 +455,13 @@ __global__ __launch_bounds__(256, SH::kOnCu) void step_product(OrthArgs p, uint3
     } else {
         struct Was {
             f16x8 hi[2], lo[2];
+            f32x8 rest, diagonal;
         };
         auto fetch = [&](int b) {
             const uint32_t i = ri + b / (T / 2) * 32, j = rj + b % (T / 2) * 32;
             Was w;
+            w.rest = *reinterpret_cast<const f32x8*>(rest_m + j);
+            w.diagonal = *reinterpret_cast<const f32x8*>(rest_m + p.side + j);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint64_t e = y_at + (uint64_t)(i + 4 * h) * p.side + j;
@@ -461,11 +482,11 @@ __global__ __launch_bounds__(256, SH::kOnCu) void step_product(OrthArgs p, uint3
                 if (b + kAhead < kBlocks && (WHOLE || there(b + kAhead))) was[b % kAhead] = fetch(b + kAhead);
                 if (!WHOLE && !there(b)) continue;
                 const uint32_t i = ri + b / (T / 2) * 32, j = rj + b % (T / 2) * 32;
-                const f32x8 factor = p.factor + *reinterpret_cast<const f32x8*>(rest_m + j);
+                const f32x8 factor = p.factor + now.rest, low = p.low * now.diagonal;
                 f16x8 o[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const f32x8 v = results(b, h) + factor * joined<f32x8>(now.hi[h], now.lo[h]);
+                    const f32x8 v = stepped(results(b, h), factor, low, now.hi[h], now.lo[h]);
                     if constexpr (KIND == kApply) {
                         const uint64_t e = y_at + (uint64_t)(i + 4 * h) * p.side + j;
                         o[h] = __builtin_convertvector(v, f16x8);
@@ -575,7 +596,7 @@ __global__ __launch_bounds__(256) void normalize(OrthArgs p, uint32_t col_tiles)
 // less than the launches that go between them (1 x 64 x 256: 71 us in 17
 // launches).  Sums, factors and roundings are those of the tiled products.
 constexpr uint32_t kSmallLength = 512;
-constexpr uint32_t small_lds(uint32_t length) { return 2 * length * 128 + 2 * 8192 + 2 * 256; }
+constexpr uint32_t small_lds(uint32_t length) { return 2 * length * 128 + 2 * 8192 + 3 * 256; }
 
 template <typename T, bool OVER>
 __global__ __launch_bounds__(512) void update_small(OrthArgs p, uint32_t steps) {
@@ -587,7 +608,7 @@ __global__ __launch_bounds__(512) void update_small(OrthArgs p, uint32_t steps) 
     const uint32_t tid = threadIdx.x, lane = __lane_id(), wave = uniform(tid >> 6), r = lane & 15, g = lane >> 4;
     const uint32_t L = p.length;
     uint8_t *const hi = lds, *const lo = lds + L * 128, *const A = lds + 2 * L * 128, *const P = A + 8192;
-    float *const rest_a = reinterpret_cast<float*>(P + 8192), *const rest_p = rest_a + 64;
+    float *const rest_a = reinterpret_cast<float*>(P + 8192), *const rest_p = rest_a + 64, *const diagonal = rest_p + 64;
     // rows of 64 fp16, their 16-byte pieces turned: Y's in pairs, so that reads
     // along rows and across them find different banks
     auto y_at = [](uint32_t row, uint32_t col) {
@@ -675,7 +696,7 @@ __global__ __launch_bounds__(512) void update_small(OrthArgs p, uint32_t steps) 
             for (int t = 0; t < 2; ++t)
                 acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(along(A, m_at((tj0 + t) * 16 + r, c0 + 8 * g)), left, acc[t], 0, 0, 0);
         }
-        const float rest_i = rest_a[i];
+        const float rest_i = rest_a[i], low = low_of(step + 1, steps);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const uint32_t j = (tj0 + t) * 16 + g * 4;
@@ -688,7 +709,10 @@ __global__ __launch_bounds__(512) void update_small(OrthArgs p, uint32_t steps) 
             *reinterpret_cast<f16x4*>(P + m_at(i, j)) = h;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                if (i == j + q) rest_p[i] = v[q] - (float)h[q];
+                if (i == j + q) {
+                    rest_p[i] = v[q] - (float)h[q];
+                    diagonal[i] = low * (float)h[q];
+                }
         }
         __syncthreads();
         const bool last = step + 1 == steps;
@@ -711,8 +735,8 @@ __global__ __launch_bounds__(512) void update_small(OrthArgs p, uint32_t steps) 
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const uint32_t j = t * 16 + g * 4, at = y_at(row, j);
-                const f32x4 was = joined<f32x4>(*reinterpret_cast<const f16x4*>(hi + at), *reinterpret_cast<const f16x4*>(lo + at));
-                const f32x4 v = acc[t] + (p.a + *reinterpret_cast<const f32x4*>(rest_p + j)) * was;
+                const f32x4 v = stepped(acc[t], p.a + *reinterpret_cast<const f32x4*>(rest_p + j), *reinterpret_cast<const f32x4*>(diagonal + j),
+                                        *reinterpret_cast<const f16x4*>(hi + at), *reinterpret_cast<const f16x4*>(lo + at));
                 if (!last) {
                     const f16x4 h = __builtin_convertvector(v, f16x4);
                     *reinterpret_cast<f16x4*>(hi + at) = h;
@@ -873,6 +897,7 @@ zc_status launch_orthogonalize(OrthArgs a, uint32_t dtype, uint32_t steps, hipSt
         a.matrix = a.square[m];
         a.rest_m = a.rest[m];
         s += two ? 2 : 1;
+        a.low = low_of(s, steps);
         if (s == steps) return over ? product_of<kLast, true>(a, stream) : product_of<kLast>(a, stream);
         if (zc_status e = product_of<kApply>(a, stream)) return e;
         std::swap(from, to);
