@@ -522,6 +522,28 @@ def test_sums_over_millions_of_tokens():
     assert abs(float(c.loss) - 0.5 * experts * float(p[3])) <= 0.5 * experts * float(p[3]) * (R + 64) * 2.0 ** -23
 
 
+@pytest.mark.parametrize("score,biased", [("softmax", False), ("sigmoid", True)])
+def test_more_workgroups_than_the_cus_hold(score, biased):
+    """Tokens past 16 of 4 at a time in 768 workgroups, some masked."""
+    tokens, topk, experts = 50_001, 3, 520
+    x, g = logits_of(tokens, experts, torch.float32, 21)
+    mask = torch.rand(tokens, generator=g) < 0.8
+    bias = torch.randn(experts, generator=g) * 0.1 if biased else None
+    router = zc.Router(tokens, topk, experts, score=score, normalize=True, balance=0.1)
+    assert router.workspace_bytes > 768 * experts * 8 + 768 * 4 + 1280
+    c = run(x, router, bias, mask)
+    s = plain.scores(x.double(), score)
+    key = x.double() if bias is None else s + bias.double()
+    ids = torch.where(mask[:, None], torch.sort(key, dim=1, descending=True, stable=True).indices[:, :topk], -1)
+    counts = torch.bincount(ids[ids >= 0], minlength=experts)
+    sums = plain.shares(s)[mask].sum(0)
+    assert torch.equal(c.ids.cpu().long(), ids) and torch.equal(c.counts.cpu().long(), counts)
+    assert int(c.counted) == int(mask.sum())
+    assert ((c.sums.cpu().double() - sums).abs() <= sums * (spread(x) + 48) * 2.0 ** -23).all()
+    loss = float(plain.loss_of(counts, sums, int(mask.sum()), topk, 0.1))
+    assert abs(float(c.loss) - loss) <= loss * (spread(x) + 64) * 2.0 ** -23
+
+
 def test_refusals():
     from lossless_bf16_exponent_zc_amd.binding import ZC_ERR_CAPACITY, ZC_ERR_INVALID_ARG, ZC_ERR_UNSUPPORTED
     router = zc.Router(8, 2, 16)
