@@ -5,8 +5,10 @@ behind the C ABI in include/zc.h; ``Plan`` is the thin ctypes binding.
 ``workloads`` draws the seeded synthetic inputs.
 
 Around a MoE's compressed all-to-all (include/zc_experts.h): ``Router`` chooses
-each token's experts and takes the loss that balances them, ``ExpertPlan`` sorts tokens by expert and brings them back, ``expert_product`` and
-``expert_weight_grad`` are the experts' products of 8-bit blocks, ``orthogonalize`` makes updates of their weights.
+each token's experts and takes the loss that balances them, ``ExpertPlan`` sorts
+tokens by expert and brings them back, ``expert_product`` and
+``expert_weight_grad`` are the experts' products of 8-bit blocks,
+``orthogonalize`` makes updates of their weights.
 """
 from .binding import (EXPORTS, LIB_PATH, Plan, ZcError, check_buffer, lib, prefer_compressed,
                       reduce_native)

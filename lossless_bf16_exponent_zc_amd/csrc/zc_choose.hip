@@ -8,12 +8,12 @@
 // steps between lanes, which a wave waits for, at four for up to 256 experts.
 //
 // The choice is bound by instructions, not by memory: 65,536 tokens on 256
-// experts, topk 8, take 33 us (47 with a bias), of which the logits are 7 (bf16)
+// experts, topk 8, take 33 us (49 with a bias), of which the logits are 7 (bf16)
 // to 14 (32 bits), about 250 vector instructions a token: a third of them the
-// sorted keys, a third the joins of 16 lanes' best.  Its gradient takes 27 us
-// (bf16) to 37 (32 bits), 67 to 134 MB at 2.5 to 3.6 TB/s.  Few tokens are bound
-// by their chain of round trips: 8 tokens 4.6 us (7.0 with a bias), gradient
-// 5.3; 8192 tokens 13 (19) and 10.
+// sorted keys, a third the joins of 16 lanes' best.  Its gradient takes 25 us
+// (bf16; of sigmoids 28) to 36 (32 bits), 67 to 134 MB at 2.6 to 3.8 TB/s.  Few
+// tokens are bound by their chain of round trips: 8 tokens 4.7 us (7.1 with a
+// bias), gradient 5.3; 8192 tokens 12 to 13 (18) and 10 to 11.
 #include "zc_experts_kernels.h"
 
 #include <type_traits>
@@ -313,8 +313,9 @@ __device__ __forceinline__ void best_of_group(double (&best)[D]) {
 
 // Scores with a bias, compared in 64 bits one choice after the other: the way
 // for the few tokens whose scores 32 bits do not tell apart and that
-// in_exact_order does not take: a wave that gets here ends some 8 us later.  The exponentials go four by four, by way of LDS
-// (a lane's values 256 apart): all side by side they would take all registers.
+// in_exact_order does not take: a wave that gets here ends some 8 us later.  The
+// exponentials go four by four, by way of LDS (a lane's values 256 apart): all
+// side by side they would take all registers.
 template <int L, int V>
 __device__ __forceinline__ void choose_exactly(const ChooseArgs& a, uint64_t at, uint32_t e0, uint32_t l, double* keys,
                                                int32_t (&ids)[64 / L]) {
@@ -818,8 +819,8 @@ __global__ __launch_bounds__(256, 4) void choose_backward(ChooseGradArgs a) {
 
 // Workgroups of a choice, and of its gradient: what the CUs hold at once, which go
 // on to the next tokens.  65,536 tokens on 256 experts, in us:
-// choices in 768 / 1024 / 1280 workgroups 33/33/35, with a bias 47/50/52; gradients
-// in 1024 / 4096 27/44.  More of them for a choice where a lane would add up more
+// choices in 768 / 1024 / 1280 workgroups 33/31/33, with a bias 49/51/53; gradients
+// in 1024 / 2048 / 4096 25/32/42.  More of them for a choice where a lane would add up more
 // than kInLane tokens' shares, which are summed in 32 bits there and in 64 from
 // workgroup to workgroup; at most kMostParts, which one launch may have (kInLane
 // holds up to 2^29 tokens, more than memory has logits for where it would not).

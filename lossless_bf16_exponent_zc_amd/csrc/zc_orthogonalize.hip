@@ -18,8 +18,8 @@
 // is large.  Near the end A and P are nearly diagonal, and what their diagonals
 // were rounded by is kept in 32 bits and put back where P and the new Y are made,
 // as is the diagonal's product with lo in the last two steps.  (Off from 64 bits
-// by, in the root mean square: Gaussian 512 x 1792 6e-4, spectrum 1/i^2 and rank
-// one in bf16 2e-4; without lo 1.4e-3, 2e-2, 1e-1.  Rank one 512 x 512 after 8, 10
+// by, in the root mean square, steps one by one: Gaussian 512 x 1792 6e-4,
+// spectrum 1/i^2 and rank one in bf16 2e-4; without lo 1.4e-3, 2e-2, 1e-1.  Rank one 512 x 512 after 8, 10
 // and 12 steps 2e-3, 2e-2 and 0.3, with all in 32 bits 5e-3, 6e-2 and 0.7.  The
 // result's own rounding to bf16 is 1.7e-3.)
 // Y is held times 2^shift, about the square root of its length, so that its
@@ -321,10 +321,10 @@ __device__ __forceinline__ Place banded(uint32_t index, uint32_t rows, uint32_t 
 #endif  // __HIP_DEVICE_COMPILE__
 
 // One product of a step, one tile a workgroup.  Long sums are bound by the matrix
-// unit (Y P of 1 x 14336 x 4096 510 us, 0.94 PFLOP/s); short ones by what a tile
+// unit (Y P of 1 x 14336 x 4096 500 us, 0.96 PFLOP/s); short ones by what a tile
 // reads and writes beside its sum, which nothing overlaps on a CU that holds one
-// tile: Y P of 32 x 7168 x 2048 2.69 ms, 0.72 PFLOP/s and 3.1 TB/s, as the result
-// (bf16 alone) 2.09.  OVER: the result leaves turned over (kLast).
+// tile: Y P of 32 x 7168 x 2048 2.42 ms, 0.80 PFLOP/s and 3.4 TB/s, as the result
+// (bf16 alone) 1.92.  OVER: the result leaves turned over (kLast).
 template <typename SH, int KIND, bool OVER>
 __global__ __launch_bounds__(256, SH::kOnCu) void step_product(OrthArgs p, uint32_t tiles, uint32_t side_tiles) {
     extern __shared__ __align__(16) uint8_t lds[];
