@@ -818,12 +818,13 @@ __global__ __launch_bounds__(256, 4) void choose_backward(ChooseGradArgs a) {
 }
 
 // Workgroups of a choice, and of its gradient: what the CUs hold at once, which go
-// on to the next tokens.  65,536 tokens on 256 experts, in us:
-// choices in 768 / 1024 / 1280 workgroups 33/31/33, with a bias 49/51/53; gradients
-// in 1024 / 2048 / 4096 25/32/42.  More of them for a choice where a lane would add up more
-// than kInLane tokens' shares, which are summed in 32 bits there and in 64 from
-// workgroup to workgroup; at most kMostParts, which one launch may have (kInLane
-// holds up to 2^29 tokens, more than memory has logits for where it would not).
+// on to the next tokens.  65,536 tokens on 256 experts, in us: choices in 768 / 1024
+// / 1280 workgroups 33/31/33, with a bias 49/51/53 (8192 tokens on 1024 experts with
+// a bias 35/42/42); gradients in 1024 / 2048 / 4096 25/32/42.  More of them for a
+// choice where a lane would add up more than kInLane tokens' shares, which are
+// summed in 32 bits there and in 64 from workgroup to workgroup; at most
+// kMostParts, which one launch may have (up to 2^29 tokens with kInLane a lane:
+// past that they would have more logits than memory holds).
 constexpr uint32_t kParts = 768, kBackward = 1024, kInLane = 16, kMostParts = 1u << 23;
 
 uint32_t tokens_at_a_time(uint32_t experts) { return experts <= 256 ? 16 : experts <= 512 ? 8 : 4; }
